@@ -8,7 +8,9 @@ is missing or no GPU is present, the calls raise.
 
 The entry points keep the C names without the ``sgc_`` prefix:
 ``compress``, ``binarize``, ``encode``, ``decode_accumulate``, plus the
-``Layout`` of segment sizes shared by both ends of the exchange.
+``Layout`` of segment sizes shared by both ends of the exchange.  The
+operators at the loss end of a language model (``layer_norm``,
+``token_logprobs``, ``distill`` and their backward calls) are in ``lm``.
 """
 from __future__ import annotations
 
@@ -44,6 +46,9 @@ EXPORTED = (
     "sgc_binarize_workspace", "sgc_binarize",
     "sgc_encode_word_bound", "sgc_encode_chunk_bound", "sgc_encode_workspace", "sgc_encode",
     "sgc_decode_accumulate_workspace", "sgc_decode_accumulate", "sgc_set_pass_events",
+    "sgc_layer_norm", "sgc_layer_norm_backward_workspace", "sgc_layer_norm_backward",
+    "sgc_token_logprobs_workspace", "sgc_token_logprobs", "sgc_token_logprobs_backward",
+    "sgc_distill_workspace", "sgc_distill", "sgc_distill_backward",
 )
 
 
@@ -125,6 +130,7 @@ def lib():
         L.sgc_decode_accumulate.restype = C.c_int
         L.sgc_set_pass_events.argtypes = [P, P]
         L.sgc_set_pass_events.restype = C.c_int
+        lm._declare(L)
         _lib = L
     return _lib
 
@@ -596,3 +602,11 @@ def set_pass_events(start: Optional["torch.cuda.Event"], stop: Optional["torch.c
     else:
         _check(lib().sgc_set_pass_events(C.c_void_p(start.cuda_event), C.c_void_p(stop.cuda_event)),
                "sgc_set_pass_events")
+
+
+from . import lm  # noqa: E402  (uses the helpers above)
+from .lm import (  # noqa: E402,F401
+    BF16, DISTILL_RENORM, DISTILL_TAIL, F16, F32, NORM_ADD_GRADS, TOKEN_I32, TOKEN_I64, TOP_MAX, Distilled,
+    NormGrads, Normalized, TokenLogprobs, distill, distill_backward, distill_workspace_bytes, layer_norm,
+    layer_norm_backward, layer_norm_backward_workspace_bytes, token_logprobs, token_logprobs_backward,
+    token_logprobs_workspace_bytes)

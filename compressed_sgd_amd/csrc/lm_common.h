@@ -1,0 +1,110 @@
+// lm_common.h -- internals shared by the language-model operators
+// (layer_norm.hip, token_logprobs.hip, distill.hip).
+#pragma once
+
+#include <cmath>
+
+#include "sgc_common.h"
+
+namespace sgc {
+
+inline bool lm_dtype(int32_t t) { return t == SGC_F32 || t == SGC_BF16 || t == SGC_F16; }
+inline int64_t lm_size(int32_t t) { return t == SGC_F32 ? 4 : 2; }
+inline bool lm_aligned(const void* p, int64_t a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
+
+// rows x len elements at `stride`: an input may repeat one row (stride 0),
+// an output's rows lie apart.
+inline bool lm_rows_ok(const void* p, int64_t stride, int64_t rows, int64_t len, int32_t dtype, bool out)
+{
+    if (!p || !lm_aligned(p, lm_size(dtype)) || stride < 0) return false;
+    return rows <= 1 || stride >= len || (!out && stride == 0);
+}
+
+// ------------------------------------------------------------ element types
+typedef __bf16 bf16_t;
+typedef _Float16 f16_t;
+
+// V consecutive elements, loaded and stored in one access at the element's
+// own alignment: rows of an odd length start at any element, and the
+// hardware takes a 16-byte access at any 2-byte address.
+template <typename T, int V>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack {
+    T v[V];
+};
+
+template <typename T>
+__device__ inline float to_f(T x) { return (float)x; }
+// one rounding, to nearest even
+template <typename T>
+__device__ inline T from_f(float x) { return (T)x; }
+
+template <typename T>
+struct VecLen {
+    static constexpr int value = 16 / (int)sizeof(T);
+};
+
+// One workgroup for each of n < 2^31 rows: a grid of at most 2^20 x 2^11
+// (a launch holds fewer than 2^32 threads in x); the last ones past n.
+inline dim3 row_grid(int64_t n)
+{
+    const int64_t gx = n < ((int64_t)1 << 20) ? n : (int64_t)1 << 20;
+    return dim3((unsigned)gx, (unsigned)cdiv(n, gx));
+}
+__device__ inline int64_t row_of_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+// ------------------------------------------------------- block reductions
+__device__ inline float wave_sum(float x)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+__device__ inline float wave_max(float x)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+    return x;
+}
+
+// Sum over a workgroup of NW waves, the same value in every thread; tmp
+// holds NW floats and is free again after the call.
+template <int NW>
+__device__ inline float block_sum(float x, float* tmp)
+{
+    x = wave_sum(x);
+    if (NW == 1) return x;
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float r = tmp[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) r += tmp[w];
+    __syncthreads();
+    return r;
+}
+template <int NW>
+__device__ inline float block_max(float x, float* tmp)
+{
+    x = wave_max(x);
+    if (NW == 1) return x;
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float r = tmp[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) r = fmaxf(r, tmp[w]);
+    __syncthreads();
+    return r;
+}
+
+// Order of values as unsigned integers: -inf lowest, both zeros alike, NaN
+// (either sign) above +inf.
+__device__ inline uint32_t order_key(float x)
+{
+    if (x != x) return 0xffffffffu;
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+// The same with the place as second key: among equals the lower one is
+// larger.  Unique within a row.
+__device__ inline uint64_t order_key(float x, uint32_t at) { return ((uint64_t)order_key(x) << 32) | (uint32_t)~at; }
+
+}  // namespace sgc

@@ -353,6 +353,144 @@ int sgc_decode_accumulate(const sgc_layout* layout, const sgc_message* msgs, int
                           uint32_t* dstatus, void* ws, size_t ws_bytes, sgc_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The loss end of a language model: the operators around the place where
+ * the gradients that the calls above exchange come from.  Rows are
+ * independent; `rows` may be 0 (nothing is read, nothing but the sums over
+ * the rows is written).  Strides are in elements from row to row, the
+ * elements of a row are contiguous and need only their type's alignment.  An
+ * input's stride may be 0 (one row for all); an output's is at least the
+ * row's length.  Arithmetic is fp32, rounded once to the output's type.   */
+#define SGC_F32 0
+#define SGC_BF16 1
+#define SGC_F16 2
+
+/* Layer norm over the last dimension.
+ *   mean = sum(x) / cols;  rstd = (sum((x - mean)^2) / cols + eps)^(-1/2)
+ *   y = (x - mean) * rstd * weight + bias
+ * and backward, with xh = (x - mean) * rstd and v = dy * weight:
+ *   dx = rstd * (v - mean(v) - xh * mean(v * xh))
+ *   dweight = sum over the rows of dy * xh;  dbias = of dy
+ * The sums over the rows are fp32 in a fixed order and go to fp32 buffers of
+ * any 4-byte alignment: segments of a flat gradient, as sgc_compress reads
+ * it.  SGC_NORM_ADD_GRADS adds them to what the buffers hold (several
+ * micro-batches).  weight, bias (NULL: 1 and 0) are wdtype: SGC_F32, or the
+ * type of x.  mean, rstd [rows fp32] may be NULL in the forward call.  dx,
+ * dweight and dbias may each be NULL: not wanted.  y may be x, and dx may
+ * be dy or x, at the same address and stride; no other overlap.
+ * 1 <= cols <= 2^20.  sgc_layer_norm_backward_workspace: 0 on bad options. */
+#define SGC_NORM_ADD_GRADS 1
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int32_t dtype;  /* x, y, dy, dx: SGC_F32 | SGC_BF16 | SGC_F16 */
+    int32_t wdtype; /* weight, bias: SGC_F32, or dtype */
+    float eps;      /* finite, >= 0 */
+    int32_t flags;  /* backward: 0 | SGC_NORM_ADD_GRADS */
+} sgc_norm_opts;
+
+int sgc_layer_norm(const sgc_norm_opts* opt, const void* x, int64_t x_stride, const void* weight, const void* bias,
+                   void* y, int64_t y_stride, float* mean, float* rstd, sgc_stream_t stream);
+size_t sgc_layer_norm_backward_workspace(const sgc_norm_opts* opt);
+int sgc_layer_norm_backward(const sgc_norm_opts* opt, const void* dy, int64_t dy_stride, const void* x,
+                            int64_t x_stride, const void* weight, const float* mean, const float* rstd, void* dx,
+                            int64_t dx_stride, float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                            sgc_stream_t stream);
+
+/* Log probabilities of given tokens, entropy and top alternatives.  With
+ * y_i = scale * (z_i - m), m = max(z), s = sum(exp(y)):
+ *   log p_i = y_i - ln(s);  logp = log p of the row's token;
+ *   entropy = -sum(p * log p), a term with p = 0 counting 0;
+ *   top_idx, top_logp [rows, top]: the tokens of largest z, best first, the
+ *   lower token first among equals, and their log p.
+ * stats [rows, 2] = {m, s}: what the backward call needs.
+ * tokens [rows] int32 (SGC_TOKEN_I32) or int64 (SGC_TOKEN_I64); a negative
+ * token is none: logp 0.  A token >= vocab: logp NaN and, where dstatus is
+ * given, SGC_STATUS_BAD_INPUT.  Logits may be -inf (p = 0).  A row of -inf
+ * alone has no probabilities: logp and top_logp -inf, entropy 0, s = 0,
+ * top_idx the lowest tokens, gradient 0.  A row holding NaN or +inf gives NaN
+ * (top_idx: NaN before +inf before all else).
+ * tokens and logp may be NULL together; entropy, stats, dstatus may be NULL;
+ * top = 0 wants no alternatives (top_idx, top_logp ignored).
+ * 0 <= top <= min(vocab, SGC_TOP_MAX), 1 <= vocab < 2^31, 0 < scale < inf.
+ * The workspace call returns 0 for bad options; a call needs at least that
+ * much, and ws may be NULL where it returns SGC_LM_WS_NONE.
+ *
+ * Backward, for upstream gradients g [rows] of logp and h [rows] of entropy
+ * (either may be NULL: zero; entropy is read with h only):
+ *   dlogits_i = scale * (g * ([i = token] - p_i) - h * p_i * (log p_i + entropy))
+ * A row whose g and h are zero gets zeros, whatever its logits are; g of a
+ * row without a token counts as zero.  dlogits may be logits, at the same
+ * address and stride.                                                      */
+#define SGC_TOKEN_I32 0
+#define SGC_TOKEN_I64 1
+#define SGC_TOP_MAX 256
+#define SGC_LM_WS_NONE ((size_t)1)
+typedef struct {
+    int64_t rows;
+    int64_t vocab;
+    int32_t dtype;      /* logits, dlogits */
+    int32_t token_type; /* SGC_TOKEN_I32 | SGC_TOKEN_I64 */
+    int32_t top;
+    float scale;        /* 1 / temperature */
+} sgc_logprob_opts;
+
+size_t sgc_token_logprobs_workspace(const sgc_logprob_opts* opt);
+int sgc_token_logprobs(const sgc_logprob_opts* opt, const void* logits, int64_t stride, const void* tokens,
+                       float* logp, float* entropy, float* stats, int32_t* top_idx, float* top_logp,
+                       uint32_t* dstatus, void* ws, size_t ws_bytes, sgc_stream_t stream);
+int sgc_token_logprobs_backward(const sgc_logprob_opts* opt, const void* logits, int64_t stride, const void* tokens,
+                                const float* stats, const float* entropy, const float* dlogp, const float* dentropy,
+                                void* dlogits, int64_t dstride, sgc_stream_t stream);
+
+/* Divergence of a student's distribution from a teacher's top entries, loss
+ * and gradient.  A row has `top` entries (t_idx [rows, top] int32, t_val
+ * [rows, top] fp32, any order): as sgc_token_logprobs lists them, or a
+ * teacher's logits; t_idx -1 is no entry.  q = softmax(scale * logits), Q =
+ * the sum of q over the entries, and the teacher's t from v = t_val:
+ *   SGC_DISTILL_RENORM: t = softmax(teacher_scale * v) over the row's entries;
+ *     loss = sum(t * (log t - log q))
+ *   SGC_DISTILL_TAIL: v are log probabilities over the whole vocabulary, t =
+ *     exp(v) (teacher_scale 1), u = max(0, 1 - sum(t)) is the rest;
+ *     loss = sum(t * (log t - log q)) + u * (log u - log(1 - Q))
+ *     where the last term is 0 if u = 0 or q = 0 everywhere outside.
+ * A term with t = 0 counts 0.  1 - Q is summed outside the entries, not
+ * subtracted.  Gradient, times the row's upstream dloss (NULL: 1):
+ *   dlogits_i = scale * dloss * ((sum(t) + u) * q_i - t_i)              entries
+ *   dlogits_i = scale * dloss * ((sum(t) + u) * q_i - u * q_i / (1 - Q))  else
+ * With dlogits the loss call gives the gradient too (dloss known before:
+ * weights of the rows); without it (NULL) the loss alone, and
+ * sgc_distill_backward gives the gradient from stats [rows, 4] = {max, sum of
+ * exp(scale * (z - max)), that sum outside the entries, 1 or 0 if the row is
+ * skipped}.  stats may be NULL.  dlogits may be logits, at the same address
+ * and stride.
+ * Rows without an entry of t > 0 (SGC_DISTILL_RENORM) or whose logits are
+ * all -inf are skipped: loss 0, gradient 0.  A row with an index >= vocab,
+ * below -1 or given twice is skipped too: loss NaN, gradient 0 and, where
+ * dstatus is given, SGC_STATUS_CORRUPT.  A row with dloss 0 gets zero
+ * gradient, whatever its logits are.  1 <= top <= SGC_TOP_MAX; top may
+ * exceed vocab; scale and teacher_scale finite and > 0.                    */
+#define SGC_DISTILL_RENORM 0
+#define SGC_DISTILL_TAIL 1
+typedef struct {
+    int64_t rows;
+    int64_t vocab;
+    int32_t dtype; /* logits, dlogits */
+    int32_t top;
+    int32_t mode;  /* SGC_DISTILL_RENORM | SGC_DISTILL_TAIL */
+    float scale;
+    float teacher_scale;
+    int32_t reserved; /* 0 */
+} sgc_distill_opts;
+
+size_t sgc_distill_workspace(const sgc_distill_opts* opt);
+int sgc_distill(const sgc_distill_opts* opt, const void* logits, int64_t stride, const int32_t* t_idx,
+                const float* t_val, float* loss, float* stats, const float* dloss, void* dlogits, int64_t dstride,
+                uint32_t* dstatus, void* ws, size_t ws_bytes, sgc_stream_t stream);
+int sgc_distill_backward(const sgc_distill_opts* opt, const void* logits, int64_t stride, const int32_t* t_idx,
+                         const float* t_val, const float* stats, const float* dloss, void* dlogits, int64_t dstride,
+                         sgc_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Measurement hook (benchmarks only).  While set, every sgc_compress call
  * (modes SGC_EXACT and SGC_SAMPLED) records `start` on its stream just
  * before launching the fused residual-add + candidate pass and `stop` just
