@@ -5,146 +5,307 @@
 //   loss = sum_j t_j (log t_j - log q_j) + u (log u - log(o / s)),  q = e / s
 //   dz_i = scale g ((T + u) q_i - t_i)          entries,  T = sum_j t_j
 //   dz_i = scale g ((T + u) q_i - u e_i / o)    else
-// where q_i o / s ... the derivative of the last term of the loss by an outer
-// logit is u (q_i - e_i / o): the rest's share that the logit has of it.
-#include "lm_common.h"
+// The entries of a row are bits in shared memory: one look tells the vectors
+// that hold one, so that o is summed without them and not found by
+// subtraction, which loses it where the student has learnt its teacher.
+#include "lm_softmax.h"
 
 namespace sgc {
 
-constexpr int kDiThreads = 256;
-constexpr int kDiWaves = kDiThreads / 64;
-static_assert(SGC_TOP_MAX <= kDiThreads, "one thread an entry");
+// Rows are shared out in chunks of at most kChunkMax elements a workgroup
+// (its bitmap is 16 KB).
+constexpr int kChunkMax = 131072;
 
-// The row's entries in shared memory, and the teacher's side of them.
-struct Entries {
-    int32_t idx[SGC_TOP_MAX];
-    float t[SGC_TOP_MAX];
-    int bad;
+struct DistillArgs {
+    int64_t rows, zs, dzs;
+    int32_t vocab, top, mode;
+    float scale, c, teacher_scale;
+    const int32_t* idx;
+    const float* val;
+    float* loss;
+    float* stats;
+    const float* dloss;
+    uint32_t* dstatus;
 };
 
-// Loads the entries of a row (bounds and repeats checked: en.bad) and gives
-// T and u; log t_j of the thread's own entry in *log_t.
-__device__ inline void load_entries(Entries& en, const int32_t* idx, const float* val, int top, int64_t vocab, int mode,
-                                    float teacher_scale, float* tmp, float* T, float* u, float* log_t)
-{
-    const int j = threadIdx.x;
-    if (j == 0) en.bad = 0;
-    __syncthreads();
-    const int32_t at = j < top ? idx[j] : -1;
-    float v = -INFINITY;
-    if (j < top) {
-        en.idx[j] = at;
-        if (at < -1 || at >= vocab) en.bad = 1;
-        if (at >= 0) v = val[j] * teacher_scale;
-    }
-    __syncthreads();
-    if (at >= 0)
-        for (int i = 0; i < j; ++i)
-            if (en.idx[i] == at) en.bad = 1;
-    float lt = v;
-    if (mode == SGC_DISTILL_RENORM) {
-        const float m = block_max<kDiWaves>(v, tmp);
-        const float d = v - (m == -INFINITY ? 0.f : m);
-        const float sum = block_sum<kDiWaves>(expf(d), tmp);
-        lt = sum == 0.f ? -INFINITY : d - logf(sum);
-    }
-    const float t = expf(lt);
-    if (j < top) en.t[j] = t;
-    *log_t = lt;
-    const float total = block_sum<kDiWaves>(t, tmp);  // its barriers make t and bad visible
-    *T = mode == SGC_DISTILL_RENORM ? (total > 0.f ? 1.f : total) : total;
-    *u = mode == SGC_DISTILL_RENORM ? 0.f : fmaxf(0.f, 1.f - total);
-}
+// A row's entries, in shared memory; entry j belongs to thread j mod NT.
+struct Entries {
+    float lt[SGC_TOP_MAX];  // log of the teacher's probability
+    float z[SGC_TOP_MAX];   // the student's logit
+    int32_t idx[SGC_TOP_MAX];
+};
 
-__device__ inline int find_entry(const Entries& en, int top, int64_t i)
+// Loads a row's entries and gives T and u.  An entry that is absent or out of
+// range has log t = -inf.  z0, z1: the part of the row that the workgroup
+// reads the logits of.
+template <typename T, int NW>
+__device__ inline void load_entries(Entries& en, const DistillArgs& a, int64_t r, const T* zr, int z0, int z1,
+                                    float* tmp, float* total, float* u)
 {
-    int at = -1;
-    for (int j = 0; j < top; ++j)
-        if (en.idx[j] == i) at = j;
-    return at;
-}
-
-template <typename T>
-__device__ inline void write_gradient(const Entries& en, int top, const T* zr, T* out, int64_t vocab, float scale,
-                                      float g, float m, float s, float o, float mass, float u, bool skip)
-{
-    const float a = mass / s, b = o > 0.f ? u / o : 0.f;
-    for (int64_t i = threadIdx.x; i < vocab; i += kDiThreads) {
-        float d = 0.f;
-        if (!skip) {
-            const float e = expf((to_f(zr[i]) - m) * scale);
-            const int at = find_entry(en, top, i);
-            d = at >= 0 ? e * a - en.t[at] : e * (a - b);
-            d *= scale * g;
-        }
-        out[i] = from_f<T>(d);
-    }
-}
-
-template <typename T>
-__global__ __launch_bounds__(kDiThreads) void k_distill(const T* z, int64_t zs, const int32_t* idx, const float* val,
-                                                        int64_t rows, int64_t vocab, int top, int mode, float scale,
-                                                        float teacher_scale, float* loss, float* stats,
-                                                        const float* dloss, T* dz, int64_t dzs, uint32_t* dstatus)
-{
-    __shared__ float tmp[kDiWaves];
-    __shared__ Entries en;
-    const int64_t r = row_of_block();
-    if (r >= rows) return;
-    const T* zr = z + r * zs;
-    float mass, u, log_t;
-    load_entries(en, idx + r * top, val + r * top, top, vocab, mode, teacher_scale, tmp, &mass, &u, &log_t);
-    const bool bad = en.bad != 0;
+    constexpr int NT = NW * 64;
     float m = -INFINITY;
-    for (int64_t i = threadIdx.x; i < vocab; i += kDiThreads) m = fmaxf(m, to_f(zr[i]));
-    m = block_max<kDiWaves>(m, tmp);
-    const float base = m == -INFINITY ? 0.f : m;
-    float o = 0.f;
-    for (int64_t i = threadIdx.x; i < vocab; i += kDiThreads)
-        if (find_entry(en, top, i) < 0) o += expf((to_f(zr[i]) - base) * scale);
-    o = block_sum<kDiWaves>(o, tmp);
-    const int j = threadIdx.x;
-    const bool has = j < top && !bad && en.idx[j] >= 0;
-    const float y = has ? (to_f(zr[en.idx[j]]) - base) * scale : -INFINITY;
-    const float s = o + block_sum<kDiWaves>(has ? expf(y) : 0.f, tmp);
-    const float ln_s = logf(s);
-    const float t = has ? en.t[j] : 0.f;
-    float l = block_sum<kDiWaves>(has && t != 0.f ? t * (log_t - (y - ln_s)) : 0.f, tmp);
-    if (u > 0.f && o != 0.f) l += u * (logf(u) - (logf(o) - ln_s));
-    const bool skip = bad || s == 0.f || (mode == SGC_DISTILL_RENORM && mass == 0.f);
-    if (threadIdx.x == 0) {
-        loss[r] = bad ? NAN : skip ? 0.f : l;
-        if (stats) {
-            stats[4 * r] = m;
-            stats[4 * r + 1] = s;
-            stats[4 * r + 2] = o;
-            stats[4 * r + 3] = skip ? 0.f : 1.f;
-        }
-        if (bad && dstatus) atomicOr(dstatus, SGC_STATUS_CORRUPT);
+    for (int j = threadIdx.x; j < a.top; j += NT) {
+        const int32_t at = a.idx[r * a.top + j];
+        const float v = at >= 0 && at < a.vocab ? a.val[r * a.top + j] * a.teacher_scale : -INFINITY;
+        en.idx[j] = at;
+        en.lt[j] = v;
+        en.z[j] = at >= z0 && at < z1 ? to_f(zr[at]) : -INFINITY;
+        m = fmaxf(m, v);
     }
-    if (dz) {
-        const float g = dloss ? dloss[r] : 1.f;
-        __syncthreads();
-        write_gradient<T>(en, top, zr, dz + r * dzs, vocab, scale, g, base, s, o, mass + u, u, skip || g == 0.f);
+    float sum = 0.f;
+    if (a.mode == SGC_DISTILL_RENORM) {
+        const float base = finite_base(block_max<NW>(m, tmp));
+        for (int j = threadIdx.x; j < a.top; j += NT) sum += expf(en.lt[j] - base);
+        sum = block_sum<NW>(sum, tmp);
+        const float ln = sum == 0.f ? 0.f : logf(sum) ;
+        for (int j = threadIdx.x; j < a.top; j += NT) en.lt[j] = (en.lt[j] - base) - ln;
+        *total = sum == 0.f ? 0.f : sum != sum ? sum : 1.f;
+        *u = 0.f;
+    } else {
+        for (int j = threadIdx.x; j < a.top; j += NT) sum += expf(en.lt[j]);
+        *total = block_sum<NW>(sum, tmp);
+        *u = fmaxf(0.f, 1.f - *total);
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kDiThreads) void k_distill_back(const T* z, int64_t zs, const int32_t* idx,
-                                                             const float* val, int64_t rows, int64_t vocab, int top,
-                                                             int mode, float scale, float teacher_scale,
-                                                             const float* stats, const float* dloss, T* dz,
-                                                             int64_t dzs)
+// Marks the entries inside [z0, z1) in the bitmap; whether one of the row's is
+// out of range or one of these repeated.  bm holds (z1 - z0 + 31) / 32 words.
+template <int NW>
+__device__ inline bool mark_entries(const Entries& en, const DistillArgs& a, int z0, int z1, uint32_t* bm)
 {
-    __shared__ float tmp[kDiWaves];
+    constexpr int NT = NW * 64;
+    for (int w = threadIdx.x; w < (z1 - z0 + 31) / 32; w += NT) bm[w] = 0;
+    __syncthreads();
+    int bad = 0;
+    for (int j = threadIdx.x; j < a.top; j += NT) {
+        const int32_t at = en.idx[j];
+        if (at < -1 || at >= a.vocab) bad = 1;
+        if (at >= z0 && at < z1) {
+            const uint32_t bit = 1u << ((at - z0) & 31);
+            if (atomicOr(&bm[(at - z0) >> 5], bit) & bit) bad = 1;
+        }
+    }
+    return __syncthreads_or(bad) != 0;
+}
+
+// The gradient of the chunk [z0, z1): e_i k_out everywhere, then the entries'
+// own values over it (every thread's stores are done at the barrier).
+template <typename T, int NW, int U>
+__device__ inline void write_gradient(const Entries& en, const DistillArgs& a, const T* zr, T* out, int z0, int z1,
+                                      float m, float k_out, float k_in, float k_t)
+{
+    constexpr int NT = NW * 64, VL = VecLen<T>::value;
+    using P = Pack<T, VL>;
+    const P* p = (const P*)(zr + z0);
+    P* o = (P*)(out + z0);
+    const int nv = (z1 - z0) / VL;
+    int v = threadIdx.x;
+    for (; v + (U - 1) * NT < nv; v += U * NT) {
+        P q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int e = 0; e < VL; ++e) q[u].v[e] = from_f<T>(exp2_fast((to_f(q[u].v[e]) - m) * a.c) * k_out);
+            o[v + u * NT] = q[u];
+        }
+    }
+    for (; v < nv; v += NT) {
+        P q = p[v];
+#pragma unroll
+        for (int e = 0; e < VL; ++e) q.v[e] = from_f<T>(exp2_fast((to_f(q.v[e]) - m) * a.c) * k_out);
+        o[v] = q;
+    }
+    const int i = z0 + nv * VL + threadIdx.x;
+    if (i < z1) out[i] = from_f<T>(exp2_fast((to_f(zr[i]) - m) * a.c) * k_out);
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.top; j += NT) {
+        const int32_t at = en.idx[j];
+        if (at >= z0 && at < z1)
+            out[at] = from_f<T>(exp2_fast((en.z[j] - m) * a.c) * k_in - expf(en.lt[j]) * k_t);
+    }
+}
+
+template <typename T, int NW>
+__device__ inline void write_zeros(T* out, int z0, int z1)
+{
+    constexpr int NT = NW * 64, VL = VecLen<T>::value;
+    using P = Pack<T, VL>;
+    P zero;
+#pragma unroll
+    for (int e = 0; e < VL; ++e) zero.v[e] = (T)0.f;
+    const int nv = (z1 - z0) / VL;
+    for (int v = threadIdx.x; v < nv; v += NT) ((P*)(out + z0))[v] = zero;
+    const int i = z0 + nv * VL + threadIdx.x;
+    if (i < z1) out[i] = (T)0.f;
+}
+
+// Loss and stats of a row from its sums; whether its gradient is zero.
+template <int NW>
+__device__ inline bool finish_row(const Entries& en, const DistillArgs& a, int64_t r, float m, float o, float s,
+                                  float total, float u, bool bad, float* tmp)
+{
+    constexpr int NT = NW * 64;
+    const float ln_s = logf(s), base = finite_base(m);
+    float l = 0.f;
+    for (int j = threadIdx.x; j < a.top; j += NT) {
+        const float lt = en.lt[j], t = expf(lt);
+        if (t != 0.f) l += t * (lt - ((en.z[j] - base) * a.scale - ln_s));
+    }
+    l = block_sum<NW>(l, tmp);
+    if (u > 0.f && o != 0.f) l += u * (logf(u) - (logf(o) - ln_s));
+    const bool skip = bad || s == 0.f || (a.mode == SGC_DISTILL_RENORM && total == 0.f);
+    if (threadIdx.x == 0) {
+        a.loss[r] = bad ? NAN : skip ? 0.f : l;
+        if (a.stats) {
+            a.stats[4 * r] = m;
+            a.stats[4 * r + 1] = s;
+            a.stats[4 * r + 2] = o;
+            a.stats[4 * r + 3] = skip ? 0.f : 1.f;
+        }
+        if (bad && a.dstatus) atomicOr(a.dstatus, SGC_STATUS_CORRUPT);
+    }
+    return skip;
+}
+
+// Factors of the gradient: exp2 terms outside and inside the entries, t.
+__device__ inline void factors(const DistillArgs& a, float g, float o, float s, float total, float u, float* k_out,
+                               float* k_in, float* k_t)
+{
+    const float k = a.scale * g, q = (total + u) / s;
+    *k_in = k * q;
+    *k_out = k * (q - (u > 0.f && o > 0.f ? u / o : 0.f));
+    *k_t = k;
+}
+
+// A row a workgroup, vocab <= kChunkMax: loss, and with dz the gradient; the
+// row's second reading comes from the cache.
+template <typename T, int NW, bool TAIL>
+__global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T* z, T* dz)
+{
+    extern __shared__ uint32_t bm[];
     __shared__ Entries en;
+    __shared__ float tmp[NW];
     const int64_t r = row_of_block();
-    if (r >= rows) return;
-    float mass, u, log_t;
-    load_entries(en, idx + r * top, val + r * top, top, vocab, mode, teacher_scale, tmp, &mass, &u, &log_t);
-    const float g = dloss ? dloss[r] : 1.f;
-    write_gradient<T>(en, top, z + r * zs, dz + r * dzs, vocab, scale, g, stats[4 * r], stats[4 * r + 1],
-                      stats[4 * r + 2], mass + u, u, stats[4 * r + 3] == 0.f || en.bad || g == 0.f);
+    if (r >= a.rows) return;
+    const T* zr = z + r * a.zs;
+    float total, u;
+    load_entries<T, NW>(en, a, r, zr, 0, a.vocab, tmp, &total, &u);
+    const bool bad = mark_entries<NW>(en, a, 0, a.vocab, bm);
+    SoftSum sum;
+    stream_sums<T, NW * 64, 4, false, TAIL>(zr, a.vocab, a.c, bm, sum);
+    block_join<NW, false>(sum, a.c, tmp);
+    const float base = finite_base(sum.m);
+    float s = sum.s, o = sum.s;
+    if (TAIL) {
+        float in = 0.f;
+        for (int j = threadIdx.x; j < a.top; j += NW * 64)
+            if (en.idx[j] >= 0 && en.idx[j] < a.vocab) in += exp2_fast((en.z[j] - base) * a.c);
+        s += block_sum<NW>(in, tmp);
+    }
+    const bool skip = finish_row<NW>(en, a, r, sum.m, o, s, total, u, bad, tmp);
+    if (!dz) return;
+    const float g = a.dloss ? a.dloss[r] : 1.f;
+    T* out = dz + r * a.dzs;
+    if (skip || g == 0.f) {
+        write_zeros<T, NW>(out, 0, a.vocab);
+        return;
+    }
+    float k_out, k_in, k_t;
+    factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
+    write_gradient<T, NW, 4>(en, a, zr, out, 0, a.vocab, base, k_out, k_in, k_t);
+}
+
+// A chunk of a row: its maximum, sum outside the entries, sum of the entries,
+// and whether one is bad.  part [rows, chunks, 4].
+template <typename T, int NW, bool TAIL>
+__global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T* z, int chunk, int chunks,
+                                                          float* part)
+{
+    extern __shared__ uint32_t bm[];
+    __shared__ Entries en;
+    __shared__ float tmp[NW];
+    const int64_t b = row_of_block(), r = b / chunks;
+    if (r >= a.rows) return;
+    const int z0 = (int)(b - r * chunks) * chunk, z1 = a.vocab - z0 < chunk ? a.vocab : z0 + chunk;
+    const T* zr = z + r * a.zs;
+    for (int j = threadIdx.x; j < a.top; j += NW * 64) {
+        const int32_t at = a.idx[r * a.top + j];
+        en.idx[j] = at;
+        en.z[j] = at >= z0 && at < z1 ? to_f(zr[at]) : -INFINITY;
+    }
+    const bool bad = mark_entries<NW>(en, a, z0, z1, bm);
+    SoftSum sum;
+    stream_sums<T, NW * 64, 4, false, TAIL>(zr + z0, z1 - z0, a.c, bm, sum);
+    block_join<NW, false>(sum, a.c, tmp);
+    float in = 0.f;
+    if (TAIL) {
+        for (int j = threadIdx.x; j < a.top; j += NW * 64)
+            in += exp2_fast((en.z[j] - finite_base(sum.m)) * a.c);
+        in = block_sum<NW>(in, tmp);
+    }
+    if (threadIdx.x == 0) {
+        float* p = part + 4 * b;
+        p[0] = sum.m;
+        p[1] = sum.s;
+        p[2] = in;
+        p[3] = bad ? 1.f : 0.f;
+    }
+}
+
+// The chunks of a row joined, then its loss.
+template <typename T, int NW, bool TAIL>
+__global__ __launch_bounds__(NW * 64) void k_distill_join(DistillArgs a, const T* z, int chunks, const float* part)
+{
+    __shared__ Entries en;
+    __shared__ float tmp[NW];
+    const int64_t r = row_of_block();
+    if (r >= a.rows) return;
+    float total, u;
+    load_entries<T, NW>(en, a, r, z + r * a.zs, 0, a.vocab, tmp, &total, &u);
+    const float* p = part + 4 * r * chunks;
+    float m = -INFINITY;
+    int bad = 0;
+    for (int k = threadIdx.x; k < chunks; k += NW * 64) {
+        m = fmaxf(m, p[4 * k]);
+        bad |= p[4 * k + 3] != 0.f;
+    }
+    m = block_max<NW>(m, tmp);
+    bad = __syncthreads_or(bad);
+    float o = 0.f, in = 0.f;
+    for (int k = threadIdx.x; k < chunks; k += NW * 64) {
+        const float f = exp2_fast(fmaxf((p[4 * k] - finite_base(m)) * a.c, kLowD));
+        o += p[4 * k + 1] * f;
+        in += p[4 * k + 2] * f;
+    }
+    o = block_sum<NW>(o, tmp);
+    in = block_sum<NW>(in, tmp);
+    finish_row<NW>(en, a, r, m, o, TAIL ? o + in : o, total, u, bad != 0, tmp);
+}
+
+// The gradient of a chunk of a row from the row's stats.
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void k_distill_grad(DistillArgs a, const float* stats, const T* z, T* dz,
+                                                          int chunk, int chunks)
+{
+    __shared__ Entries en;
+    __shared__ float tmp[NW];
+    const int64_t b = row_of_block(), r = b / chunks;
+    if (r >= a.rows) return;
+    const int z0 = (int)(b - r * chunks) * chunk, z1 = a.vocab - z0 < chunk ? a.vocab : z0 + chunk;
+    const T* zr = z + r * a.zs;
+    T* out = dz + r * a.dzs;
+    const float g = a.dloss ? a.dloss[r] : 1.f;
+    if (stats[4 * r + 3] == 0.f || g == 0.f) {
+        write_zeros<T, NW>(out, z0, z1);
+        return;
+    }
+    float total, u, k_out, k_in, k_t;
+    load_entries<T, NW>(en, a, r, zr, z0, z1, tmp, &total, &u);
+    __syncthreads();  // the entries' logits are read before any of the chunk's gradient is written
+    factors(a, g, stats[4 * r + 2], stats[4 * r + 1], total, u, &k_out, &k_in, &k_t);
+    write_gradient<T, NW, 4>(en, a, zr, out, z0, z1, finite_base(stats[4 * r]), k_out, k_in, k_t);
 }
 
 static bool distill_opts_ok(const sgc_distill_opts* o)
@@ -161,27 +322,109 @@ static bool entries_ok(const int32_t* idx, const float* val)
     return idx && val && lm_aligned(idx, 4) && lm_aligned(val, 4);
 }
 
-template <typename T>
-static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const int32_t* idx, const float* val,
-                   float* loss, float* stats, const float* dloss, void* dz, int64_t dzs, uint32_t* dstatus,
-                   hipStream_t s)
+// How the rows are shared out.  One workgroup a row where the rows alone fill
+// the card; else chunks, so that there are about kWantBlocks workgroups, of at
+// least kChunkMin elements each.
+constexpr int64_t kWantBlocks = 512;
+constexpr int kChunkMin = 4096;
+
+static int chunks_of(const sgc_distill_opts* o)
 {
-    k_distill<T><<<row_grid(o->rows), kDiThreads, 0, s>>>((const T*)z, zs, idx, val, o->rows, o->vocab, o->top,
-                                                          o->mode, o->scale, o->teacher_scale, loss, stats, dloss,
-                                                          (T*)dz, dzs, dstatus);
+    int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
+    if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
+    if (o->rows >= kWantBlocks) n = 1;
+    if (n < cdiv(o->vocab, kChunkMax)) n = cdiv(o->vocab, kChunkMax);
+    return (int)n;
+}
+
+// Chunks start at a multiple of 64 elements.
+static int chunk_size(int64_t vocab, int chunks) { return (int)((cdiv(vocab, chunks) + 63) & ~(int64_t)63); }
+
+static DistillArgs distill_args(const sgc_distill_opts* o, int64_t zs, const int32_t* idx, const float* val,
+                                const float* dloss, int64_t dzs)
+{
+    DistillArgs a = {};
+    a.rows = o->rows;
+    a.zs = zs;
+    a.dzs = dzs;
+    a.vocab = (int32_t)o->vocab;
+    a.top = o->top;
+    a.mode = o->mode;
+    a.scale = o->scale;
+    a.c = (float)((double)o->scale * M_LOG2E);
+    a.teacher_scale = o->teacher_scale;
+    a.idx = idx;
+    a.val = val;
+    a.dloss = dloss;
+    return a;
+}
+
+template <typename T>
+static int distill_grad(const DistillArgs& a, const float* stats, const T* z, T* dz, hipStream_t s)
+{
+    if (a.vocab <= 2048) {
+        k_distill_grad<T, 1><<<row_grid(a.rows), 64, 0, s>>>(a, stats, z, dz, 2048, 1);
+    } else {
+        const int chunk = 8192, chunks = (int)cdiv(a.vocab, chunk);
+        k_distill_grad<T, 4><<<row_grid(a.rows * chunks), 256, 0, s>>>(a, stats, z, dz, chunk, chunks);
+    }
     SGC_LAUNCH_CHECK();
     return SGC_OK;
+}
+
+template <typename T, bool TAIL>
+static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, float* part, float* stats,
+                        hipStream_t s)
+{
+    const dim3 rows = row_grid(a.rows);
+    if (chunks == 1) {
+        const size_t lds = (size_t)(a.vocab + 31) / 32 * 4;
+        if (a.vocab <= 2048)
+            k_distill_row<T, 1, TAIL><<<rows, 64, lds, s>>>(a, z, dz);
+        else if (a.vocab <= 16384)
+            k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
+        else
+            k_distill_row<T, 8, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+        SGC_LAUNCH_CHECK();
+        return SGC_OK;
+    }
+    const int chunk = chunk_size(a.vocab, chunks);
+    const int used = (int)cdiv(a.vocab, chunk);
+    k_distill_part<T, 4, TAIL><<<row_grid(a.rows * used), 256, (size_t)chunk / 8, s>>>(a, z, chunk, used, part);
+    SGC_LAUNCH_CHECK();
+    DistillArgs j = a;
+    j.stats = stats;
+    k_distill_join<T, 4, TAIL><<<rows, 256, 0, s>>>(j, z, used, part);
+    SGC_LAUNCH_CHECK();
+    return dz ? distill_grad<T>(a, stats, z, dz, s) : SGC_OK;
+}
+
+template <typename T>
+static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const int32_t* idx, const float* val,
+                   float* loss, float* stats, const float* dloss, void* dz, int64_t dzs, uint32_t* dstatus, void* ws,
+                   hipStream_t s)
+{
+    DistillArgs a = distill_args(o, zs, idx, val, dloss, dzs);
+    a.loss = loss;
+    a.stats = stats;
+    a.dstatus = dstatus;
+    const int chunks = chunks_of(o);
+    float* part = nullptr;
+    if (chunks > 1) {
+        Carver c(ws);
+        part = c.take<float>(4 * o->rows * chunks);
+        float* own = c.take<float>(4 * o->rows);
+        if (!stats) stats = own;
+    }
+    return o->mode == SGC_DISTILL_TAIL ? distill_mode<T, true>(a, chunks, (const T*)z, (T*)dz, part, stats, s)
+                                       : distill_mode<T, false>(a, chunks, (const T*)z, (T*)dz, part, stats, s);
 }
 
 template <typename T>
 static int distill_back(const sgc_distill_opts* o, const void* z, int64_t zs, const int32_t* idx, const float* val,
                         const float* stats, const float* dloss, void* dz, int64_t dzs, hipStream_t s)
 {
-    k_distill_back<T><<<row_grid(o->rows), kDiThreads, 0, s>>>((const T*)z, zs, idx, val, o->rows, o->vocab, o->top,
-                                                               o->mode, o->scale, o->teacher_scale, stats, dloss,
-                                                               (T*)dz, dzs);
-    SGC_LAUNCH_CHECK();
-    return SGC_OK;
+    return distill_grad<T>(distill_args(o, zs, idx, val, dloss, dzs), stats, (const T*)z, (T*)dz, s);
 }
 
 }  // namespace sgc
@@ -191,7 +434,12 @@ using namespace sgc;
 extern "C" size_t sgc_distill_workspace(const sgc_distill_opts* o)
 {
     if (!distill_opts_ok(o)) return 0;
-    return SGC_LM_WS_NONE;
+    const int chunks = chunks_of(o);
+    if (chunks == 1) return SGC_LM_WS_NONE;
+    Carver c(nullptr);
+    c.take<float>(4 * o->rows * chunks);
+    c.take<float>(4 * o->rows);
+    return c.off;
 }
 
 extern "C" int sgc_distill(const sgc_distill_opts* o, const void* logits, int64_t stride, const int32_t* t_idx,
@@ -212,10 +460,10 @@ extern "C" int sgc_distill(const sgc_distill_opts* o, const void* logits, int64_
     }
     const hipStream_t s = (hipStream_t)stream;
     return o->dtype == SGC_F32
-               ? distill<float>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, s)
+               ? distill<float>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, ws, s)
            : o->dtype == SGC_BF16
-               ? distill<bf16_t>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, s)
-               : distill<f16_t>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, s);
+               ? distill<bf16_t>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, ws, s)
+               : distill<f16_t>(o, logits, stride, t_idx, t_val, loss, stats, dloss, dlogits, dstride, dstatus, ws, s);
 }
 
 extern "C" int sgc_distill_backward(const sgc_distill_opts* o, const void* logits, int64_t stride,
