@@ -4,112 +4,360 @@
 //   y_i = scale (z_i - m),  m = max z,  s = sum exp(y)
 //   log p_i = y_i - ln s,   H = ln s - sum(exp(y) y) / s
 //   dz_i = scale (g ([i = token] - p_i) - h p_i (log p_i + H))
-#include "lm_common.h"
+//
+// The alternatives cost the pass over the row nothing: each thread's running
+// maximum, which the softmax needs anyway, is a filter.  At least `top`
+// elements reach the top-th largest of the threads' maxima, few others do,
+// and only the threads whose own maximum reaches it hold any: their elements
+// are read again (from the cache), the ones that reach it are ranked by
+// counting.
+#include "lm_softmax.h"
 
 namespace sgc {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWaves = kLpThreads / 64;
+constexpr float kLn2 = 0.693147180559945309f;
+
+struct LogprobArgs {
+    int64_t rows, zs;
+    int32_t vocab, top, token_type;
+    float scale, c;
+    const void* tokens;
+    float* logp;
+    float* entropy;
+    float* stats;
+    int32_t* top_idx;
+    float* top_logp;
+    uint32_t* dstatus;
+};
 
 __device__ inline int64_t token_at(const void* tokens, int type, int64_t r)
 {
     return type == SGC_TOKEN_I64 ? ((const int64_t*)tokens)[r] : (int64_t)((const int32_t*)tokens)[r];
 }
 
-template <typename T>
-__global__ __launch_bounds__(kLpThreads) void k_logprobs(const T* z, int64_t zs, const void* tokens, int token_type,
-                                                         int64_t rows, int64_t vocab, float scale, int top,
-                                                         float* logp, float* entropy, float* stats, int32_t* top_idx,
-                                                         float* top_logp, uint32_t* dstatus)
+// The value an order key was made of (the two zeros as +0, any NaN as one).
+__device__ inline float key_value(uint32_t k)
 {
-    __shared__ float tmp[kLpWaves];
-    __shared__ unsigned long long best;
-    const int64_t r = row_of_block();
-    if (r >= rows) return;
-    const T* zr = z + r * zs;
-    float m = -INFINITY;
-    for (int64_t i = threadIdx.x; i < vocab; i += kLpThreads) m = fmaxf(m, to_f(zr[i]));
-    m = block_max<kLpWaves>(m, tmp);
-    const float base = m == -INFINITY ? 0.f : m;
-    float s = 0.f, t = 0.f;
-    for (int64_t i = threadIdx.x; i < vocab; i += kLpThreads) {
-        const float y = (to_f(zr[i]) - base) * scale;
-        const float e = expf(y);
-        s += e;
-        t = fmaf(e, fmaxf(y, -1e4f), t);
+    if (k == 0xffffffffu) return NAN;
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
+// Candidates in shared memory: the fallback adds two a thread to a kept list.
+template <int NW>
+struct Candidates {
+    static constexpr int NT = NW * 64;
+    static constexpr int kCap = 2 * NT + SGC_TOP_MAX;
+    uint64_t key[kCap];
+    uint64_t sorted[SGC_TOP_MAX];
+    uint32_t peak[NT];  // the threads' maxima as order keys, then the threads that hold candidates
+    int n, threads;
+    uint32_t bar;
+};
+
+// sorted[0 .. min(n, top)) = the largest of key[0 .. n), largest first: each
+// key's place is the number of larger ones (keys are unique).
+template <int NW>
+__device__ inline void rank_keys(Candidates<NW>& cd, int n, int top)
+{
+    for (int i = threadIdx.x; i < n; i += NW * 64) {
+        const uint64_t k = cd.key[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += cd.key[j] > k;
+        if (place < top) cd.sorted[place] = k;
     }
-    s = block_sum<kLpWaves>(s, tmp);
-    t = block_sum<kLpWaves>(t, tmp);
-    const float ln_s = logf(s);
-    const bool none = s == 0.f;
-    if (threadIdx.x == 0) {
-        if (stats) {
-            stats[2 * r] = m;
-            stats[2 * r + 1] = s;
+    __syncthreads();
+}
+
+// The `top` best of any row, one pass in order of the places: a full list is
+// cut to its best, whose last key later elements have to pass.  For rows with
+// NaN or +inf, or with so many equal values that the filter lets too many
+// through.  Returns how many there are (less than top in a short row).
+template <typename K, int NW>
+__device__ inline int top_in_order(Candidates<NW>& cd, const K& key_at, int len, int top)
+{
+    constexpr int NT = NW * 64;
+    uint64_t bar = 0;
+    if (threadIdx.x == 0) cd.n = 0;
+    __syncthreads();
+    int n = 0;
+    for (int i0 = 0; i0 < len; i0 += 2 * NT) {
+        if (n > SGC_TOP_MAX) {
+            rank_keys<NW>(cd, n, top);
+            bar = cd.sorted[top - 1];  // n > top
+            for (int j = threadIdx.x; j < top; j += NT) cd.key[j] = cd.sorted[j];
+            if (threadIdx.x == 0) cd.n = top;
+            __syncthreads();
         }
-        if (entropy) entropy[r] = none ? 0.f : ln_s - t / s;
-        if (logp) {
-            const int64_t tok = token_at(tokens, token_type, r);
-            float lp = 0.f;
-            if (tok >= vocab) {
-                lp = NAN;
-                if (dstatus) atomicOr(dstatus, SGC_STATUS_BAD_INPUT);
-            } else if (tok >= 0) {
-                lp = none ? -INFINITY : (to_f(zr[tok]) - base) * scale - ln_s;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = i0 + e * NT + threadIdx.x;
+            const uint64_t k = i < len ? key_at(i) : 0;
+            if (k > bar) cd.key[atomicAdd(&cd.n, 1)] = k;
+        }
+        __syncthreads();
+        n = cd.n;
+        __syncthreads();
+    }
+    rank_keys<NW>(cd, n, top);
+    return n < top ? n : top;
+}
+
+// The `top` best elements of z[0, len) into cd.sorted as order keys with their
+// places from `first` on.  m: the thread's maximum over its elements, those of
+// stream_sums.  Returns how many.
+template <typename T, int NW>
+__device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first, int top, float m, bool broken)
+{
+    constexpr int NT = NW * 64, VL = VecLen<T>::value;
+    const auto key_at = [&](int i) { return order_key(to_f(z[i]), (uint32_t)(first + i)); };
+    const int nv = len / VL;
+    if (!broken) {
+        cd.peak[threadIdx.x] = order_key(m);
+        if (threadIdx.x == 0) cd.n = cd.threads = 0;
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            // the largest value of 16 leading bits that `top` maxima reach
+            uint32_t k[NW], bar = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) k[w] = cd.peak[w * 64 + threadIdx.x];
+            if (top <= NT)
+                for (int b = 31; b >= 16; --b) {
+                    const uint32_t to = bar | (1u << b);
+                    int reach = 0;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) reach += __popcll(__ballot(k[w] >= to));
+                    if (reach >= top) bar = to;
+                }
+            if (threadIdx.x == 0) cd.bar = bar;
+        }
+        __syncthreads();
+        const uint32_t bar = cd.bar;
+        const float low = bar < 0x00800000u ? -INFINITY : key_value(bar);
+        const bool holds = m >= low;
+        __syncthreads();
+        if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
+        __syncthreads();
+        // (thread, vector) pairs, and one more for its element past the vectors
+        const int per = (nv + NT - 1) / NT + 1, items = cd.threads * per;
+        for (int it = threadIdx.x; it < items; it += NT) {
+            const int f = it / per, v = it - f * per, th = (int)cd.peak[f];
+            const auto offer = [&](float x, int i) {
+                if (x >= low) {
+                    const int at = atomicAdd(&cd.n, 1);
+                    if (at < cd.kCap) cd.key[at] = order_key(x, (uint32_t)(first + i));
+                }
+            };
+            if (v == per - 1) {
+                const int i = nv * VL + th;
+                if (i < len) offer(to_f(z[i]), i);
+            } else if (th + v * NT < nv) {
+                const int at = th + v * NT;
+                const Pack<T, VL> q = ((const Pack<T, VL>*)z)[at];
+#pragma unroll
+                for (int e = 0; e < VL; ++e) offer(to_f(q.v[e]), at * VL + e);
             }
-            logp[r] = lp;
         }
+        __syncthreads();
+        const int n = cd.n;
+        if (n <= cd.kCap) {
+            rank_keys<NW>(cd, n, top);
+            return n < top ? n : top;
+        }
+        __syncthreads();
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < top; ++k) {
-        if (threadIdx.x == 0) best = 0;
-        __syncthreads();
-        unsigned long long mine = 0;
-        for (int64_t i = threadIdx.x; i < vocab; i += kLpThreads) {
-            const unsigned long long key = order_key(to_f(zr[i]), (uint32_t)i);
-            if ((key < last || k == 0) && key > mine) mine = key;
+    return top_in_order<decltype(key_at), NW>(cd, key_at, len, top);
+}
+
+// What a row's sums give: logp, entropy, stats; ln s and the base of y.
+__device__ inline void finish_row(const LogprobArgs& a, int64_t r, float z_tok, int64_t tok, const SoftSum& sum,
+                                  float ln_s)
+{
+    const bool none = sum.s == 0.f;
+    if (a.stats) {
+        a.stats[2 * r] = sum.m;
+        a.stats[2 * r + 1] = sum.s;
+    }
+    if (a.entropy) a.entropy[r] = none ? 0.f : ln_s - kLn2 * (sum.t / sum.s);
+    if (a.logp) {
+        float lp = 0.f;
+        if (tok >= a.vocab) {
+            lp = NAN;
+            if (a.dstatus) atomicOr(a.dstatus, SGC_STATUS_BAD_INPUT);
+        } else if (tok >= 0) {
+            lp = none ? -INFINITY : (z_tok - finite_base(sum.m)) * a.scale - ln_s;
         }
-        atomicMax(&best, mine);
-        __syncthreads();
-        last = best;
-        if (threadIdx.x == 0) {
-            const uint32_t at = ~(uint32_t)last;
-            top_idx[r * top + k] = (int32_t)at;
-            top_logp[r * top + k] = none ? -INFINITY : (to_f(zr[at]) - base) * scale - ln_s;
-        }
-        __syncthreads();
+        a.logp[r] = lp;
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kLpThreads) void k_logprobs_back(const T* z, int64_t zs, const void* tokens,
-                                                              int token_type, int64_t rows, int64_t vocab, float scale,
-                                                              const float* stats, const float* entropy,
-                                                              const float* dlogp, const float* dentropy, T* dz,
-                                                              int64_t dzs)
+__device__ inline void write_top(const LogprobArgs& a, int64_t r, int k, uint64_t key, const SoftSum& sum, float ln_s)
 {
+    const float v = key_value((uint32_t)(key >> 32));
+    a.top_idx[r * a.top + k] = (int32_t)~(uint32_t)key;
+    a.top_logp[r * a.top + k] = sum.s == 0.f ? -INFINITY : (v - finite_base(sum.m)) * a.scale - ln_s;
+}
+
+// A row a workgroup.
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)
+{
+    __shared__ Candidates<NW> cd;
+    __shared__ float tmp[NW];
     const int64_t r = row_of_block();
-    if (r >= rows) return;
-    const T* zr = z + r * zs;
-    T* out = dz + r * dzs;
-    const float m = stats[2 * r], s = stats[2 * r + 1];
-    const int64_t tok = tokens ? token_at(tokens, token_type, r) : -1;
-    const float g = dlogp && tok >= 0 && tok < vocab ? dlogp[r] : 0.f;
-    const float h = dentropy ? dentropy[r] : 0.f;
-    const float H = dentropy ? entropy[r] : 0.f;
-    const bool zero = (g == 0.f && h == 0.f) || s == 0.f;
-    const float ln_s = logf(s);
-    for (int64_t i = threadIdx.x; i < vocab; i += kLpThreads) {
-        float d = 0.f;
-        if (!zero) {
-            const float y = (to_f(zr[i]) - m) * scale;
-            const float p = expf(y) / s;
-            d = -p * (g + h * (fmaxf(y, -1e4f) - ln_s + H));
-            if (i == tok) d += g;
-            d *= scale;
-        }
-        out[i] = from_f<T>(d);
+    if (r >= a.rows) return;
+    const T* zr = z + r * a.zs;
+    int64_t tok = -1;
+    float z_tok = 0.f;
+    if (threadIdx.x == 0 && a.logp) {
+        tok = token_at(a.tokens, a.token_type, r);
+        if (tok >= 0 && tok < a.vocab) z_tok = to_f(zr[tok]);
     }
+    SoftSum sum;
+    stream_sums<T, NW * 64, 4, true, false>(zr, a.vocab, a.c, nullptr, sum);
+    const float m = sum.m;
+    block_join<NW, true>(sum, a.c, tmp);
+    const float ln_s = logf(sum.s);
+    if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
+    if (a.top) {
+        const int n = top_of<T, NW>(cd, zr, a.vocab, 0, a.top, m, sum.s != sum.s);
+        for (int k = threadIdx.x; k < n; k += NW * 64) write_top(a, r, k, cd.sorted[k], sum, ln_s);
+    }
+}
+
+// A chunk of a row: its sums in part [rows, chunks, 4], its best elements in
+// keys [rows, chunks, top] (0: none).
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, int chunk, int chunks, float* part,
+                                                     uint64_t* keys)
+{
+    __shared__ Candidates<NW> cd;
+    __shared__ float tmp[NW];
+    const int64_t b = row_of_block(), r = b / chunks;
+    if (r >= a.rows) return;
+    const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
+    const T* zr = z + r * a.zs + z0;
+    SoftSum sum;
+    stream_sums<T, NW * 64, 4, true, false>(zr, len, a.c, nullptr, sum);
+    const float m = sum.m;
+    block_join<NW, true>(sum, a.c, tmp);
+    if (threadIdx.x == 0) {
+        part[4 * b] = sum.m;
+        part[4 * b + 1] = sum.s;
+        part[4 * b + 2] = sum.t;
+    }
+    if (a.top) {
+        const int n = top_of<T, NW>(cd, zr, len, z0, a.top, m, sum.s != sum.s);
+        for (int k = threadIdx.x; k < a.top; k += NW * 64) keys[b * a.top + k] = k < n ? cd.sorted[k] : 0;
+    }
+}
+
+// The chunks of a row joined.  The best keys of all chunks are cut to `top` as
+// a row's elements are: by the threads' largest, on the keys' upper half.
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, int chunks, const float* part,
+                                                     const uint64_t* keys)
+{
+    constexpr int NT = NW * 64;
+    __shared__ Candidates<NW> cd;
+    __shared__ float tmp[NW];
+    const int64_t r = row_of_block();
+    if (r >= a.rows) return;
+    int64_t tok = -1;
+    float z_tok = 0.f;
+    if (threadIdx.x == 0 && a.logp) {
+        tok = token_at(a.tokens, a.token_type, r);
+        if (tok >= 0 && tok < a.vocab) z_tok = to_f(z[r * a.zs + tok]);
+    }
+    SoftSum sum;
+    const float* p = part + 4 * r * chunks;
+    for (int k = threadIdx.x; k < chunks; k += NT) {
+        SoftSum o;
+        o.m = p[4 * k];
+        o.s = p[4 * k + 1];
+        o.t = p[4 * k + 2];
+        if (o.m > sum.m)
+            sum.raise<true>(o.m, a.c);
+        const float d = fmaxf((o.m - finite_base(sum.m)) * a.c, kLowD), f = exp2_fast(d);
+        sum.t += fmaf(d, o.s, o.t) * f;
+        sum.s += o.s * f;
+    }
+    block_join<NW, true>(sum, a.c, tmp);
+    const float ln_s = logf(sum.s);
+    if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
+    if (!a.top) return;
+    const uint64_t* kr = keys + r * chunks * a.top;
+    const int len = chunks * a.top;
+    const auto key_at = [&](int i) { return kr[i]; };
+    int n;
+    if (len <= cd.kCap) {
+        for (int i = threadIdx.x; i < len; i += NT) cd.key[i] = kr[i];
+        __syncthreads();
+        rank_keys<NW>(cd, len, a.top);
+        n = a.top;
+    } else {
+        n = top_in_order<decltype(key_at), NW>(cd, key_at, len, a.top);
+    }
+    for (int k = threadIdx.x; k < n; k += NT) write_top(a, r, k, cd.sorted[k], sum, ln_s);
+}
+
+// The gradient of a chunk of a row: e (A + B d) with d and e of the softmax's
+// pass, and the token's own part where it falls.
+template <typename T, int NW, bool ENT>
+__global__ __launch_bounds__(NW * 64) void k_lp_back(LogprobArgs a, const float* stats, const float* entropy,
+                                                     const float* dlogp, const float* dentropy, const T* z, T* dz,
+                                                     int64_t dzs, int chunk, int chunks)
+{
+    constexpr int NT = NW * 64, VL = VecLen<T>::value, U = 4;
+    using P = Pack<T, VL>;
+    const int64_t b = row_of_block(), r = b / chunks;
+    if (r >= a.rows) return;
+    const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
+    const int nv = len / VL;
+    const P* p = (const P*)(z + r * a.zs + z0);
+    P* o = (P*)(dz + r * dzs + z0);
+    const int64_t tok = dlogp ? token_at(a.tokens, a.token_type, r) : -1;
+    const float g = tok >= 0 && tok < a.vocab ? dlogp[r] : 0.f;
+    const float h = ENT ? dentropy[r] : 0.f;
+    const float s = stats[2 * r + 1];
+    if ((g == 0.f && h == 0.f) || s == 0.f) {
+        P zero;
+#pragma unroll
+        for (int e = 0; e < VL; ++e) zero.v[e] = (T)0.f;
+        for (int v = threadIdx.x; v < nv; v += NT) o[v] = zero;
+        if (nv * VL + (int)threadIdx.x < len) ((T*)o)[nv * VL + threadIdx.x] = (T)0.f;
+        return;
+    }
+    const float m = finite_base(stats[2 * r]);
+    const float A = -a.scale / s * (ENT ? fmaf(h, entropy[r] - logf(s), g) : g), B = ENT ? -a.scale * h * kLn2 / s : 0.f;
+    const int at = tok >= z0 && tok < z0 + len ? (int)(tok - z0) : -1;  // the token's place in the chunk
+    const float add = a.scale * g;
+    const auto grad = [&](float x, int i) {
+        const float d = (x - m) * a.c;
+        const float v = exp2_fast(d) * (ENT ? fmaf(B, fmaxf(d, kLowD), A) : A);
+        return i == at ? v + add : v;
+    };
+    int v = threadIdx.x;
+    for (; v + (U - 1) * NT < nv; v += U * NT) {
+        P q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int e = 0; e < VL; ++e)
+                q[u].v[e] = from_f<T>(grad(to_f(q[u].v[e]), (v + u * NT) * VL + e));
+            o[v + u * NT] = q[u];
+        }
+    }
+    for (; v < nv; v += NT) {
+        P q = p[v];
+#pragma unroll
+        for (int e = 0; e < VL; ++e) q.v[e] = from_f<T>(grad(to_f(q.v[e]), v * VL + e));
+        o[v] = q;
+    }
+    const int i = nv * VL + threadIdx.x;
+    if (i < len) ((T*)o)[i] = from_f<T>(grad(to_f(((const T*)p)[i]), i));
 }
 
 static bool logprob_opts_ok(const sgc_logprob_opts* o)
@@ -124,13 +372,86 @@ static bool tokens_ok(const sgc_logprob_opts* o, const void* tokens)
     return tokens && lm_aligned(tokens, o->token_type == SGC_TOKEN_I64 ? 8 : 4);
 }
 
-template <typename T>
-static int logprobs(const sgc_logprob_opts* o, const void* z, int64_t zs, const void* tokens, float* logp,
-                    float* entropy, float* stats, int32_t* top_idx, float* top_logp, uint32_t* dstatus, hipStream_t s)
+// How the rows are shared out: one workgroup a row where the rows alone fill
+// the card; else chunks, so that there are about kWantBlocks workgroups, of at
+// least kChunkMin elements each.
+constexpr int64_t kWantBlocks = 512;
+constexpr int kChunkMin = 4096;
+
+static int chunks_of(const sgc_logprob_opts* o)
 {
-    k_logprobs<T><<<row_grid(o->rows), kLpThreads, 0, s>>>((const T*)z, zs, tokens, o->token_type, o->rows, o->vocab,
-                                                           o->scale, o->top, logp, entropy, stats, top_idx, top_logp,
-                                                           dstatus);
+    int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
+    if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
+    return o->rows >= kWantBlocks ? 1 : (int)n;
+}
+
+// Chunks start at a multiple of 64 elements.
+static int chunk_size(int64_t vocab, int chunks) { return (int)((cdiv(vocab, chunks) + 63) & ~(int64_t)63); }
+
+static LogprobArgs logprob_args(const sgc_logprob_opts* o, int64_t zs, const void* tokens)
+{
+    LogprobArgs a = {};
+    a.rows = o->rows;
+    a.zs = zs;
+    a.vocab = (int32_t)o->vocab;
+    a.top = o->top;
+    a.token_type = o->token_type;
+    a.scale = o->scale;
+    a.c = (float)((double)o->scale * M_LOG2E);
+    a.tokens = tokens;
+    return a;
+}
+
+template <typename T>
+static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const void* tokens, float* logp,
+                    float* entropy, float* stats, int32_t* top_idx, float* top_logp, uint32_t* dstatus, void* ws,
+                    hipStream_t s)
+{
+    LogprobArgs a = logprob_args(o, zs, tokens);
+    a.logp = logp;
+    a.entropy = entropy;
+    a.stats = stats;
+    a.top_idx = top_idx;
+    a.top_logp = top_logp;
+    a.dstatus = dstatus;
+    const T* z = (const T*)zv;
+    const int chunks = chunks_of(o);
+    const dim3 rows = row_grid(o->rows);
+    if (chunks == 1) {
+        if (a.vocab <= 2048 && a.top <= 32)
+            k_lp_row<T, 1><<<rows, 64, 0, s>>>(a, z);
+        else if (a.vocab <= 16384 && a.top <= 64)
+            k_lp_row<T, 4><<<rows, 256, 0, s>>>(a, z);
+        else
+            k_lp_row<T, 8><<<rows, 512, 0, s>>>(a, z);
+        SGC_LAUNCH_CHECK();
+        return SGC_OK;
+    }
+    const int chunk = chunk_size(a.vocab, chunks), used = (int)cdiv(a.vocab, chunk);
+    Carver c(ws);
+    float* part = c.take<float>(4 * o->rows * chunks);
+    uint64_t* keys = c.take<uint64_t>((int64_t)o->top * o->rows * chunks);
+    const dim3 parts = row_grid(o->rows * used);
+    if (a.top <= 64)
+        k_lp_part<T, 4><<<parts, 256, 0, s>>>(a, z, chunk, used, part, keys);
+    else
+        k_lp_part<T, 8><<<parts, 512, 0, s>>>(a, z, chunk, used, part, keys);
+    SGC_LAUNCH_CHECK();
+    k_lp_join<T, 8><<<rows, 512, 0, s>>>(a, z, used, part, keys);
+    SGC_LAUNCH_CHECK();
+    return SGC_OK;
+}
+
+template <typename T, int NW>
+static int logprobs_back(const LogprobArgs& a, const T* z, const float* stats, const float* entropy,
+                         const float* dlogp, const float* dentropy, T* dz, int64_t dzs, int chunk, hipStream_t s)
+{
+    const int chunks = (int)cdiv(a.vocab, chunk);
+    const dim3 grid = row_grid(a.rows * chunks);
+    if (dentropy)
+        k_lp_back<T, NW, true><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk, chunks);
+    else
+        k_lp_back<T, NW, false><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk, chunks);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
@@ -140,11 +461,10 @@ static int logprobs_back(const sgc_logprob_opts* o, const void* z, int64_t zs, c
                          const float* entropy, const float* dlogp, const float* dentropy, void* dz, int64_t dzs,
                          hipStream_t s)
 {
-    k_logprobs_back<T><<<row_grid(o->rows), kLpThreads, 0, s>>>((const T*)z, zs, tokens, o->token_type, o->rows,
-                                                                o->vocab, o->scale, stats, entropy, dlogp, dentropy,
-                                                                (T*)dz, dzs);
-    SGC_LAUNCH_CHECK();
-    return SGC_OK;
+    const LogprobArgs a = logprob_args(o, zs, tokens);
+    return a.vocab <= 2048
+               ? logprobs_back<T, 1>(a, (const T*)z, stats, entropy, dlogp, dentropy, (T*)dz, dzs, 2048, s)
+               : logprobs_back<T, 4>(a, (const T*)z, stats, entropy, dlogp, dentropy, (T*)dz, dzs, 8192, s);
 }
 
 }  // namespace sgc
@@ -154,7 +474,12 @@ using namespace sgc;
 extern "C" size_t sgc_token_logprobs_workspace(const sgc_logprob_opts* o)
 {
     if (!logprob_opts_ok(o)) return 0;
-    return SGC_LM_WS_NONE;
+    const int chunks = chunks_of(o);
+    if (chunks == 1) return SGC_LM_WS_NONE;
+    Carver c(nullptr);
+    c.take<float>(4 * o->rows * chunks);
+    c.take<uint64_t>((int64_t)o->top * o->rows * chunks);
+    return c.off;
 }
 
 extern "C" int sgc_token_logprobs(const sgc_logprob_opts* o, const void* logits, int64_t stride, const void* tokens,
@@ -176,10 +501,10 @@ extern "C" int sgc_token_logprobs(const sgc_logprob_opts* o, const void* logits,
     }
     const hipStream_t s = (hipStream_t)stream;
     return o->dtype == SGC_F32
-               ? logprobs<float>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, s)
+               ? logprobs<float>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, ws, s)
            : o->dtype == SGC_BF16
-               ? logprobs<bf16_t>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, s)
-               : logprobs<f16_t>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, s);
+               ? logprobs<bf16_t>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, ws, s)
+               : logprobs<f16_t>(o, logits, stride, tokens, logp, entropy, stats, top_idx, top_logp, dstatus, ws, s);
 }
 
 extern "C" int sgc_token_logprobs_backward(const sgc_logprob_opts* o, const void* logits, int64_t stride,
