@@ -4,32 +4,302 @@
 //   y  = (x - mean) rstd w + b
 //   dx = rstd (v - mean(v) - xh mean(v xh)),  v = dy w,  xh = (x - mean) rstd
 //   dw = sum_rows dy xh,  db = sum_rows dy
+//
+// A row stays in registers between its sums and its output: it is read once.
+// NWR waves share a row, EPT elements a thread; RPB rows go through a
+// workgroup side by side, and a workgroup takes row after row, so that its
+// columns' weights are loaded once and their gradients' sums stay in its
+// registers; the next rows are on their way while one is worked on.  Rows too
+// long for that (over kNormHeld elements) are read again for every pass.
 #include "lm_common.h"
 
 namespace sgc {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormWaves = kNormThreads / 64;
+constexpr int64_t kNormHeld = 16384;
+constexpr int64_t kCus = 256;
+
+// Elements [v VL, v VL + VL) of a row that end at cols; past it 0.
+template <typename T, int VL>
+__device__ inline Pack<T, VL> load_vec(const T* p, int v, int cols)
+{
+    Pack<T, VL> q;
+    if ((v + 1) * VL <= cols) {
+        q = ((const Pack<T, VL>*)p)[v];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; ++e) q.v[e] = v * VL + e < cols ? p[v * VL + e] : (T)0.f;
+    }
+    return q;
+}
+template <typename T, int VL>
+__device__ inline void store_vec(T* p, int v, int cols, const Pack<T, VL>& q)
+{
+    if ((v + 1) * VL <= cols) {
+        ((Pack<T, VL>*)p)[v] = q;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; ++e)
+            if (v * VL + e < cols) p[v * VL + e] = q.v[e];
+    }
+}
+// EPT columns of a thread's weights as fp32; `none` where there are none.
+template <typename W, int VL, int NV, int NTR>
+__device__ inline void load_weights(const W* w, int t, int cols, float none, float* out)
+{
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int v = n * NTR + t;
+        if (w) {
+            const Pack<W, VL> q = load_vec<W, VL>(w, v, cols);
+#pragma unroll
+            for (int e = 0; e < VL; ++e) out[n * VL + e] = to_f(q.v[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VL; ++e) out[n * VL + e] = none;
+        }
+    }
+}
+
+// Two sums over the NWR waves of a row, one barrier; tmp is another half at
+// every other call (`turn`), so the next call may write while this one reads.
+template <int NWR, int RPB>
+__device__ inline void row_sums(float& a, float& b, float (*tmp)[RPB][NWR][2], int turn)
+{
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if (NWR == 1) return;
+    const int wave = threadIdx.x >> 6, sub = wave / NWR, w = wave % NWR;
+    if ((threadIdx.x & 63) == 0) {
+        tmp[turn][sub][w][0] = a;
+        tmp[turn][sub][w][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < NWR; ++i) {
+        a += tmp[turn][sub][i][0];
+        b += tmp[turn][sub][i][1];
+    }
+}
+
+template <typename T, typename W, int NWR, int EPT, int RPB>
+__global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
+                                                        int64_t ys, float* mean, float* rstd, int64_t rows, int cols,
+                                                        float eps)
+{
+    constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
+    __shared__ float tmp[2][RPB][NWR][2];
+    const int sub = threadIdx.x / NTR, t = threadIdx.x % NTR;
+    float wf[EPT], bf[EPT];
+    load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
+    load_weights<W, VL, NV, NTR>(b, t, cols, 0.f, bf);
+    const float inv = 1.f / (float)cols;
+    Pack<T, VL> next[NV] = {};
+    int64_t r = (int64_t)blockIdx.x * RPB + sub;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    if (r < rows) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) next[n] = load_vec<T, VL>(x + r * xs, n * NTR + t, cols);
+    }
+    for (; r - sub < rows; r += step) {
+        float f[EPT];
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < VL; ++e) f[n * VL + e] = to_f(next[n].v[e]);
+        if (r + step < rows) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) next[n] = load_vec<T, VL>(x + (r + step) * xs, n * NTR + t, cols);
+        }
+        float s = 0.f, q = 0.f, none = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) s += f[i];
+        row_sums<NWR, RPB>(s, none, tmp, 0);
+        const float m = s / (float)cols;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const float d = f[i] - m;
+            f[i] = d;
+            if ((i / VL * NTR + t) * VL + i % VL < cols) q = fmaf(d, d, q);
+        }
+        none = 0.f;
+        row_sums<NWR, RPB>(q, none, tmp, 1);
+        const float rs = 1.f / sqrtf(q / (float)cols + eps);
+        if (r < rows) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                Pack<T, VL> o;
+#pragma unroll
+                for (int e = 0; e < VL; ++e) {
+                    const int i = n * VL + e;
+                    o.v[e] = from_f<T>(fmaf(f[i] * rs, wf[i], bf[i]));
+                }
+                store_vec<T, VL>(y + r * ys, n * NTR + t, cols, o);
+            }
+            if (t == 0) {
+                if (mean) mean[r] = m;
+                if (rstd) rstd[r] = rs;
+            }
+        }
+    }
+}
+
+// dx, and the workgroup's sums of dy xh and dy over its rows: part
+// [workgroups, 2, cols].
+template <typename T, typename W, int NWR, int EPT, int RPB>
+__global__ __launch_bounds__(NWR* RPB * 64) void k_norm_back(const T* dy, int64_t dys, const T* x, int64_t xs,
+                                                             const W* w, const float* mean, const float* rstd, T* dx,
+                                                             int64_t dxs, float* part, int64_t rows, int cols)
+{
+    constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
+    __shared__ float tmp[2][RPB][NWR][2];
+    const int sub = threadIdx.x / NTR, t = threadIdx.x % NTR;
+    float wf[EPT], aw[EPT], ab[EPT];
+    load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
+    Pack<T, VL> nx[NV] = {}, ny[NV] = {};
+    float nm = 0.f, nr = 0.f;
+    int64_t r = (int64_t)blockIdx.x * RPB + sub;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    const auto fetch = [&](int64_t at) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            nx[n] = load_vec<T, VL>(x + at * xs, n * NTR + t, cols);
+            ny[n] = load_vec<T, VL>(dy + at * dys, n * NTR + t, cols);
+        }
+        nm = mean[at];
+        nr = rstd[at];
+    };
+    // 16 elements a thread leave no registers for the next row's (128 of them at
+    // 16 waves; fetched ahead they spill 108)
+    constexpr bool kAhead = EPT < 16;
+    if (kAhead && r < rows) fetch(r);
+    int turn = 0;
+    for (; r - sub < rows; r += step, turn ^= 1) {
+        const bool live = r < rows;
+        if (!kAhead && live) fetch(r);
+        float h[EPT], g[EPT];
+        const float m = nm, rs = nr;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < VL; ++e) {
+                h[n * VL + e] = live ? to_f(nx[n].v[e]) : m;
+                g[n * VL + e] = live ? to_f(ny[n].v[e]) : 0.f;
+            }
+        if (kAhead && r + step < rows) fetch(r + step);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {  // past cols dy is 0
+            h[i] = (h[i] - m) * rs;
+            aw[i] = fmaf(g[i], h[i], aw[i]);
+            ab[i] += g[i];
+            g[i] *= wf[i];
+            s1 += g[i];
+            s2 = fmaf(g[i], h[i], s2);
+        }
+        if (dx) {
+            row_sums<NWR, RPB>(s1, s2, tmp, turn);
+            const float c1 = s1 / (float)cols, c2 = s2 / (float)cols;
+            if (live) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    Pack<T, VL> o;
+#pragma unroll
+                    for (int e = 0; e < VL; ++e) {
+                        const int i = n * VL + e;
+                        o.v[e] = from_f<T>(rs * (g[i] - fmaf(h[i], c2, c1)));
+                    }
+                    store_vec<T, VL>(dx + r * dxs, n * NTR + t, cols, o);
+                }
+            }
+        }
+    }
+    if (!part) return;
+    // the rows side by side in the workgroup, one after the other
+    constexpr int kSum = RPB > 1 ? NTR * EPT : 1;
+    __shared__ float sw[2][kSum];
+    if (RPB > 1) {
+        for (int k = RPB - 1; k > 0; --k) {
+            __syncthreads();
+            if (sub == k) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) {
+                    if (k < RPB - 1) {
+                        aw[i] += sw[0][i * NTR + t];
+                        ab[i] += sw[1][i * NTR + t];
+                    }
+                    sw[0][i * NTR + t] = aw[i];
+                    sw[1][i * NTR + t] = ab[i];
+                }
+            }
+        }
+        __syncthreads();
+        if (sub) return;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            aw[i] += sw[0][i * NTR + t];
+            ab[i] += sw[1][i * NTR + t];
+        }
+    }
+    float* p = part + 2 * (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        Pack<float, VL> o;
+#pragma unroll
+        for (int e = 0; e < VL; ++e) o.v[e] = aw[n * VL + e];
+        store_vec<float, VL>(p, n * NTR + t, cols, o);
+#pragma unroll
+        for (int e = 0; e < VL; ++e) o.v[e] = ab[n * VL + e];
+        store_vec<float, VL>(p + cols, n * NTR + t, cols, o);
+    }
+}
+
+// The parts' sums: a workgroup takes 32 of the 2 cols columns, 32 threads each.
+constexpr int kJoinCols = 32, kJoinDeep = 32;
+__global__ __launch_bounds__(kJoinCols* kJoinDeep) void k_norm_join(const float* part, int64_t parts, int64_t cols,
+                                                                    float* dw, float* db, int add)
+{
+    __shared__ float tmp[kJoinDeep][kJoinCols];
+    const int tc = threadIdx.x % kJoinCols, td = threadIdx.x / kJoinCols;
+    const int64_t c = (int64_t)blockIdx.x * kJoinCols + tc;
+    float s = 0.f;
+    if (c < 2 * cols)
+        for (int64_t p = td; p < parts; p += kJoinDeep) s += part[2 * p * cols + c];
+    tmp[td][tc] = s;
+    __syncthreads();
+    if (td || c >= 2 * cols) return;
+#pragma unroll
+    for (int d = 1; d < kJoinDeep; ++d) s += tmp[d][tc];
+    float* out = c < cols ? dw : db;
+    const int64_t at = c < cols ? c : c - cols;
+    if (out) out[at] = add ? out[at] + s : s;
+}
+
+// ------------------------------------------------- rows that are not held
+constexpr int kLongThreads = 1024, kLongWaves = kLongThreads / 64;
 
 template <typename T, typename W>
-__global__ __launch_bounds__(kNormThreads) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
-                                                       int64_t ys, float* mean, float* rstd, int64_t rows, int64_t cols, float eps)
+__global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* x, int64_t xs, const W* w, const W* b, T* y,
+                                                            int64_t ys, float* mean, float* rstd, int64_t rows,
+                                                            int cols, float eps)
 {
-    __shared__ float tmp[kNormWaves];
+    __shared__ float tmp[kLongWaves];
     const int64_t r = row_of_block();
     if (r >= rows) return;
     const T* xr = x + r * xs;
     T* yr = y + r * ys;
     float s = 0.f;
-    for (int64_t c = threadIdx.x; c < cols; c += kNormThreads) s += to_f(xr[c]);
-    const float m = block_sum<kNormWaves>(s, tmp) / (float)cols;
+    for (int c = threadIdx.x; c < cols; c += kLongThreads) s += to_f(xr[c]);
+    const float m = block_sum<kLongWaves>(s, tmp) / (float)cols;
     float q = 0.f;
-    for (int64_t c = threadIdx.x; c < cols; c += kNormThreads) {
+    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
         const float d = to_f(xr[c]) - m;
         q = fmaf(d, d, q);
     }
-    const float rs = 1.0f / sqrtf(block_sum<kNormWaves>(q, tmp) / (float)cols + eps);
-    for (int64_t c = threadIdx.x; c < cols; c += kNormThreads) {
+    const float rs = 1.f / sqrtf(block_sum<kLongWaves>(q, tmp) / (float)cols + eps);
+    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
         const float h = (to_f(xr[c]) - m) * rs;
         yr[c] = from_f<T>(fmaf(h, w ? to_f(w[c]) : 1.f, b ? to_f(b[c]) : 0.f));
     }
@@ -40,36 +310,36 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(const T* x, int64_t xs, c
 }
 
 template <typename T, typename W>
-__global__ __launch_bounds__(kNormThreads) void k_norm_dx(const T* dy, int64_t dys, const T* x, int64_t xs, const W* w,
-                                                          const float* mean, const float* rstd, T* dx, int64_t dxs,
-                                                          int64_t rows, int64_t cols)
+__global__ __launch_bounds__(kLongThreads) void k_norm_long_dx(const T* dy, int64_t dys, const T* x, int64_t xs,
+                                                               const W* w, const float* mean, const float* rstd,
+                                                               T* dx, int64_t dxs, int64_t rows, int cols)
 {
-    __shared__ float tmp[kNormWaves];
+    __shared__ float tmp[kLongWaves];
     const int64_t r = row_of_block();
     if (r >= rows) return;
     const float m = mean[r], rs = rstd[r];
     float s1 = 0.f, s2 = 0.f;
-    for (int64_t c = threadIdx.x; c < cols; c += kNormThreads) {
+    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
         const float v = to_f(dy[r * dys + c]) * (w ? to_f(w[c]) : 1.f);
         s1 += v;
         s2 = fmaf(v, (to_f(x[r * xs + c]) - m) * rs, s2);
     }
-    const float c1 = block_sum<kNormWaves>(s1, tmp) / (float)cols;
-    const float c2 = block_sum<kNormWaves>(s2, tmp) / (float)cols;
-    for (int64_t c = threadIdx.x; c < cols; c += kNormThreads) {
+    const float c1 = block_sum<kLongWaves>(s1, tmp) / (float)cols;
+    const float c2 = block_sum<kLongWaves>(s2, tmp) / (float)cols;
+    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
         const float v = to_f(dy[r * dys + c]) * (w ? to_f(w[c]) : 1.f);
         const float h = (to_f(x[r * xs + c]) - m) * rs;
         dx[r * dxs + c] = from_f<T>(rs * (v - fmaf(h, c2, c1)));
     }
 }
 
-// Partial sums over the rows part, part + parts, ...
+// Sums over the rows part, part + parts, ... of 256 columns.
 template <typename T>
-__global__ __launch_bounds__(kNormThreads) void k_norm_dw(const T* dy, int64_t dys, const T* x, int64_t xs,
-                                                          const float* mean, const float* rstd, float* part,
-                                                          int64_t rows, int64_t cols)
+__global__ __launch_bounds__(256) void k_norm_long_dw(const T* dy, int64_t dys, const T* x, int64_t xs,
+                                                      const float* mean, const float* rstd, float* part, int64_t rows,
+                                                      int64_t cols)
 {
-    const int64_t c = (int64_t)blockIdx.x * kNormThreads + threadIdx.x;
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= cols) return;
     float aw = 0.f, ab = 0.f;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
@@ -77,22 +347,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_dw(const T* dy, int64_t d
         aw = fmaf(g, (to_f(x[r * xs + c]) - mean[r]) * rstd[r], aw);
         ab += g;
     }
-    part[(2 * (int64_t)blockIdx.y + 0) * cols + c] = aw;
+    part[2 * (int64_t)blockIdx.y * cols + c] = aw;
     part[(2 * (int64_t)blockIdx.y + 1) * cols + c] = ab;
-}
-
-__global__ __launch_bounds__(kNormThreads) void k_norm_join(const float* part, int64_t parts, int64_t cols, float* dw,
-                                                            float* db, int add)
-{
-    const int64_t c = (int64_t)blockIdx.x * kNormThreads + threadIdx.x;
-    if (c >= cols) return;
-    float aw = 0.f, ab = 0.f;
-    for (int64_t p = 0; p < parts; ++p) {
-        aw += part[(2 * p + 0) * cols + c];
-        ab += part[(2 * p + 1) * cols + c];
-    }
-    if (dw) dw[c] = add ? dw[c] + aw : aw;
-    if (db) db[c] = add ? db[c] + ab : ab;
 }
 
 constexpr int64_t kNormMaxCols = (int64_t)1 << 20;
@@ -104,37 +360,103 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
            std::isfinite(o->eps) && (o->flags & ~SGC_NORM_ADD_GRADS) == 0;
 }
 
-static int64_t norm_parts(const sgc_norm_opts* o) { return o->rows < 256 ? o->rows : 256; }
+// The shape of a workgroup for rows of `cols` held elements: 8 elements a
+// thread (16 for the longest rows), as few waves a row as that takes, at least
+// 4 waves.
+struct NormShape {
+    int nwr, ept, rpb;
+};
+static NormShape norm_shape(int64_t cols)
+{
+    int nwr = 1;
+    while (nwr < 16 && nwr * 512 < cols) nwr *= 2;
+    return {nwr, nwr * 512 < cols ? 16 : 8, nwr < 4 ? 4 / nwr : 1};
+}
+
+// Workgroups that share out the rows: `waves` of them a compute unit.
+static int64_t norm_groups(const sgc_norm_opts* o, int waves)
+{
+    const NormShape sh = norm_shape(o->cols);
+    const int64_t most = kCus * waves / (sh.nwr * sh.rpb), need = cdiv(o->rows, sh.rpb);
+    return need < most ? need : most;
+}
+constexpr int kForwardWaves = 32, kBackwardWaves = 16;
+
+static int64_t norm_parts(const sgc_norm_opts* o)
+{
+    if (o->cols <= kNormHeld) return norm_groups(o, kBackwardWaves);
+    return o->rows < 64 ? o->rows : 64;
+}
 
 template <typename T, typename W>
-static int norm_forward(const sgc_norm_opts* o, const void* x, int64_t xs, const void* w, const void* b, void* y,
+static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, const void* wv, const void* bv, void* yv,
                         int64_t ys, float* mean, float* rstd, hipStream_t s)
 {
-    k_norm<T, W><<<row_grid(o->rows), kNormThreads, 0, s>>>((const T*)x, xs, (const W*)w, (const W*)b, (T*)y, ys, mean,
-                                                            rstd, o->rows, o->cols, o->eps);
+    const T* x = (const T*)xv;
+    const W *w = (const W*)wv, *b = (const W*)bv;
+    T* y = (T*)yv;
+    const int cols = (int)o->cols;
+    if (cols > kNormHeld) {
+        k_norm_long<T, W><<<row_grid(o->rows), kLongThreads, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols,
+                                                                     o->eps);
+    } else {
+        const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
+#define SGC_NORM(NWR, EPT, RPB) \
+    k_norm<T, W, NWR, EPT, RPB><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols, o->eps)
+        const NormShape sh = norm_shape(cols);
+        if (sh.ept == 16) SGC_NORM(16, 16, 1);
+        else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
+        else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
+        else if (sh.nwr == 4) SGC_NORM(4, 8, 1);
+        else if (sh.nwr == 2) SGC_NORM(2, 8, 2);
+        else SGC_NORM(1, 8, 4);
+#undef SGC_NORM
+    }
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
 
 template <typename T, typename W>
-static int norm_backward(const sgc_norm_opts* o, const void* dy, int64_t dys, const void* x, int64_t xs, const void* w,
-                         const float* mean, const float* rstd, void* dx, int64_t dxs, float* dw, float* db, float* part,
-                         hipStream_t s)
+static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, const void* xv, int64_t xs,
+                         const void* wv, const float* mean, const float* rstd, void* dxv, int64_t dxs, float* dw,
+                         float* db, float* part, hipStream_t s)
 {
+    const T *dy = (const T*)dyv, *x = (const T*)xv;
+    const W* w = (const W*)wv;
+    T* dx = (T*)dxv;
+    const int cols = (int)o->cols;
     const int64_t parts = norm_parts(o);
-    const unsigned cb = (unsigned)cdiv(o->cols, kNormThreads);
-    if ((dw || db) && parts) {
-        k_norm_dw<T><<<dim3(cb, (unsigned)parts), kNormThreads, 0, s>>>((const T*)dy, dys, (const T*)x, xs, mean, rstd,
-                                                                       part, o->rows, o->cols);
+    if (!o->rows) {
+        // nothing to read
+    } else if (cols > kNormHeld) {
+        if (part) {  // before dx, which may take dy's or x's place
+            k_norm_long_dw<T><<<dim3((unsigned)cdiv(cols, 256), (unsigned)parts), 256, 0, s>>>(
+                dy, dys, x, xs, mean, rstd, part, o->rows, cols);
+            SGC_LAUNCH_CHECK();
+        }
+        if (dx) {
+            k_norm_long_dx<T, W><<<row_grid(o->rows), kLongThreads, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs,
+                                                                            o->rows, cols);
+            SGC_LAUNCH_CHECK();
+        }
+    } else if (dx || part) {
+        const unsigned g = (unsigned)parts;
+#define SGC_NORM(NWR, EPT, RPB)                                                                               \
+    k_norm_back<T, W, NWR, EPT, RPB><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, part, \
+                                                                  o->rows, cols)
+        const NormShape sh = norm_shape(cols);
+        if (sh.ept == 16) SGC_NORM(16, 16, 1);
+        else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
+        else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
+        else if (sh.nwr == 4) SGC_NORM(4, 8, 1);
+        else if (sh.nwr == 2) SGC_NORM(2, 8, 2);
+        else SGC_NORM(1, 8, 4);
+#undef SGC_NORM
         SGC_LAUNCH_CHECK();
     }
-    if (dx && o->rows) {
-        k_norm_dx<T, W><<<row_grid(o->rows), kNormThreads, 0, s>>>((const T*)dy, dys, (const T*)x, xs, (const W*)w,
-                                                                   mean, rstd, (T*)dx, dxs, o->rows, o->cols);
-        SGC_LAUNCH_CHECK();
-    }
-    if (dw || db) {
-        k_norm_join<<<cb, kNormThreads, 0, s>>>(part, parts, o->cols, dw, db, o->flags & SGC_NORM_ADD_GRADS);
+    if (part) {
+        k_norm_join<<<(unsigned)cdiv(2 * o->cols, kJoinCols), kJoinCols * kJoinDeep, 0, s>>>(
+            part, parts, o->cols, dw, db, o->flags & SGC_NORM_ADD_GRADS);
         SGC_LAUNCH_CHECK();
     }
     return SGC_OK;

@@ -53,17 +53,38 @@ inline dim3 row_grid(int64_t n)
 __device__ inline int64_t row_of_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // ------------------------------------------------------- block reductions
+// Over a wave by data-parallel moves inside the vector unit (shifts in rows of
+// 16 lanes, then rows 0 and 2 into 1 and 3, then the lower half into the
+// upper): lane 63 has seen every lane.  No trip through shared memory, which
+// a shuffle makes.  The steps' lanes without a source add 0, or keep their own.
+template <int CTRL, int ROWS>
+__device__ inline float dpp_or(float old, float x)
+{
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ inline float last_lane(float x) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63)); }
+
+// Every lane of the wave must be active.
 __device__ inline float wave_sum(float x)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
-    return x;
+    x += dpp_or<0x111, 0xf>(0.f, x);
+    x += dpp_or<0x112, 0xf>(0.f, x);
+    x += dpp_or<0x114, 0xf>(0.f, x);
+    x += dpp_or<0x118, 0xf>(0.f, x);
+    x += dpp_or<0x142, 0xa>(0.f, x);
+    x += dpp_or<0x143, 0xc>(0.f, x);
+    return last_lane(x);
 }
 __device__ inline float wave_max(float x)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
-    return x;
+    x = fmaxf(x, dpp_or<0x111, 0xf>(x, x));
+    x = fmaxf(x, dpp_or<0x112, 0xf>(x, x));
+    x = fmaxf(x, dpp_or<0x114, 0xf>(x, x));
+    x = fmaxf(x, dpp_or<0x118, 0xf>(x, x));
+    x = fmaxf(x, dpp_or<0x142, 0xa>(x, x));
+    x = fmaxf(x, dpp_or<0x143, 0xc>(x, x));
+    return last_lane(x);
 }
 
 // Sum over a workgroup of NW waves, the same value in every thread; tmp
