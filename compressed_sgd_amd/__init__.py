@@ -145,8 +145,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device: torch.device, stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return C.c_void_p(s.cuda_stream)
+    if stream is None:
+        # the current stream's handle without the Stream object around it (0.1 against 2 us a call)
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return C.c_void_p(stream.cuda_stream)
 
 
 def _on(stream):
@@ -267,8 +269,8 @@ def workspace(nbytes: int, device: torch.device, slot: str = "default", stream=N
         raise RuntimeError("a call captured into a graph needs its own workspace: pass ws= "
                            "(sized with the *_workspace_bytes helpers)")
     index = device.index if device.index is not None else torch.cuda.current_device()
-    s = stream if stream is not None else torch.cuda.current_stream(index)
-    key = (index, int(s.cuda_stream), slot)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
+    key = (index, handle, slot)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         _ws_cache.pop(key, None)

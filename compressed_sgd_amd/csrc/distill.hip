@@ -187,6 +187,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     extern __shared__ uint32_t bm[];
     __shared__ Entries en;
     __shared__ float tmp[NW];
+    __shared__ float tmj[NW][3];
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
     const T* zr = z + r * a.zs;
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     const bool bad = mark_entries<NW>(en, a, 0, a.vocab, bm);
     SoftSum sum;
     stream_sums<T, NW * 64, 4, false, TAIL>(zr, a.vocab, a.c, bm, sum);
-    block_join<NW, false>(sum, a.c, tmp);
+    block_join<NW, false>(sum, a.c, tmj);
     const float base = finite_base(sum.m);
     float s = sum.s, o = sum.s;
     if (TAIL) {
@@ -217,6 +218,151 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     write_gradient<T, NW, 4>(en, a, zr, out, 0, a.vocab, base, k_out, k_in, k_t);
 }
 
+// The held vectors are the same 16 bytes after this, but the compiler does not
+// know it: else it keeps the elements that it unpacked to fp32 for the next
+// pass, in twice the registers.
+template <int NV>
+__device__ inline void keep_packed(Raw (&q)[NV])
+{
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(q[n].w[i]));
+}
+
+// A row a workgroup with loss and gradient in one reading: NV vectors of the
+// row stay in each thread's registers from the sums to the gradient (a vector
+// past the row is -inf).  One entry a thread.  The exponent is one fma,
+// z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
+// which the sums are freed from once a row.  A maximum so large that M c
+// leaves fp32 (rows that a mask at the type's lowest value leaves nothing but
+// itself) takes z - M first.
+template <typename T, int NW, int NV, bool TAIL>
+__global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T* z, T* dz)
+{
+    constexpr int NT = NW * 64, VL = VecLen<T>::value;
+    static_assert(NT >= SGC_TOP_MAX, "one entry a thread");
+    extern __shared__ uint32_t bm[];
+    __shared__ float tmp[NW];
+    const int64_t r = row_of_block();
+    if (r >= a.rows) return;
+    const T* zr = z + r * a.zs;
+    const int tid = threadIdx.x, nv = a.vocab / VL;
+    const float g = a.dloss ? a.dloss[r] : 1.f;
+    int32_t at = -1;
+    float v = -INFINITY;
+    if (tid < a.top) {
+        at = a.idx[r * a.top + tid];
+        v = a.val[r * a.top + tid] * a.teacher_scale;
+    }
+    Raw q[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) q[n] = tid + n * NT < nv ? ((const Raw*)zr)[tid + n * NT] : raw_low<T>();
+    const int last = nv * VL + tid;
+    const float z_last = last < a.vocab ? to_f(zr[last]) : -INFINITY;
+    // the entries: marks, T and u
+    const bool in_row = at >= 0 && at < a.vocab;
+    const float z_in = in_row ? to_f(zr[at]) : -INFINITY;
+    if (!in_row) v = -INFINITY;
+    for (int w = tid; w < (a.vocab + 31) / 32; w += NT) bm[w] = 0;
+    __syncthreads();
+    int bad = at < -1 || at >= a.vocab;
+    if (in_row) bad |= (atomicOr(&bm[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u;
+    bad = __syncthreads_or(bad);
+    float lt = v, total, u = 0.f;
+    if (TAIL) {
+        total = block_sum<NW>(expf(lt), tmp);
+        u = fmaxf(0.f, 1.f - total);
+    } else {
+        const float base = finite_base(block_max<NW>(v, tmp));
+        const float sum = block_sum<NW>(expf(v - base), tmp);
+        lt = (v - base) - (sum == 0.f ? 0.f : logf(sum));
+        total = sum == 0.f ? 0.f : sum != sum ? sum : 1.f;
+    }
+    const float t = expf(lt);
+    // the row's maximum and sums
+    float m = z_last;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        float x[VL];
+        unpack<T>(q[n], x);
+#pragma unroll
+        for (int e = 0; e < VL; ++e) m = fmaxf(m, x[e]);
+    }
+    m = block_max<NW>(m, tmp);
+    keep_packed(q);
+    const float base = finite_base(m), b = base * a.c;
+    const bool far = !(fabsf(b) < 1e30f);
+    const auto power = [&](float x) { return exp2_fast(far ? (x - base) * a.c : fmaf(x, a.c, -b)); };
+    float o = 0.f, o2 = 0.f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        float x[VL];
+        unpack<T>(q[n], x);
+        if (TAIL) {
+            const uint32_t skip = tid + n * NT < nv ? vec_bits<VL>(bm, tid + n * NT) : 0u;
+            if (skip) {
+#pragma unroll
+                for (int e = 0; e < VL; ++e) x[e] = (skip >> e) & 1u ? -INFINITY : x[e];
+            }
+        }
+        if (far) {
+#pragma unroll
+            for (int e = 0; e < VL; ++e) (e & 1 ? o2 : o) += exp2_fast((x[e] - base) * a.c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VL; ++e) (e & 1 ? o2 : o) += exp2_fast(fmaf(x[e], a.c, -b));
+        }
+    }
+    if (last < a.vocab && !(TAIL && (bm[last >> 5] >> (last & 31)) & 1u)) o += power(z_last);
+    keep_packed(q);
+    o = block_sum<NW>(o + o2, tmp);
+    const float e_in = power(z_in);
+    float s = o;
+    if (TAIL) s += block_sum<NW>(in_row ? e_in : 0.f, tmp);
+    // loss: ln s of the sum freed from 2^(M c - b)
+    const float free = far ? 1.f : exp2_fast(-fmaf(base, a.c, -b));
+    const float ln_s = logf(s * free);
+    float l = block_sum<NW>(t != 0.f ? t * (lt - ((z_in - base) * a.scale - ln_s)) : 0.f, tmp);
+    if (u > 0.f && o != 0.f) l += u * (logf(u) - (logf(o) - logf(s)));
+    const bool skip = bad || s == 0.f || (!TAIL && total == 0.f);
+    if (tid == 0) {
+        a.loss[r] = bad ? NAN : skip ? 0.f : l;
+        if (a.stats) {
+            a.stats[4 * r] = m;
+            a.stats[4 * r + 1] = s * free;
+            a.stats[4 * r + 2] = o * free;
+            a.stats[4 * r + 3] = skip ? 0.f : 1.f;
+        }
+        if (bad && a.dstatus) atomicOr(a.dstatus, SGC_STATUS_CORRUPT);
+    }
+    T* out = dz + r * a.dzs;
+    if (skip || g == 0.f) {
+        write_zeros<T, NW>(out, 0, a.vocab);
+        return;
+    }
+    float k_out, k_in, k_t;
+    factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        if (tid + n * NT < nv) {
+            float x[VL];
+            unpack<T>(q[n], x);
+            if (far) {
+#pragma unroll
+                for (int e = 0; e < VL; ++e) x[e] = exp2_fast((x[e] - base) * a.c) * k_out;
+            } else {
+#pragma unroll
+                for (int e = 0; e < VL; ++e) x[e] = exp2_fast(fmaf(x[e], a.c, -b)) * k_out;
+            }
+            ((Raw*)out)[tid + n * NT] = pack<T>(x);
+        }
+    }
+    if (last < a.vocab) out[last] = from_f<T>(power(z_last) * k_out);
+    __syncthreads();
+    if (in_row) out[at] = from_f<T>(e_in * k_in - t * k_t);
+}
+
 // A chunk of a row: its maximum, sum outside the entries, sum of the entries,
 // and whether one is bad.  part [rows, chunks, 4].
 template <typename T, int NW, bool TAIL>
@@ -226,6 +372,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T
     extern __shared__ uint32_t bm[];
     __shared__ Entries en;
     __shared__ float tmp[NW];
+    __shared__ float tmj[NW][3];
     const int64_t b = row_of_block(), r = b / chunks;
     if (r >= a.rows) return;
     const int z0 = (int)(b - r * chunks) * chunk, z1 = a.vocab - z0 < chunk ? a.vocab : z0 + chunk;
@@ -238,7 +385,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T
     const bool bad = mark_entries<NW>(en, a, z0, z1, bm);
     SoftSum sum;
     stream_sums<T, NW * 64, 4, false, TAIL>(zr + z0, z1 - z0, a.c, bm, sum);
-    block_join<NW, false>(sum, a.c, tmp);
+    block_join<NW, false>(sum, a.c, tmj);
     float in = 0.f;
     if (TAIL) {
         for (int j = threadIdx.x; j < a.top; j += NW * 64)
@@ -379,8 +526,19 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
     const dim3 rows = row_grid(a.rows);
     if (chunks == 1) {
         const size_t lds = (size_t)(a.vocab + 31) / 32 * 4;
+        const int nv = a.vocab / VecLen<T>::value;
         if (a.vocab <= 2048)
             k_distill_row<T, 1, TAIL><<<rows, 64, lds, s>>>(a, z, dz);
+        else if (dz && nv <= 1024)
+            k_distill_held<T, 4, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
+        else if (dz && nv <= 2048)
+            k_distill_held<T, 4, 8, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
+        else if (dz && nv <= 4096)
+            k_distill_held<T, 8, 8, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+        else if (dz && nv <= 8192)
+            k_distill_held<T, 8, 16, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+        else if (dz && nv <= 16384)
+            k_distill_held<T, 16, 16, TAIL><<<rows, 1024, lds, s>>>(a, z, dz);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
         else

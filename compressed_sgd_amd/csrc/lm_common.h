@@ -43,6 +43,56 @@ struct VecLen {
     static constexpr int value = 16 / (int)sizeof(T);
 };
 
+// 16 bytes of a row as four words, which stay packed in registers, and their
+// elements as fp32.
+struct __attribute__((packed, aligned(2))) Raw {
+    uint32_t w[4];
+};
+template <typename T>
+__device__ inline void unpack(const Raw& q, float* x)
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(q.w[i]);
+    } else if constexpr (__is_same(T, bf16_t)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(q.w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(q.w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = (float)__builtin_bit_cast(f16_t, (uint16_t)q.w[i]);
+            x[2 * i + 1] = (float)__builtin_bit_cast(f16_t, (uint16_t)(q.w[i] >> 16));
+        }
+    }
+}
+template <typename T>
+__device__ inline Raw pack(const float* x)
+{
+    Raw q;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.w[i] = __float_as_uint(x[i]);
+    } else {
+        typedef T Two __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Two t = {from_f<T>(x[2 * i]), from_f<T>(x[2 * i + 1])};
+            q.w[i] = __builtin_bit_cast(uint32_t, t);
+        }
+    }
+    return q;
+}
+// -inf in every element.
+template <typename T>
+__device__ inline Raw raw_low()
+{
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : __is_same(T, bf16_t) ? 0xff80ff80u : 0xfc00fc00u;
+    return {{w, w, w, w}};
+}
+
 // One workgroup for each of n < 2^31 rows: a grid of at most 2^20 x 2^11
 // (a launch holds fewer than 2^32 threads in x); the last ones past n.
 inline dim3 row_grid(int64_t n)

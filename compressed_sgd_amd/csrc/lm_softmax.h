@@ -107,16 +107,41 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
     }
 }
 
-// The threads' sums joined: the same values in every thread.
+// The threads' sums joined: the same values in every thread.  Each wave joins
+// its own, then all threads the waves': one barrier, and one after, so that
+// tmp may be used again.
 template <int NW, bool ENT>
-__device__ inline void block_join(SoftSum& a, float c, float* tmp)
+__device__ inline void block_join(SoftSum& a, float c, float (*tmp)[3])
 {
-    const float m = block_max<NW>(a.m, tmp);
-    const float d = fmaxf((a.m - finite_base(m)) * c, kLowD);
+    const float wm = wave_max(a.m);
+    const float d = fmaxf((a.m - finite_base(wm)) * c, kLowD);
     const float f = exp2_fast(d);
-    if (ENT) a.t = block_sum<NW>(fmaf(d, a.s, a.t) * f, tmp);
-    a.s = block_sum<NW>(a.s * f, tmp);
+    float t = ENT ? wave_sum(fmaf(d, a.s, a.t) * f) : 0.f;
+    float s = wave_sum(a.s * f);
+    float m = wm;
+    if (NW > 1) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            tmp[w][0] = wm;
+            tmp[w][1] = s;
+            tmp[w][2] = t;
+        }
+        __syncthreads();
+        m = tmp[0][0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) m = fmaxf(m, tmp[i][0]);
+        s = t = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const float di = fmaxf((tmp[i][0] - finite_base(m)) * c, kLowD), fi = exp2_fast(di);
+            s += tmp[i][1] * fi;
+            if (ENT) t += fmaf(di, tmp[i][1], tmp[i][2]) * fi;
+        }
+        __syncthreads();
+    }
     a.m = m;
+    a.s = s;
+    a.t = t;
 }
 
 }  // namespace sgc

@@ -52,6 +52,7 @@ struct Candidates {
     uint32_t peak[NT];  // the threads' maxima as order keys, then the threads that hold candidates
     int n, threads;
     uint32_t bar;
+    uint64_t floor;
 };
 
 // sorted[0 .. min(n, top)) = the largest of key[0 .. n), largest first: each
@@ -62,7 +63,7 @@ __device__ inline void rank_keys(Candidates<NW>& cd, int n, int top)
     for (int i = threadIdx.x; i < n; i += NW * 64) {
         const uint64_t k = cd.key[i];
         int place = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j) place += cd.key[j] > k;
         if (place < top) cd.sorted[place] = k;
     }
@@ -73,7 +74,7 @@ __device__ inline void rank_keys(Candidates<NW>& cd, int n, int top)
 // cut to its best, whose last key later elements have to pass.  For rows with
 // NaN or +inf, or with so many equal values that the filter lets too many
 // through.  Returns how many there are (less than top in a short row).
-template <typename K, int NW>
+template <int NW, typename K>
 __device__ inline int top_in_order(Candidates<NW>& cd, const K& key_at, int len, int top)
 {
     constexpr int NT = NW * 64;
@@ -166,7 +167,7 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
         }
         __syncthreads();
     }
-    return top_in_order<decltype(key_at), NW>(cd, key_at, len, top);
+    return top_in_order<NW>(cd, key_at, len, top);
 }
 
 // What a row's sums give: logp, entropy, stats; ln s and the base of y.
@@ -203,7 +204,7 @@ template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)
 {
     __shared__ Candidates<NW> cd;
-    __shared__ float tmp[NW];
+    __shared__ float tmp[NW][3];
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
     const T* zr = z + r * a.zs;
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, 
                                                      uint64_t* keys)
 {
     __shared__ Candidates<NW> cd;
-    __shared__ float tmp[NW];
+    __shared__ float tmp[NW][3];
     const int64_t b = row_of_block(), r = b / chunks;
     if (r >= a.rows) return;
     const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
@@ -252,15 +253,14 @@ __global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, 
     }
 }
 
-// The chunks of a row joined.  The best keys of all chunks are cut to `top` as
-// a row's elements are: by the threads' largest, on the keys' upper half.
+// The chunks of a row joined.
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, int chunks, const float* part,
                                                      const uint64_t* keys)
 {
     constexpr int NT = NW * 64;
     __shared__ Candidates<NW> cd;
-    __shared__ float tmp[NW];
+    __shared__ float tmp[NW][3];
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
     int64_t tok = -1;
@@ -286,17 +286,38 @@ __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, 
     const float ln_s = logf(sum.s);
     if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
     if (!a.top) return;
+    // Each chunk has `top` keys that reach its last one (0 where it is short):
+    // keys below the largest of the chunks' last keys are not among the best.
     const uint64_t* kr = keys + r * chunks * a.top;
     const int len = chunks * a.top;
-    const auto key_at = [&](int i) { return kr[i]; };
-    int n;
-    if (len <= cd.kCap) {
-        for (int i = threadIdx.x; i < len; i += NT) cd.key[i] = kr[i];
-        __syncthreads();
-        rank_keys<NW>(cd, len, a.top);
-        n = a.top;
+    uint64_t bar = 0;
+    for (int k = threadIdx.x; k < chunks; k += NT) {
+        const uint64_t last = kr[(int64_t)(k + 1) * a.top - 1];
+        bar = bar > last ? bar : last;
+    }
+    if (threadIdx.x == 0) {
+        cd.n = 0;
+        cd.floor = 0;
+    }
+    __syncthreads();
+    if (bar) atomicMax((unsigned long long*)&cd.floor, (unsigned long long)bar);
+    __syncthreads();
+    bar = cd.floor;
+    for (int i = threadIdx.x; i < len; i += NT) {
+        const uint64_t k = kr[i];
+        if (k && k >= bar) {
+            const int at = atomicAdd(&cd.n, 1);
+            if (at < cd.kCap) cd.key[at] = k;
+        }
+    }
+    __syncthreads();
+    int n = cd.n;
+    if (n <= cd.kCap) {
+        rank_keys<NW>(cd, n, a.top);
+        n = n < a.top ? n : a.top;
     } else {
-        n = top_in_order<decltype(key_at), NW>(cd, key_at, len, a.top);
+        __syncthreads();
+        n = top_in_order<NW>(cd, [&](int i) { return kr[i]; }, len, a.top);
     }
     for (int k = threadIdx.x; k < n; k += NT) write_top(a, r, k, cd.sorted[k], sum, ln_s);
 }
@@ -437,7 +458,7 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     else
         k_lp_part<T, 8><<<parts, 512, 0, s>>>(a, z, chunk, used, part, keys);
     SGC_LAUNCH_CHECK();
-    k_lp_join<T, 8><<<rows, 512, 0, s>>>(a, z, used, part, keys);
+    k_lp_join<T, 4><<<rows, 256, 0, s>>>(a, z, used, part, keys);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }

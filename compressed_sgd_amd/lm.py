@@ -15,7 +15,7 @@ from typing import Optional
 
 import torch
 
-from . import SGCError, _check, _empty, _ptr, _stream, lib, workspace
+from . import SGCError, _check, _on, _ptr, _stream, lib, workspace
 
 F32, BF16, F16 = 0, 1, 2
 NORM_ADD_GRADS = 1
@@ -58,26 +58,30 @@ def _declare(L) -> None:
         f.argtypes, f.restype = args, res
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
     """Checks a 2-D device tensor of rows; its row stride."""
-    _need(t.is_cuda, f"{name} must be a device (HIP) tensor")
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{name} must be 2-D with contiguous rows")
-    _need(t.dtype in _DTYPES, f"{name} must be float32, bfloat16 or float16")
-    if like is not None:
-        _need(t.shape == like.shape and t.dtype == like.dtype and t.device == like.device,
-              f"{name} must match the input's shape, type and device")
-    return t.stride(0)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (HIP) tensor")
+    if t.dim() != 2 or t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be 2-D float32, bfloat16 or float16")
+    stride = t.stride()
+    if stride[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match the input's shape, type and device")
+    return stride[0]
 
 
 def _vec(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> None:
     """Checks a contiguous operand of a known shape, type and device (None passes)."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
-                          or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -109,10 +113,11 @@ class NormGrads:
 
 
 def _affine(weight, bias, x) -> int:
-    wdt = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
-    _need(wdt in (torch.float32, x.dtype), "weight and bias must be float32 or the type of x")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _vec(t, name, (x.shape[1],), wdt, x.device)
+    wdt = weight.dtype if weight is not None else bias.dtype if bias is not None else torch.float32
+    if wdt != torch.float32 and wdt != x.dtype:
+        raise ValueError("weight and bias must be float32 or the type of x")
+    _vec(weight, "weight", x.shape[1:], wdt, x.device)
+    _vec(bias, "bias", x.shape[1:], wdt, x.device)
     return _DTYPES[wdt]
 
 
@@ -123,10 +128,12 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     wdt = _affine(weight, bias, x)
     rows, cols = x.shape
     dev = x.device
-    y = _empty(stream, rows, cols, dtype=x.dtype, device=dev) if out is None else out
-    ys = _rows(y, "out", x)
-    st = _empty(stream, 2, rows, dtype=torch.float32, device=dev)
-    mean, rstd = st[0], st[1]
+    if out is None:
+        y, ys = _empty(stream, (rows, cols), x.dtype, dev), cols
+    else:
+        y, ys = out, _rows(out, "out", x)
+    mean = _empty(stream, (rows,), torch.float32, dev)
+    rstd = _empty(stream, (rows,), torch.float32, dev)
     o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, eps, 0)
     _check(lib().sgc_layer_norm(C.byref(o), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean),
                                 _ptr(rstd), _stream(dev, stream)), "sgc_layer_norm")
@@ -153,14 +160,15 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (dweight, "dweight", cols),
                        (dbias, "dbias", cols)):
         _vec(t, name, (n,), torch.float32, dev)
-    _need(not accumulate or (dweight is not None and dbias is not None), "accumulate needs dweight and dbias")
+    if accumulate and (dweight is None or dbias is None):
+        raise ValueError("accumulate needs dweight and dbias")
     if dx is None and want_dx:
-        dx = _empty(stream, rows, cols, dtype=x.dtype, device=dev)
+        dx = _empty(stream, (rows, cols), x.dtype, dev)
     dxs = _rows(dx, "dx", x) if dx is not None else 0
     if dweight is None:
-        dweight = _empty(stream, cols, dtype=torch.float32, device=dev)
+        dweight = _empty(stream, (cols,), torch.float32, dev)
     if dbias is None:
-        dbias = _empty(stream, cols, dtype=torch.float32, device=dev)
+        dbias = _empty(stream, (cols,), torch.float32, dev)
     o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
     need = lib().sgc_layer_norm_backward_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "layer_norm", stream, "sgc_layer_norm_backward_workspace")
@@ -184,7 +192,8 @@ class TokenLogprobs:
 def _tokens(tokens: Optional[torch.Tensor], logits: torch.Tensor) -> int:
     if tokens is None:
         return TOKEN_I64
-    _need(tokens.dtype in (torch.int32, torch.int64), "tokens must be int32 or int64")
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise ValueError("tokens must be int32 or int64")
     _vec(tokens, "tokens", (logits.shape[0],), tokens.dtype, logits.device)
     return TOKEN_I64 if tokens.dtype == torch.int64 else TOKEN_I32
 
@@ -211,11 +220,10 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     _status(status, dev)
     f32 = torch.float32
     if out is None:
-        out = TokenLogprobs(None if tokens is None else _empty(stream, rows, dtype=f32, device=dev),
-                            _empty(stream, rows, dtype=f32, device=dev),
-                            _empty(stream, rows, 2, dtype=f32, device=dev),
-                            _empty(stream, rows, top, dtype=torch.int32, device=dev) if top > 0 else None,
-                            _empty(stream, rows, top, dtype=f32, device=dev) if top > 0 else None)
+        out = TokenLogprobs(None if tokens is None else _empty(stream, (rows,), f32, dev),
+                            _empty(stream, (rows,), f32, dev), _empty(stream, (rows, 2), f32, dev),
+                            _empty(stream, (rows, top), torch.int32, dev) if top > 0 else None,
+                            _empty(stream, (rows, top), f32, dev) if top > 0 else None)
     else:
         for t, name, shape, dt in ((out.logp, "out.logp", (rows,), f32), (out.entropy, "out.entropy", (rows,), f32),
                                    (out.stats, "out.stats", (rows, 2), f32),
@@ -246,7 +254,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor]
     for t, name in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
         _vec(t, name, (rows,), f32, dev)
     if dlogits is None:
-        dlogits = _empty(stream, rows, vocab, dtype=logits.dtype, device=dev)
+        dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
     ds = _rows(dlogits, "dlogits", logits)
     o = LogprobOpts(rows, vocab, _DTYPES[logits.dtype], tt, 0, scale)
     _check(lib().sgc_token_logprobs_backward(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(stats), _ptr(entropy),
@@ -264,7 +272,8 @@ class Distilled:
 
 
 def _entries(t_idx: torch.Tensor, t_val: torch.Tensor, logits: torch.Tensor) -> int:
-    _need(t_idx.dim() == 2, "t_idx must be 2-D [rows, top]")
+    if t_idx.dim() != 2:
+        raise ValueError("t_idx must be 2-D [rows, top]")
     shape = (logits.shape[0], t_idx.shape[1])
     _vec(t_idx, "t_idx", shape, torch.int32, logits.device)
     _vec(t_val, "t_val", shape, torch.float32, logits.device)
@@ -294,10 +303,10 @@ def distill(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Tensor, *, m
     _status(status, dev)
     _vec(dloss, "dloss", (rows,), torch.float32, dev)
     if dlogits is None and dloss is not None:
-        dlogits = _empty(stream, rows, vocab, dtype=logits.dtype, device=dev)
+        dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
     ds = _rows(dlogits, "dlogits", logits) if dlogits is not None else 0
-    loss = _empty(stream, rows, dtype=torch.float32, device=dev)
-    stats = _empty(stream, rows, 4, dtype=torch.float32, device=dev)
+    loss = _empty(stream, (rows,), torch.float32, dev)
+    stats = _empty(stream, (rows, 4), torch.float32, dev)
     o = DistillOpts(rows, vocab, _DTYPES[logits.dtype], top, mode, scale, teacher_scale, 0)
     need = lib().sgc_distill_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "distill", stream, "sgc_distill")
@@ -319,7 +328,7 @@ def distill_backward(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Ten
     _vec(stats, "stats", (rows, 4), torch.float32, dev)
     _vec(dloss, "dloss", (rows,), torch.float32, dev)
     if dlogits is None:
-        dlogits = _empty(stream, rows, vocab, dtype=logits.dtype, device=dev)
+        dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
     ds = _rows(dlogits, "dlogits", logits)
     o = DistillOpts(rows, vocab, _DTYPES[logits.dtype], top, mode, scale, teacher_scale, 0)
     _check(lib().sgc_distill_backward(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(stats),
