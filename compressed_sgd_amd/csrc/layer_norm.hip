@@ -17,29 +17,35 @@ namespace sgc {
 
 constexpr int64_t kNormHeld = 16384;
 constexpr int64_t kCus = 256;
+// Waves that a compute unit holds of the forward and the backward kernel.
+constexpr int kForwardWaves = 32, kBackwardWaves = 16;
 
-// Elements [v VL, v VL + VL) of a row that end at cols; past it 0.
-template <typename T, int VL>
-__device__ inline Pack<T, VL> load_vec(const T* p, int v, int cols)
+// Elements [v VL, v VL + VL) of a row that ends at cols; past it 0.  RAG: cols
+// is no multiple of VL.
+template <typename T, bool RAG>
+__device__ inline Raw load_raw(const T* p, int v, int cols)
 {
-    Pack<T, VL> q;
-    if ((v + 1) * VL <= cols) {
-        q = ((const Pack<T, VL>*)p)[v];
-    } else {
+    constexpr int VL = VecLen<T>::value;
+    if ((v + 1) * VL <= cols) return ((const Raw*)p)[v];
+    Raw q = {{0, 0, 0, 0}};
+    if (RAG && v * VL < cols) {
+        float x[VL];
 #pragma unroll
-        for (int e = 0; e < VL; ++e) q.v[e] = v * VL + e < cols ? p[v * VL + e] : (T)0.f;
+        for (int e = 0; e < VL; ++e) x[e] = v * VL + e < cols ? to_f(p[v * VL + e]) : 0.f;
+        q = pack<T>(x);
     }
     return q;
 }
-template <typename T, int VL>
-__device__ inline void store_vec(T* p, int v, int cols, const Pack<T, VL>& q)
+template <typename T, bool RAG>
+__device__ inline void store_raw(T* p, int v, int cols, const float* x)
 {
+    constexpr int VL = VecLen<T>::value;
     if ((v + 1) * VL <= cols) {
-        ((Pack<T, VL>*)p)[v] = q;
-    } else {
+        ((Raw*)p)[v] = pack<T>(x);
+    } else if (RAG && v * VL < cols) {
 #pragma unroll
         for (int e = 0; e < VL; ++e)
-            if (v * VL + e < cols) p[v * VL + e] = q.v[e];
+            if (v * VL + e < cols) p[v * VL + e] = from_f<T>(x[e]);
     }
 }
 // EPT columns of a thread's weights as fp32; `none` where there are none.
@@ -49,14 +55,8 @@ __device__ inline void load_weights(const W* w, int t, int cols, float none, flo
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int v = n * NTR + t;
-        if (w) {
-            const Pack<W, VL> q = load_vec<W, VL>(w, v, cols);
 #pragma unroll
-            for (int e = 0; e < VL; ++e) out[n * VL + e] = to_f(q.v[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VL; ++e) out[n * VL + e] = none;
-        }
+        for (int e = 0; e < VL; ++e) out[n * VL + e] = w && v * VL + e < cols ? to_f(w[v * VL + e]) : none;
     }
 }
 
@@ -74,42 +74,36 @@ __device__ inline void row_sums(float& a, float& b, float (*tmp)[RPB][NWR][2], i
         tmp[turn][sub][w][1] = b;
     }
     __syncthreads();
-    a = b = 0.f;
-#pragma unroll
-    for (int i = 0; i < NWR; ++i) {
-        a += tmp[turn][sub][i][0];
-        b += tmp[turn][sub][i][1];
-    }
+    a = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][0]);
+    b = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][1]);
 }
 
-template <typename T, typename W, int NWR, int EPT, int RPB>
+template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG>
 __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
                                                         int64_t ys, float* mean, float* rstd, int64_t rows, int cols,
                                                         float eps)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
     __shared__ float tmp[2][RPB][NWR][2];
-    const int sub = threadIdx.x / NTR, t = threadIdx.x % NTR;
+    const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / NTR), t = threadIdx.x % NTR;
     float wf[EPT], bf[EPT];
     load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
     load_weights<W, VL, NV, NTR>(b, t, cols, 0.f, bf);
     const float inv = 1.f / (float)cols;
-    Pack<T, VL> next[NV] = {};
+    Raw next[NV] = {};
     int64_t r = (int64_t)blockIdx.x * RPB + sub;
     const int64_t step = (int64_t)gridDim.x * RPB;
     if (r < rows) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) next[n] = load_vec<T, VL>(x + r * xs, n * NTR + t, cols);
+        for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG>(x + r * xs, n * NTR + t, cols);
     }
     for (; r - sub < rows; r += step) {
         float f[EPT];
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int e = 0; e < VL; ++e) f[n * VL + e] = to_f(next[n].v[e]);
+        for (int n = 0; n < NV; ++n) unpack<T>(next[n], f + n * VL);
         if (r + step < rows) {
 #pragma unroll
-            for (int n = 0; n < NV; ++n) next[n] = load_vec<T, VL>(x + (r + step) * xs, n * NTR + t, cols);
+            for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG>(x + (r + step) * xs, n * NTR + t, cols);
         }
         float s = 0.f, q = 0.f, none = 0.f;
 #pragma unroll
@@ -127,15 +121,9 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
         const float rs = 1.f / sqrtf(q / (float)cols + eps);
         if (r < rows) {
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                Pack<T, VL> o;
+            for (int i = 0; i < EPT; ++i) f[i] = fmaf(f[i] * rs, wf[i], bf[i]);
 #pragma unroll
-                for (int e = 0; e < VL; ++e) {
-                    const int i = n * VL + e;
-                    o.v[e] = from_f<T>(fmaf(f[i] * rs, wf[i], bf[i]));
-                }
-                store_vec<T, VL>(y + r * ys, n * NTR + t, cols, o);
-            }
+            for (int n = 0; n < NV; ++n) store_raw<T, RAG>(y + r * ys, n * NTR + t, cols, f + n * VL);
             if (t == 0) {
                 if (mean) mean[r] = m;
                 if (rstd) rstd[r] = rs;
@@ -146,27 +134,27 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
 
 // dx, and the workgroup's sums of dy xh and dy over its rows: part
 // [workgroups, 2, cols].
-template <typename T, typename W, int NWR, int EPT, int RPB>
-__global__ __launch_bounds__(NWR* RPB * 64) void k_norm_back(const T* dy, int64_t dys, const T* x, int64_t xs,
+template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG>
+__global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) void k_norm_back(const T* dy, int64_t dys, const T* x, int64_t xs,
                                                              const W* w, const float* mean, const float* rstd, T* dx,
                                                              int64_t dxs, float* part, int64_t rows, int cols)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
     __shared__ float tmp[2][RPB][NWR][2];
-    const int sub = threadIdx.x / NTR, t = threadIdx.x % NTR;
+    const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / NTR), t = threadIdx.x % NTR;
     float wf[EPT], aw[EPT], ab[EPT];
     load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
 #pragma unroll
     for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
-    Pack<T, VL> nx[NV] = {}, ny[NV] = {};
+    Raw nx[NV] = {}, ny[NV] = {};
     float nm = 0.f, nr = 0.f;
     int64_t r = (int64_t)blockIdx.x * RPB + sub;
     const int64_t step = (int64_t)gridDim.x * RPB;
     const auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            nx[n] = load_vec<T, VL>(x + at * xs, n * NTR + t, cols);
-            ny[n] = load_vec<T, VL>(dy + at * dys, n * NTR + t, cols);
+            nx[n] = load_raw<T, RAG>(x + at * xs, n * NTR + t, cols);
+            ny[n] = load_raw<T, RAG>(dy + at * dys, n * NTR + t, cols);
         }
         nm = mean[at];
         nr = rstd[at];
@@ -182,12 +170,14 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm_back(const T* dy, int64_
         float h[EPT], g[EPT];
         const float m = nm, rs = nr;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n) {
+            unpack<T>(nx[n], h + n * VL);
+            unpack<T>(ny[n], g + n * VL);
+        }
+        if (!live) {
 #pragma unroll
-            for (int e = 0; e < VL; ++e) {
-                h[n * VL + e] = live ? to_f(nx[n].v[e]) : m;
-                g[n * VL + e] = live ? to_f(ny[n].v[e]) : 0.f;
-            }
+            for (int i = 0; i < EPT; ++i) h[i] = m, g[i] = 0.f;
+        }
         if (kAhead && r + step < rows) fetch(r + step);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -204,15 +194,9 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm_back(const T* dy, int64_
             const float c1 = s1 / (float)cols, c2 = s2 / (float)cols;
             if (live) {
 #pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    Pack<T, VL> o;
+                for (int i = 0; i < EPT; ++i) g[i] = rs * (g[i] - fmaf(h[i], c2, c1));
 #pragma unroll
-                    for (int e = 0; e < VL; ++e) {
-                        const int i = n * VL + e;
-                        o.v[e] = from_f<T>(rs * (g[i] - fmaf(h[i], c2, c1)));
-                    }
-                    store_vec<T, VL>(dx + r * dxs, n * NTR + t, cols, o);
-                }
+                for (int n = 0; n < NV; ++n) store_raw<T, RAG>(dx + r * dxs, n * NTR + t, cols, g + n * VL);
             }
         }
     }
@@ -245,15 +229,13 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm_back(const T* dy, int64_
     }
     float* p = part + 2 * (int64_t)blockIdx.x * cols;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        Pack<float, VL> o;
+    for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int e = 0; e < VL; ++e) o.v[e] = aw[n * VL + e];
-        store_vec<float, VL>(p, n * NTR + t, cols, o);
-#pragma unroll
-        for (int e = 0; e < VL; ++e) o.v[e] = ab[n * VL + e];
-        store_vec<float, VL>(p + cols, n * NTR + t, cols, o);
-    }
+        for (int e = 0; e < VL; e += 4) {
+            const int v = (n * NTR + t) * (VL / 4) + e / 4;
+            store_raw<float, RAG>(p, v, cols, aw + n * VL + e);
+            store_raw<float, RAG>(p + cols, v, cols, ab + n * VL + e);
+        }
 }
 
 // The parts' sums: a workgroup takes 32 of the 2 cols columns, 32 threads each.
@@ -265,8 +247,10 @@ __global__ __launch_bounds__(kJoinCols* kJoinDeep) void k_norm_join(const float*
     const int tc = threadIdx.x % kJoinCols, td = threadIdx.x / kJoinCols;
     const int64_t c = (int64_t)blockIdx.x * kJoinCols + tc;
     float s = 0.f;
-    if (c < 2 * cols)
+    if (c < 2 * cols) {
+#pragma unroll 8
         for (int64_t p = td; p < parts; p += kJoinDeep) s += part[2 * p * cols + c];
+    }
     tmp[td][tc] = s;
     __syncthreads();
     if (td || c >= 2 * cols) return;
@@ -362,7 +346,7 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
 
 // The shape of a workgroup for rows of `cols` held elements: 8 elements a
 // thread (16 for the longest rows), as few waves a row as that takes, at least
-// 4 waves.
+// 8 waves.
 struct NormShape {
     int nwr, ept, rpb;
 };
@@ -370,7 +354,7 @@ static NormShape norm_shape(int64_t cols)
 {
     int nwr = 1;
     while (nwr < 16 && nwr * 512 < cols) nwr *= 2;
-    return {nwr, nwr * 512 < cols ? 16 : 8, nwr < 4 ? 4 / nwr : 1};
+    return {nwr, nwr * 512 < cols ? 16 : 8, nwr < 8 ? 8 / nwr : 1};
 }
 
 // Workgroups that share out the rows: `waves` of them a compute unit.
@@ -380,7 +364,6 @@ static int64_t norm_groups(const sgc_norm_opts* o, int waves)
     const int64_t most = kCus * waves / (sh.nwr * sh.rpb), need = cdiv(o->rows, sh.rpb);
     return need < most ? need : most;
 }
-constexpr int kForwardWaves = 32, kBackwardWaves = 16;
 
 static int64_t norm_parts(const sgc_norm_opts* o)
 {
@@ -401,16 +384,23 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
                                                                      o->eps);
     } else {
         const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
-#define SGC_NORM(NWR, EPT, RPB) \
-    k_norm<T, W, NWR, EPT, RPB><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols, o->eps)
+#define SGC_NORM_RUN(NWR, EPT, RPB, RAG)                                                                            \
+    k_norm<T, W, NWR, EPT, RPB, RAG><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols, o->eps)
+#define SGC_NORM(NWR, EPT, RPB)                        \
+    do {                                               \
+        if (cols % VecLen<T>::value)                   \
+            SGC_NORM_RUN(NWR, EPT, RPB, true);         \
+        else                                           \
+            SGC_NORM_RUN(NWR, EPT, RPB, false);        \
+    } while (0)
         const NormShape sh = norm_shape(cols);
         if (sh.ept == 16) SGC_NORM(16, 16, 1);
         else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
         else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
-        else if (sh.nwr == 4) SGC_NORM(4, 8, 1);
-        else if (sh.nwr == 2) SGC_NORM(2, 8, 2);
-        else SGC_NORM(1, 8, 4);
-#undef SGC_NORM
+        else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
+        else if (sh.nwr == 2) SGC_NORM(2, 8, 4);
+        else SGC_NORM(1, 8, 8);
+#undef SGC_NORM_RUN
     }
     SGC_LAUNCH_CHECK();
     return SGC_OK;
@@ -441,17 +431,18 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
         }
     } else if (dx || part) {
         const unsigned g = (unsigned)parts;
-#define SGC_NORM(NWR, EPT, RPB)                                                                               \
-    k_norm_back<T, W, NWR, EPT, RPB><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, part, \
-                                                                  o->rows, cols)
+#define SGC_NORM_RUN(NWR, EPT, RPB, RAG)                                                                             \
+    k_norm_back<T, W, NWR, EPT, RPB, RAG><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, part, \
+                                                                       o->rows, cols)
         const NormShape sh = norm_shape(cols);
         if (sh.ept == 16) SGC_NORM(16, 16, 1);
         else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
         else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
-        else if (sh.nwr == 4) SGC_NORM(4, 8, 1);
-        else if (sh.nwr == 2) SGC_NORM(2, 8, 2);
-        else SGC_NORM(1, 8, 4);
+        else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
+        else if (sh.nwr == 2) SGC_NORM(2, 8, 4);
+        else SGC_NORM(1, 8, 8);
 #undef SGC_NORM
+#undef SGC_NORM_RUN
         SGC_LAUNCH_CHECK();
     }
     if (part) {

@@ -137,6 +137,18 @@ __device__ inline float wave_max(float x)
     return last_lane(x);
 }
 
+// The sum of N values (a power of two up to 16) of which lane l holds number
+// l mod N: rotations in rows of 16 lanes.
+template <int N>
+__device__ inline float sum_of_lanes(float x)
+{
+    if (N > 8) x += dpp_or<0x128, 0xf>(0.f, x);
+    if (N > 4) x += dpp_or<0x124, 0xf>(0.f, x);
+    if (N > 2) x += dpp_or<0x122, 0xf>(0.f, x);
+    if (N > 1) x += dpp_or<0x121, 0xf>(0.f, x);
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
 // Sum over a workgroup of NW waves, the same value in every thread; tmp
 // holds NW floats and is free again after the call.
 template <int NW>
