@@ -194,9 +194,8 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     float total, u;
     load_entries<T, NW>(en, a, r, zr, 0, a.vocab, tmp, &total, &u);
     const bool bad = mark_entries<NW>(en, a, 0, a.vocab, bm);
-    SoftSum sum;
-    stream_sums<T, NW * 64, 4, false, TAIL>(zr, a.vocab, a.c, bm, sum);
-    block_join<NW, false>(sum, a.c, tmj);
+    float own;
+    const Sums sum = row_softmax<T, NW, false, TAIL>(zr, a.vocab, a.c, bm, tmj, &own);
     const float base = finite_base(sum.m);
     float s = sum.s, o = sum.s;
     if (TAIL) {
@@ -234,9 +233,8 @@ __device__ inline void keep_packed(Raw (&q)[NV])
 // row stay in each thread's registers from the sums to the gradient (a vector
 // past the row is -inf).  One entry a thread.  The exponent is one fma,
 // z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
-// which the sums are freed from once a row.  A maximum so large that M c
-// leaves fp32 (rows that a mask at the type's lowest value leaves nothing but
-// itself) takes z - M first.
+// which the sums are freed from once a row (lm_softmax.h); a maximum far from
+// zero takes z - M first.
 template <typename T, int NW, int NV, bool TAIL>
 __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T* z, T* dz)
 {
@@ -292,7 +290,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     m = block_max<NW>(m, tmp);
     keep_packed(q);
     const float base = finite_base(m), b = base * a.c;
-    const bool far = !(fabsf(b) < 1e30f);
+    const bool far = is_far(m, a.c);
     const auto power = [&](float x) { return exp2_fast(far ? (x - base) * a.c : fmaf(x, a.c, -b)); };
     float o = 0.f, o2 = 0.f;
 #pragma unroll
@@ -383,9 +381,8 @@ __global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T
         en.z[j] = at >= z0 && at < z1 ? to_f(zr[at]) : -INFINITY;
     }
     const bool bad = mark_entries<NW>(en, a, z0, z1, bm);
-    SoftSum sum;
-    stream_sums<T, NW * 64, 4, false, TAIL>(zr + z0, z1 - z0, a.c, bm, sum);
-    block_join<NW, false>(sum, a.c, tmj);
+    float own;
+    const Sums sum = row_softmax<T, NW, false, TAIL>(zr + z0, z1 - z0, a.c, bm, tmj, &own);
     float in = 0.f;
     if (TAIL) {
         for (int j = threadIdx.x; j < a.top; j += NW * 64)

@@ -2,11 +2,16 @@
 // sums of its softmax, shared by token_logprobs.hip and distill.hip.
 //
 // A thread keeps m = max z, s = sum e and, for the entropy, t = sum e d, with
-// d = (z - m) c, e = 2^d and c = scale / ln 2; when a group of its elements
-// raises m, s and t are carried over to the new one.  Two threads' (or two
-// workgroups') triples join the same way.  z - m is taken before the factor:
-// masks at the type's lowest value then stay finite next to any maximum, and
-// rows of that value alone are uniform as they should be.
+// e = 2^d, d = (z - m) c and c = scale / ln 2; when a group of its elements
+// raises m, s and t are carried over to the new one.  Two threads' sums join
+// the same way.
+//
+// The pass is bound by the vector unit as much as by memory, so d is one fma:
+// z c - b with b = m c rounded to fp32.  All e are then too large by the same
+// 2^r, r = m c - b, which the sums are freed from once a row.  That needs a
+// small r: b is at least -1e8 (|r| <= 4), and a row whose |m c| is more than
+// 1e8 is done again with z - m before the factor (FAR).  Such is the row that a
+// mask at the type's lowest value leaves nothing but itself; it is uniform.
 #pragma once
 
 #include "lm_common.h"
@@ -21,18 +26,20 @@ constexpr float kLowD = -1000.f;
 
 __device__ inline float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+constexpr float kFar = 1e8f;
+__device__ inline bool is_far(float m, float c) { return fabsf(m * c) > kFar && fabsf(m) != INFINITY; }
+
+template <bool FAR>
 struct SoftSum {
     float m = -INFINITY, s = 0.f, t = 0.f;
 
-    // Carry the sums over to a larger maximum.
-    template <bool ENT>
-    __device__ void raise(float to, float c)
+    // What z is measured from: m itself (FAR), or m c.
+    __device__ static float base_of(float m, float c) { return FAR ? finite_base(m) : fmaxf(m * c, -kFar); }
+    __device__ static float power(float x, float base, float c) { return FAR ? (x - base) * c : fmaf(x, c, -base); }
+    // log2 of the factor from sums at one maximum to sums at a larger one
+    __device__ static float step(float from, float to, float c)
     {
-        const float d = fmaxf((m - to) * c, kLowD);
-        const float f = exp2_fast(d);
-        if (ENT) t = fmaf(d, s, t) * f;
-        s *= f;
-        m = to;
+        return fmaxf(FAR ? (from - finite_base(to)) * c : base_of(from, c) - base_of(to, c), kLowD);
     }
 
     // N elements; those with a bit in `skip` count for the maximum alone.
@@ -42,22 +49,34 @@ struct SoftSum {
         float g = x[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) g = fmaxf(g, x[i]);
-        if (g > m) raise<ENT>(g, c);
+        if (g > m) {
+            const float d = step(m, g, c), f = exp2_fast(d);
+            if (ENT) t = fmaf(d, s, t) * f;
+            s *= f;
+            m = g;
+        }
         if (SKIP && skip) {
 #pragma unroll
             for (int i = 0; i < N; ++i) x[i] = (skip >> i) & 1u ? -INFINITY : x[i];
         }
-        const float base = finite_base(m);
+        const float base = base_of(m, c), was = t;
         float s2 = 0.f, t2 = 0.f;  // two chains of additions
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float d = (x[i] - base) * c;
-            const float e = exp2_fast(d);
+            x[i] = power(x[i], base, c);
+            const float e = exp2_fast(x[i]);
             (i & 1 ? s2 : s) += e;
-            if (ENT) (i & 1 ? t2 : t) = fmaf(e, fmaxf(d, kLowD), i & 1 ? t2 : t);
+            if (ENT) (i & 1 ? t2 : t) = fmaf(e, x[i], i & 1 ? t2 : t);
         }
         s += s2;
-        if (ENT) t += t2;
+        if (ENT) {
+            t += t2;
+            if (t != t) {  // 0 * -inf: only groups with masked elements pay for the clamp
+                t = was;
+#pragma unroll
+                for (int i = 0; i < N; ++i) t = fmaf(exp2_fast(x[i]), fmaxf(x[i], kLowD), t);
+            }
+        }
     }
 };
 
@@ -69,18 +88,19 @@ __device__ inline uint32_t vec_bits(const uint32_t* bm, int v)
     return (((const uint8_t*)bm)[v >> 1] >> ((v & 1) * 4)) & 0xfu;
 }
 
-// The elements [0, len) of z, by the NT threads of a workgroup.  U vectors of
-// 16 bytes are in flight for each thread.
-template <typename T, int NT, int U, bool ENT, bool SKIP>
-__device__ inline void stream_sums(const T* z, int len, float c, const uint32_t* bm, SoftSum& a)
+// The elements [0, len) of z, by the NT threads of a workgroup: thread i takes
+// the vectors i, i + NT, ... and one element past the last whole vector.  U
+// vectors of 16 bytes are in flight for each thread.  (The next U fetched
+// ahead, with the last group padded: 195 -> 199 us for 4096 x 131072 bf16.)
+template <typename T, int NT, int U, bool ENT, bool SKIP, bool FAR>
+__device__ inline void stream_sums(const T* z, int len, float c, const uint32_t* bm, SoftSum<FAR>& a)
 {
     constexpr int VL = VecLen<T>::value;
-    using P = Pack<T, VL>;
-    const P* p = (const P*)z;
+    const Raw* p = (const Raw*)z;
     const int nv = len / VL;
     int v = threadIdx.x;
     for (; v + (U - 1) * NT < nv; v += U * NT) {
-        P q[U];
+        Raw q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
         uint32_t skip = 0;
@@ -88,16 +108,13 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (SKIP) skip |= vec_bits<VL>(bm, v + u * NT) << (u * VL);
-#pragma unroll
-            for (int e = 0; e < VL; ++e) x[u * VL + e] = to_f(q[u].v[e]);
+            unpack<T>(q[u], x + u * VL);
         }
         a.template add<U * VL, ENT, SKIP>(x, c, skip);
     }
     for (; v < nv; v += NT) {
-        const P q = p[v];
         float x[VL];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) x[e] = to_f(q.v[e]);
+        unpack<T>(p[v], x);
         a.template add<VL, ENT, SKIP>(x, c, SKIP ? vec_bits<VL>(bm, v) : 0u);
     }
     const int i = nv * VL + threadIdx.x;
@@ -107,22 +124,20 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
     }
 }
 
-// The threads' sums joined: the same values in every thread.  Each wave joins
-// its own, then all threads the waves': one barrier, and one after, so that
-// tmp may be used again.
-template <int NW, bool ENT>
-__device__ inline void block_join(SoftSum& a, float c, float (*tmp)[3])
+// The threads' sums joined, the same values in every thread, s and t at m
+// itself.  Each wave joins its own, then all threads the waves': one barrier,
+// and one after, so that tmp may be used again.
+template <int NW, bool ENT, bool FAR>
+__device__ inline void block_join(SoftSum<FAR>& a, float c, float (*tmp)[3])
 {
-    const float wm = wave_max(a.m);
-    const float d = fmaxf((a.m - finite_base(wm)) * c, kLowD);
-    const float f = exp2_fast(d);
+    float m = wave_max(a.m);
+    const float d = SoftSum<FAR>::step(a.m, m, c), f = exp2_fast(d);
     float t = ENT ? wave_sum(fmaf(d, a.s, a.t) * f) : 0.f;
     float s = wave_sum(a.s * f);
-    float m = wm;
     if (NW > 1) {
         const int w = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
-            tmp[w][0] = wm;
+            tmp[w][0] = m;
             tmp[w][1] = s;
             tmp[w][2] = t;
         }
@@ -133,15 +148,55 @@ __device__ inline void block_join(SoftSum& a, float c, float (*tmp)[3])
         s = t = 0.f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            const float di = fmaxf((tmp[i][0] - finite_base(m)) * c, kLowD), fi = exp2_fast(di);
+            const float di = SoftSum<FAR>::step(tmp[i][0], m, c), fi = exp2_fast(di);
             s += tmp[i][1] * fi;
             if (ENT) t += fmaf(di, tmp[i][1], tmp[i][2]) * fi;
         }
         __syncthreads();
     }
+    if (!FAR) {
+        const float r = m == -INFINITY ? 0.f : fmaf(m, c, -SoftSum<FAR>::base_of(m, c)), f1 = exp2_fast(-r);
+        if (ENT) t = fmaf(-r, s, t) * f1;
+        s *= f1;
+    }
     a.m = m;
     a.s = s;
     a.t = t;
+}
+
+// A row's (or chunk's) m, s, t in every thread; *own: the thread's maximum.
+struct Sums {
+    float m, s, t;
+};
+template <typename T, int NW, bool ENT, bool SKIP>
+__device__ inline Sums row_softmax(const T* z, int len, float c, const uint32_t* bm, float (*tmp)[3], float* own)
+{
+    SoftSum<false> a;
+    stream_sums<T, NW * 64, 4, ENT, SKIP>(z, len, c, bm, a);
+    *own = a.m;
+    block_join<NW, ENT>(a, c, tmp);
+    if (!is_far(a.m, c)) return {a.m, a.s, a.t};
+    SoftSum<true> b;
+    stream_sums<T, NW * 64, 1, ENT, SKIP>(z, len, c, bm, b);
+    block_join<NW, ENT>(b, c, tmp);
+    return {b.m, b.s, b.t};
+}
+
+// The sums of the parts k, k + NT, ... of n, four floats each, joined.
+template <int NW, bool ENT>
+__device__ inline Sums join_parts(const float* p, int n, float c, float (*tmp)[3])
+{
+    SoftSum<true> a;
+    for (int k = threadIdx.x; k < n; k += NW * 64) {
+        const float m = p[4 * k], s = p[4 * k + 1], t = p[4 * k + 2];
+        const float to = fmaxf(m, a.m);
+        const float d0 = a.step(a.m, to, c), f0 = exp2_fast(d0), d1 = a.step(m, to, c), f1 = exp2_fast(d1);
+        if (ENT) a.t = fmaf(d0, a.s, a.t) * f0 + fmaf(d1, s, t) * f1;
+        a.s = a.s * f0 + s * f1;
+        a.m = to;
+    }
+    block_join<NW, ENT>(a, c, tmp);
+    return {a.m, a.s, a.t};
 }
 
 }  // namespace sgc

@@ -171,7 +171,7 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
 }
 
 // What a row's sums give: logp, entropy, stats; ln s and the base of y.
-__device__ inline void finish_row(const LogprobArgs& a, int64_t r, float z_tok, int64_t tok, const SoftSum& sum,
+__device__ inline void finish_row(const LogprobArgs& a, int64_t r, float z_tok, int64_t tok, const Sums& sum,
                                   float ln_s)
 {
     const bool none = sum.s == 0.f;
@@ -192,7 +192,7 @@ __device__ inline void finish_row(const LogprobArgs& a, int64_t r, float z_tok, 
     }
 }
 
-__device__ inline void write_top(const LogprobArgs& a, int64_t r, int k, uint64_t key, const SoftSum& sum, float ln_s)
+__device__ inline void write_top(const LogprobArgs& a, int64_t r, int k, uint64_t key, const Sums& sum, float ln_s)
 {
     const float v = key_value((uint32_t)(key >> 32));
     a.top_idx[r * a.top + k] = (int32_t)~(uint32_t)key;
@@ -214,14 +214,12 @@ __global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)
         tok = token_at(a.tokens, a.token_type, r);
         if (tok >= 0 && tok < a.vocab) z_tok = to_f(zr[tok]);
     }
-    SoftSum sum;
-    stream_sums<T, NW * 64, 4, true, false>(zr, a.vocab, a.c, nullptr, sum);
-    const float m = sum.m;
-    block_join<NW, true>(sum, a.c, tmp);
+    float m;
+    const Sums sum = row_softmax<T, NW, true, false>(zr, a.vocab, a.c, nullptr, tmp, &m);
     const float ln_s = logf(sum.s);
     if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
     if (a.top) {
-        const int n = top_of<T, NW>(cd, zr, a.vocab, 0, a.top, m, sum.s != sum.s);
+        const int n = top_of<T, NW>(cd, zr, a.vocab, 0, a.top, m, !(sum.s < INFINITY));
         for (int k = threadIdx.x; k < n; k += NW * 64) write_top(a, r, k, cd.sorted[k], sum, ln_s);
     }
 }
@@ -238,17 +236,15 @@ __global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, 
     if (r >= a.rows) return;
     const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
     const T* zr = z + r * a.zs + z0;
-    SoftSum sum;
-    stream_sums<T, NW * 64, 4, true, false>(zr, len, a.c, nullptr, sum);
-    const float m = sum.m;
-    block_join<NW, true>(sum, a.c, tmp);
+    float m;
+    const Sums sum = row_softmax<T, NW, true, false>(zr, len, a.c, nullptr, tmp, &m);
     if (threadIdx.x == 0) {
         part[4 * b] = sum.m;
         part[4 * b + 1] = sum.s;
         part[4 * b + 2] = sum.t;
     }
     if (a.top) {
-        const int n = top_of<T, NW>(cd, zr, len, z0, a.top, m, sum.s != sum.s);
+        const int n = top_of<T, NW>(cd, zr, len, z0, a.top, m, !(sum.s < INFINITY));
         for (int k = threadIdx.x; k < a.top; k += NW * 64) keys[b * a.top + k] = k < n ? cd.sorted[k] : 0;
     }
 }
@@ -269,20 +265,7 @@ __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, 
         tok = token_at(a.tokens, a.token_type, r);
         if (tok >= 0 && tok < a.vocab) z_tok = to_f(z[r * a.zs + tok]);
     }
-    SoftSum sum;
-    const float* p = part + 4 * r * chunks;
-    for (int k = threadIdx.x; k < chunks; k += NT) {
-        SoftSum o;
-        o.m = p[4 * k];
-        o.s = p[4 * k + 1];
-        o.t = p[4 * k + 2];
-        if (o.m > sum.m)
-            sum.raise<true>(o.m, a.c);
-        const float d = fmaxf((o.m - finite_base(sum.m)) * a.c, kLowD), f = exp2_fast(d);
-        sum.t += fmaf(d, o.s, o.t) * f;
-        sum.s += o.s * f;
-    }
-    block_join<NW, true>(sum, a.c, tmp);
+    const Sums sum = join_parts<NW, true>(part + 4 * r * chunks, chunks, a.c, tmp);
     const float ln_s = logf(sum.s);
     if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
     if (!a.top) return;

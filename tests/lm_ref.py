@@ -12,6 +12,8 @@ import torch
 
 U = 2.0 ** -24
 DEPTH = 64
+# powers of two below fp32's normal range are 0 in the kernels
+FLUSH = 2.0 ** -126
 
 
 def half_step(dtype, ref):
@@ -146,6 +148,7 @@ def logprobs_backward(sm, tokens, g, h):
     d = sm.scale * (g * (hot - sm.p) - h * sm.p * (lp + H))
     tol = sm.scale * (g.abs() * (sm.p * (sm.t_lp + 4 * U) + 2 * U * hot) + h.abs() * sm.p * (
         (lp + H).abs() * (sm.t_lp + 4 * U) + sm.t_lp + sm.t_H + 4 * U * (lp.abs() + H.abs()))) + 4 * U * d.abs()
+    tol = tol + sm.scale * (g.abs() + h.abs() * (lp + H).abs()) * FLUSH
     zero = sm.none | ((g == 0) & (h == 0))[:, 0]
     d[zero] = 0.0
     tol[zero] = 0.0
@@ -219,6 +222,7 @@ def distill(z, t_idx, t_val, tail, scale, teacher_scale=1.0, g=None):
     d = gs * (mass * sm.p - tt - u * share)
     tol = gs.abs() * (mass * sm.p * (sm.t_lp + 6 * U) + t_tt + te["t_u"] * (sm.p + share)
                       + u * share * (2 * sm.t_lp + (DEPTH + 8) * U)) + 4 * U * d.abs()
+    tol = tol + gs.abs() * FLUSH * (mass + torch.where(tail_on, u / outside.clamp(min=1e-300), 0.0))
     zero = skip | (g == 0)
     d[zero] = 0.0
     tol[zero] = 0.0

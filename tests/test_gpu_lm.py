@@ -413,6 +413,26 @@ def test_distill_edges(vocab, k, kind, tail, dtype):
     check_distill(z, idx, val, tail, scale=0.75)
 
 
+@pytest.mark.parametrize("vocab", [98, 3001, 40004, 150001])
+def test_logits_far_from_zero(vocab):
+    """Maxima of 1e4 to 3e38 either way, alone in their row or with an ordinary rest."""
+    rows = 600 if vocab < 5000 else 12
+    announce(f"logits far from zero, {rows}x{vocab}")
+    z = torch.randn(rows, vocab, generator=gen(vocab))
+    for r in range(rows):
+        far = (1e4, -1e4, 7e7, -7e7, 3e8, -3e8, 1e12, -1e12, 1e30, -1e30, 3e38, -3e38)[r % 12]
+        if r % 24 < 12:
+            z[r] = far + z[r] * max(1.0, abs(far) * 1e-7)
+        else:
+            z[r, vocab // 2] = far
+    check_logprobs(z, tokens_for(rows, vocab, 3), 1.0, 10)
+    idx, val = entries_for(z, 12, 3, True)
+    for tail in (False, True):
+        # entries far below their row's maximum would have an infinite loss
+        near = z.gather(1, idx.long().clamp(min=0)) > z.amax(1, keepdim=True) - 80
+        check_distill(z, idx, torch.where(near, val, -INF), tail)
+
+
 def test_distill_student_without_the_teachers_token():
     announce("distill: the student gives a taught token nothing")
     z = torch.randn(2, 500, generator=gen(1))
