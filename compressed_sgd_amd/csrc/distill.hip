@@ -90,33 +90,30 @@ __device__ inline bool mark_entries(const Entries& en, const DistillArgs& a, int
 
 // The gradient of the chunk [z0, z1): e_i k_out everywhere, then the entries'
 // own values over it (every thread's stores are done at the barrier).
-template <typename T, int NW, int U>
+template <typename T, int NW, int U, bool ONCE>
 __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, const T* zr, T* out, int z0, int z1,
                                       float m, float k_out, float k_in, float k_t)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
-    using P = Pack<T, VL>;
-    const P* p = (const P*)(zr + z0);
-    P* o = (P*)(out + z0);
+    const Raw* p = (const Raw*)(zr + z0);
+    Raw* o = (Raw*)(out + z0);
     const int nv = (z1 - z0) / VL;
+    const auto one = [&](const Raw& q, int v) {
+        float x[VL];
+        unpack<T>(q, x);
+#pragma unroll
+        for (int e = 0; e < VL; ++e) x[e] = exp2_fast((x[e] - m) * a.c) * k_out;
+        store_row<ONCE>(o + v, pack<T>(x));
+    };
     int v = threadIdx.x;
     for (; v + (U - 1) * NT < nv; v += U * NT) {
-        P q[U];
+        Raw q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
+        for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int e = 0; e < VL; ++e) q[u].v[e] = from_f<T>(exp2_fast((to_f(q[u].v[e]) - m) * a.c) * k_out);
-            o[v + u * NT] = q[u];
-        }
+        for (int u = 0; u < U; ++u) one(q[u], v + u * NT);
     }
-    for (; v < nv; v += NT) {
-        P q = p[v];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) q.v[e] = from_f<T>(exp2_fast((to_f(q.v[e]) - m) * a.c) * k_out);
-        o[v] = q;
-    }
+    for (; v < nv; v += NT) one(load_row<ONCE>(p + v), v);
     const int i = z0 + nv * VL + threadIdx.x;
     if (i < z1) out[i] = from_f<T>(exp2_fast((to_f(zr[i]) - m) * a.c) * k_out);
     __syncthreads();
@@ -127,16 +124,12 @@ __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, c
     }
 }
 
-template <typename T, int NW>
+template <typename T, int NW, bool ONCE>
 __device__ inline void write_zeros(T* out, int z0, int z1)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
-    using P = Pack<T, VL>;
-    P zero;
-#pragma unroll
-    for (int e = 0; e < VL; ++e) zero.v[e] = (T)0.f;
     const int nv = (z1 - z0) / VL;
-    for (int v = threadIdx.x; v < nv; v += NT) ((P*)(out + z0))[v] = zero;
+    for (int v = threadIdx.x; v < nv; v += NT) store_row<ONCE>((Raw*)(out + z0) + v, Raw{{0, 0, 0, 0}});
     const int i = z0 + nv * VL + threadIdx.x;
     if (i < z1) out[i] = (T)0.f;
 }
@@ -195,7 +188,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     load_entries<T, NW>(en, a, r, zr, 0, a.vocab, tmp, &total, &u);
     const bool bad = mark_entries<NW>(en, a, 0, a.vocab, bm);
     float own;
-    const Sums sum = row_softmax<T, NW, false, TAIL>(zr, a.vocab, a.c, bm, tmj, &own);
+    const Sums sum = row_softmax<T, NW, false, TAIL, false>(zr, a.vocab, a.c, bm, tmj, &own);
     const float base = finite_base(sum.m);
     float s = sum.s, o = sum.s;
     if (TAIL) {
@@ -209,12 +202,12 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     const float g = a.dloss ? a.dloss[r] : 1.f;
     T* out = dz + r * a.dzs;
     if (skip || g == 0.f) {
-        write_zeros<T, NW>(out, 0, a.vocab);
+        write_zeros<T, NW, false>(out, 0, a.vocab);
         return;
     }
     float k_out, k_in, k_t;
     factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
-    write_gradient<T, NW, 4>(en, a, zr, out, 0, a.vocab, base, k_out, k_in, k_t);
+    write_gradient<T, NW, 4, false>(en, a, zr, out, 0, a.vocab, base, k_out, k_in, k_t);
 }
 
 // The held vectors are the same 16 bytes after this, but the compiler does not
@@ -235,7 +228,7 @@ __device__ inline void keep_packed(Raw (&q)[NV])
 // z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
 // which the sums are freed from once a row (lm_softmax.h); a maximum far from
 // zero takes z - M first.
-template <typename T, int NW, int NV, bool TAIL>
+template <typename T, int NW, int NV, bool TAIL, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T* z, T* dz)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
@@ -255,7 +248,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     }
     Raw q[NV];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) q[n] = tid + n * NT < nv ? ((const Raw*)zr)[tid + n * NT] : raw_low<T>();
+    for (int n = 0; n < NV; ++n) q[n] = tid + n * NT < nv ? load_row<ONCE>((const Raw*)zr + tid + n * NT) : raw_low<T>();
     const int last = nv * VL + tid;
     const float z_last = last < a.vocab ? to_f(zr[last]) : -INFINITY;
     // the entries: marks, T and u
@@ -336,7 +329,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     }
     T* out = dz + r * a.dzs;
     if (skip || g == 0.f) {
-        write_zeros<T, NW>(out, 0, a.vocab);
+        write_zeros<T, NW, ONCE>(out, 0, a.vocab);
         return;
     }
     float k_out, k_in, k_t;
@@ -353,7 +346,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
 #pragma unroll
                 for (int e = 0; e < VL; ++e) x[e] = exp2_fast(fmaf(x[e], a.c, -b)) * k_out;
             }
-            ((Raw*)out)[tid + n * NT] = pack<T>(x);
+            store_row<ONCE>((Raw*)out + tid + n * NT, pack<T>(x));
         }
     }
     if (last < a.vocab) out[last] = from_f<T>(power(z_last) * k_out);
@@ -382,7 +375,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T
     }
     const bool bad = mark_entries<NW>(en, a, z0, z1, bm);
     float own;
-    const Sums sum = row_softmax<T, NW, false, TAIL>(zr + z0, z1 - z0, a.c, bm, tmj, &own);
+    const Sums sum = row_softmax<T, NW, false, TAIL, false>(zr + z0, z1 - z0, a.c, bm, tmj, &own);
     float in = 0.f;
     if (TAIL) {
         for (int j = threadIdx.x; j < a.top; j += NW * 64)
@@ -429,7 +422,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_join(DistillArgs a, const T
 }
 
 // The gradient of a chunk of a row from the row's stats.
-template <typename T, int NW>
+template <typename T, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_distill_grad(DistillArgs a, const float* stats, const T* z, T* dz,
                                                           int chunk, int chunks)
 {
@@ -442,14 +435,14 @@ __global__ __launch_bounds__(NW * 64) void k_distill_grad(DistillArgs a, const f
     T* out = dz + r * a.dzs;
     const float g = a.dloss ? a.dloss[r] : 1.f;
     if (stats[4 * r + 3] == 0.f || g == 0.f) {
-        write_zeros<T, NW>(out, z0, z1);
+        write_zeros<T, NW, ONCE>(out, z0, z1);
         return;
     }
     float total, u, k_out, k_in, k_t;
     load_entries<T, NW>(en, a, r, zr, z0, z1, tmp, &total, &u);
     __syncthreads();  // the entries' logits are read before any of the chunk's gradient is written
     factors(a, g, stats[4 * r + 2], stats[4 * r + 1], total, u, &k_out, &k_in, &k_t);
-    write_gradient<T, NW, 4>(en, a, zr, out, z0, z1, finite_base(stats[4 * r]), k_out, k_in, k_t);
+    write_gradient<T, NW, 4, ONCE>(en, a, zr, out, z0, z1, finite_base(stats[4 * r]), k_out, k_in, k_t);
 }
 
 static bool distill_opts_ok(const sgc_distill_opts* o)
@@ -506,14 +499,26 @@ static DistillArgs distill_args(const sgc_distill_opts* o, int64_t zs, const int
 template <typename T>
 static int distill_grad(const DistillArgs& a, const float* stats, const T* z, T* dz, hipStream_t s)
 {
-    if (a.vocab <= 2048) {
-        k_distill_grad<T, 1><<<row_grid(a.rows), 64, 0, s>>>(a, stats, z, dz, 2048, 1);
-    } else {
-        const int chunk = 8192, chunks = (int)cdiv(a.vocab, chunk);
-        k_distill_grad<T, 4><<<row_grid(a.rows * chunks), 256, 0, s>>>(a, stats, z, dz, chunk, chunks);
-    }
+    const bool once = 2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes;
+    const int chunk = a.vocab <= 2048 ? 2048 : 8192, chunks = (int)cdiv(a.vocab, chunk);
+    const dim3 grid = row_grid(a.rows * chunks);
+    if (a.vocab <= 2048)
+        once ? k_distill_grad<T, 1, true><<<grid, 64, 0, s>>>(a, stats, z, dz, chunk, chunks)
+             : k_distill_grad<T, 1, false><<<grid, 64, 0, s>>>(a, stats, z, dz, chunk, chunks);
+    else
+        once ? k_distill_grad<T, 4, true><<<grid, 256, 0, s>>>(a, stats, z, dz, chunk, chunks)
+             : k_distill_grad<T, 4, false><<<grid, 256, 0, s>>>(a, stats, z, dz, chunk, chunks);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
+}
+
+template <typename T, int NW, int NV, bool TAIL>
+static void distill_held(const DistillArgs& a, const T* z, T* dz, size_t lds, hipStream_t s)
+{
+    if (2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes)
+        k_distill_held<T, NW, NV, TAIL, true><<<row_grid(a.rows), NW * 64, lds, s>>>(a, z, dz);
+    else
+        k_distill_held<T, NW, NV, TAIL, false><<<row_grid(a.rows), NW * 64, lds, s>>>(a, z, dz);
 }
 
 template <typename T, bool TAIL>
@@ -527,15 +532,15 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
         if (a.vocab <= 2048)
             k_distill_row<T, 1, TAIL><<<rows, 64, lds, s>>>(a, z, dz);
         else if (dz && nv <= 1024)
-            k_distill_held<T, 4, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
+            distill_held<T, 4, 4, TAIL>(a, z, dz, lds, s);
         else if (dz && nv <= 2048)
-            k_distill_held<T, 4, 8, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
+            distill_held<T, 4, 8, TAIL>(a, z, dz, lds, s);
         else if (dz && nv <= 4096)
-            k_distill_held<T, 8, 8, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+            distill_held<T, 8, 8, TAIL>(a, z, dz, lds, s);
         else if (dz && nv <= 8192)
-            k_distill_held<T, 8, 16, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+            distill_held<T, 8, 16, TAIL>(a, z, dz, lds, s);
         else if (dz && nv <= 16384)
-            k_distill_held<T, 16, 16, TAIL><<<rows, 1024, lds, s>>>(a, z, dz);
+            distill_held<T, 16, 16, TAIL>(a, z, dz, lds, s);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
         else

@@ -22,11 +22,11 @@ constexpr int kForwardWaves = 32, kBackwardWaves = 16;
 
 // Elements [v VL, v VL + VL) of a row that ends at cols; past it 0.  RAG: cols
 // is no multiple of VL.
-template <typename T, bool RAG>
+template <typename T, bool RAG, bool ONCE>
 __device__ inline Raw load_raw(const T* p, int v, int cols)
 {
     constexpr int VL = VecLen<T>::value;
-    if ((v + 1) * VL <= cols) return ((const Raw*)p)[v];
+    if ((v + 1) * VL <= cols) return load_row<ONCE>((const Raw*)p + v);
     Raw q = {{0, 0, 0, 0}};
     if (RAG && v * VL < cols) {
         float x[VL];
@@ -36,12 +36,12 @@ __device__ inline Raw load_raw(const T* p, int v, int cols)
     }
     return q;
 }
-template <typename T, bool RAG>
+template <typename T, bool RAG, bool ONCE>
 __device__ inline void store_raw(T* p, int v, int cols, const float* x)
 {
     constexpr int VL = VecLen<T>::value;
     if ((v + 1) * VL <= cols) {
-        ((Raw*)p)[v] = pack<T>(x);
+        store_row<ONCE>((Raw*)p + v, pack<T>(x));
     } else if (RAG && v * VL < cols) {
 #pragma unroll
         for (int e = 0; e < VL; ++e)
@@ -78,7 +78,7 @@ __device__ inline void row_sums(float& a, float& b, float (*tmp)[RPB][NWR][2], i
     b = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][1]);
 }
 
-template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG>
+template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG, bool ONCE>
 __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
                                                         int64_t ys, float* mean, float* rstd, int64_t rows, int cols,
                                                         float eps)
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
     const int64_t step = (int64_t)gridDim.x * RPB;
     if (r < rows) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG>(x + r * xs, n * NTR + t, cols);
+        for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG, ONCE>(x + r * xs, n * NTR + t, cols);
     }
     for (; r - sub < rows; r += step) {
         float f[EPT];
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
         for (int n = 0; n < NV; ++n) unpack<T>(next[n], f + n * VL);
         if (r + step < rows) {
 #pragma unroll
-            for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG>(x + (r + step) * xs, n * NTR + t, cols);
+            for (int n = 0; n < NV; ++n) next[n] = load_raw<T, RAG, ONCE>(x + (r + step) * xs, n * NTR + t, cols);
         }
         float s = 0.f, q = 0.f, none = 0.f;
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
 #pragma unroll
             for (int i = 0; i < EPT; ++i) f[i] = fmaf(f[i] * rs, wf[i], bf[i]);
 #pragma unroll
-            for (int n = 0; n < NV; ++n) store_raw<T, RAG>(y + r * ys, n * NTR + t, cols, f + n * VL);
+            for (int n = 0; n < NV; ++n) store_raw<T, RAG, ONCE>(y + r * ys, n * NTR + t, cols, f + n * VL);
             if (t == 0) {
                 if (mean) mean[r] = m;
                 if (rstd) rstd[r] = rs;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
 
 // dx, and the workgroup's sums of dy xh and dy over its rows: part
 // [workgroups, 2, cols].
-template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG>
+template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG, bool ONCE>
 __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) void k_norm_back(const T* dy, int64_t dys, const T* x, int64_t xs,
                                                              const W* w, const float* mean, const float* rstd, T* dx,
                                                              int64_t dxs, float* part, int64_t rows, int cols)
@@ -153,8 +153,8 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
     const auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            nx[n] = load_raw<T, RAG>(x + at * xs, n * NTR + t, cols);
-            ny[n] = load_raw<T, RAG>(dy + at * dys, n * NTR + t, cols);
+            nx[n] = load_raw<T, RAG, ONCE>(x + at * xs, n * NTR + t, cols);
+            ny[n] = load_raw<T, RAG, ONCE>(dy + at * dys, n * NTR + t, cols);
         }
         nm = mean[at];
         nr = rstd[at];
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) g[i] = rs * (g[i] - fmaf(h[i], c2, c1));
 #pragma unroll
-                for (int n = 0; n < NV; ++n) store_raw<T, RAG>(dx + r * dxs, n * NTR + t, cols, g + n * VL);
+                for (int n = 0; n < NV; ++n) store_raw<T, RAG, ONCE>(dx + r * dxs, n * NTR + t, cols, g + n * VL);
             }
         }
     }
@@ -233,8 +233,8 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
 #pragma unroll
         for (int e = 0; e < VL; e += 4) {
             const int v = (n * NTR + t) * (VL / 4) + e / 4;
-            store_raw<float, RAG>(p, v, cols, aw + n * VL + e);
-            store_raw<float, RAG>(p + cols, v, cols, ab + n * VL + e);
+            store_raw<float, RAG, false>(p, v, cols, aw + n * VL + e);
+            store_raw<float, RAG, false>(p + cols, v, cols, ab + n * VL + e);
         }
 }
 
@@ -384,14 +384,20 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
                                                                      o->eps);
     } else {
         const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
-#define SGC_NORM_RUN(NWR, EPT, RPB, RAG)                                                                            \
-    k_norm<T, W, NWR, EPT, RPB, RAG><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols, o->eps)
-#define SGC_NORM(NWR, EPT, RPB)                        \
-    do {                                               \
-        if (cols % VecLen<T>::value)                   \
-            SGC_NORM_RUN(NWR, EPT, RPB, true);         \
-        else                                           \
-            SGC_NORM_RUN(NWR, EPT, RPB, false);        \
+        const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) > kCacheBytes;
+#define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                 \
+    k_norm<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, \
+                                                                        cols, o->eps)
+// rows of whole vectors or not, past the caches or not
+#define SGC_NORM(NWR, EPT, RPB)                                  \
+    do {                                                         \
+        if (cols % VecLen<T>::value) {                           \
+            if (once) SGC_NORM_RUN(NWR, EPT, RPB, true, true);   \
+            else SGC_NORM_RUN(NWR, EPT, RPB, true, false);       \
+        } else {                                                 \
+            if (once) SGC_NORM_RUN(NWR, EPT, RPB, false, true);  \
+            else SGC_NORM_RUN(NWR, EPT, RPB, false, false);      \
+        }                                                        \
     } while (0)
         const NormShape sh = norm_shape(cols);
         if (sh.ept == 16) SGC_NORM(16, 16, 1);
@@ -431,9 +437,10 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
         }
     } else if (dx || part) {
         const unsigned g = (unsigned)parts;
-#define SGC_NORM_RUN(NWR, EPT, RPB, RAG)                                                                             \
-    k_norm_back<T, W, NWR, EPT, RPB, RAG><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, part, \
-                                                                       o->rows, cols)
+        const bool once = (dx ? 3 : 2) * o->rows * cols * (int64_t)sizeof(T) > kCacheBytes;
+#define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                         \
+    k_norm_back<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
+                                                                             part, o->rows, cols)
         const NormShape sh = norm_shape(cols);
         if (sh.ept == 16) SGC_NORM(16, 16, 1);
         else if (sh.nwr == 16) SGC_NORM(16, 8, 1);

@@ -48,6 +48,30 @@ struct VecLen {
 struct __attribute__((packed, aligned(2))) Raw {
     uint32_t w[4];
 };
+// Accesses of data that passes once (ONCE) go past the caches: a bare copy of 1
+// GiB in rows of 256 KB runs at 5.9 TB/s with both of them so, 4.6 with
+// neither.  A call takes them where what it reads and writes is more than the
+// last-level cache holds; below that the next call finds its input there (a
+// layer norm backward of 156 MB: 40.1 us without, 40.9 with; the gradients of
+// 2048 x 50000 logits, 410 MB: 66 without, 47 with).
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
+typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+template <bool ONCE>
+__device__ inline Raw load_row(const Raw* p)
+{
+    if (!ONCE) return *p;
+    const Words w = __builtin_nontemporal_load((const Words*)p);
+    return {{w.x, w.y, w.z, w.w}};
+}
+template <bool ONCE>
+__device__ inline void store_row(Raw* p, const Raw& q)
+{
+    const Words w = {q.w[0], q.w[1], q.w[2], q.w[3]};
+    if (ONCE)
+        __builtin_nontemporal_store(w, (Words*)p);
+    else
+        *p = q;
+}
 template <typename T>
 __device__ inline void unpack(const Raw& q, float* x)
 {

@@ -92,7 +92,7 @@ __device__ inline uint32_t vec_bits(const uint32_t* bm, int v)
 // the vectors i, i + NT, ... and one element past the last whole vector.  U
 // vectors of 16 bytes are in flight for each thread.  (The next U fetched
 // ahead, with the last group padded: 195 -> 199 us for 4096 x 131072 bf16.)
-template <typename T, int NT, int U, bool ENT, bool SKIP, bool FAR>
+template <typename T, int NT, int U, bool ENT, bool SKIP, bool ONCE, bool FAR>
 __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t* bm, SoftSum<FAR>& a)
 {
     constexpr int VL = VecLen<T>::value;
@@ -102,7 +102,7 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
     for (; v + (U - 1) * NT < nv; v += U * NT) {
         Raw q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
+        for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
         uint32_t skip = 0;
         float x[U * VL];
 #pragma unroll
@@ -114,7 +114,7 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
     }
     for (; v < nv; v += NT) {
         float x[VL];
-        unpack<T>(p[v], x);
+        unpack<T>(load_row<ONCE>(p + v), x);
         a.template add<VL, ENT, SKIP>(x, c, SKIP ? vec_bits<VL>(bm, v) : 0u);
     }
     const int i = nv * VL + threadIdx.x;
@@ -168,16 +168,16 @@ __device__ inline void block_join(SoftSum<FAR>& a, float c, float (*tmp)[3])
 struct Sums {
     float m, s, t;
 };
-template <typename T, int NW, bool ENT, bool SKIP>
+template <typename T, int NW, bool ENT, bool SKIP, bool ONCE>
 __device__ inline Sums row_softmax(const T* z, int len, float c, const uint32_t* bm, float (*tmp)[3], float* own)
 {
     SoftSum<false> a;
-    stream_sums<T, NW * 64, 4, ENT, SKIP>(z, len, c, bm, a);
+    stream_sums<T, NW * 64, 4, ENT, SKIP, ONCE>(z, len, c, bm, a);
     *own = a.m;
     block_join<NW, ENT>(a, c, tmp);
     if (!is_far(a.m, c)) return {a.m, a.s, a.t};
     SoftSum<true> b;
-    stream_sums<T, NW * 64, 1, ENT, SKIP>(z, len, c, bm, b);
+    stream_sums<T, NW * 64, 1, ENT, SKIP, ONCE>(z, len, c, bm, b);
     block_join<NW, ENT>(b, c, tmp);
     return {b.m, b.s, b.t};
 }

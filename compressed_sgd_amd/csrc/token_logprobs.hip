@@ -200,7 +200,7 @@ __device__ inline void write_top(const LogprobArgs& a, int64_t r, int k, uint64_
 }
 
 // A row a workgroup.
-template <typename T, int NW>
+template <typename T, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)
 {
     __shared__ Candidates<NW> cd;
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)
         if (tok >= 0 && tok < a.vocab) z_tok = to_f(zr[tok]);
     }
     float m;
-    const Sums sum = row_softmax<T, NW, true, false>(zr, a.vocab, a.c, nullptr, tmp, &m);
+    const Sums sum = row_softmax<T, NW, true, false, ONCE>(zr, a.vocab, a.c, nullptr, tmp, &m);
     const float ln_s = logf(sum.s);
     if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
     if (a.top) {
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, 
     const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
     const T* zr = z + r * a.zs + z0;
     float m;
-    const Sums sum = row_softmax<T, NW, true, false>(zr, len, a.c, nullptr, tmp, &m);
+    const Sums sum = row_softmax<T, NW, true, false, false>(zr, len, a.c, nullptr, tmp, &m);
     if (threadIdx.x == 0) {
         part[4 * b] = sum.m;
         part[4 * b + 1] = sum.s;
@@ -307,29 +307,27 @@ __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, 
 
 // The gradient of a chunk of a row: e (A + B d) with d and e of the softmax's
 // pass, and the token's own part where it falls.
-template <typename T, int NW, bool ENT>
+template <typename T, int NW, bool ENT, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_lp_back(LogprobArgs a, const float* stats, const float* entropy,
                                                      const float* dlogp, const float* dentropy, const T* z, T* dz,
                                                      int64_t dzs, int chunk, int chunks)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value, U = 4;
-    using P = Pack<T, VL>;
     const int64_t b = row_of_block(), r = b / chunks;
     if (r >= a.rows) return;
     const int z0 = (int)(b - r * chunks) * chunk, len = a.vocab - z0 < chunk ? a.vocab - z0 : chunk;
     const int nv = len / VL;
-    const P* p = (const P*)(z + r * a.zs + z0);
-    P* o = (P*)(dz + r * dzs + z0);
+    const T* zr = z + r * a.zs + z0;
+    T* out = dz + r * dzs + z0;
+    const Raw* p = (const Raw*)zr;
+    Raw* o = (Raw*)out;
     const int64_t tok = dlogp ? token_at(a.tokens, a.token_type, r) : -1;
     const float g = tok >= 0 && tok < a.vocab ? dlogp[r] : 0.f;
     const float h = ENT ? dentropy[r] : 0.f;
     const float s = stats[2 * r + 1];
     if ((g == 0.f && h == 0.f) || s == 0.f) {
-        P zero;
-#pragma unroll
-        for (int e = 0; e < VL; ++e) zero.v[e] = (T)0.f;
-        for (int v = threadIdx.x; v < nv; v += NT) o[v] = zero;
-        if (nv * VL + (int)threadIdx.x < len) ((T*)o)[nv * VL + threadIdx.x] = (T)0.f;
+        for (int v = threadIdx.x; v < nv; v += NT) store_row<ONCE>(o + v, Raw{{0, 0, 0, 0}});
+        if (nv * VL + (int)threadIdx.x < len) out[nv * VL + threadIdx.x] = (T)0.f;
         return;
     }
     const float m = finite_base(stats[2 * r]);
@@ -342,26 +340,23 @@ __global__ __launch_bounds__(NW * 64) void k_lp_back(LogprobArgs a, const float*
         return i == at ? v + add : v;
     };
     int v = threadIdx.x;
+    const auto one = [&](const Raw& q, int at_v) {
+        float x[VL];
+        unpack<T>(q, x);
+#pragma unroll
+        for (int e = 0; e < VL; ++e) x[e] = grad(x[e], at_v * VL + e);
+        store_row<ONCE>(o + at_v, pack<T>(x));
+    };
     for (; v + (U - 1) * NT < nv; v += U * NT) {
-        P q[U];
+        Raw q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = p[v + u * NT];
+        for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int e = 0; e < VL; ++e)
-                q[u].v[e] = from_f<T>(grad(to_f(q[u].v[e]), (v + u * NT) * VL + e));
-            o[v + u * NT] = q[u];
-        }
+        for (int u = 0; u < U; ++u) one(q[u], v + u * NT);
     }
-    for (; v < nv; v += NT) {
-        P q = p[v];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) q.v[e] = from_f<T>(grad(to_f(q.v[e]), v * VL + e));
-        o[v] = q;
-    }
+    for (; v < nv; v += NT) one(load_row<ONCE>(p + v), v);
     const int i = nv * VL + threadIdx.x;
-    if (i < len) ((T*)o)[i] = from_f<T>(grad(to_f(((const T*)p)[i]), i));
+    if (i < len) out[i] = from_f<T>(grad(to_f(zr[i]), i));
 }
 
 static bool logprob_opts_ok(const sgc_logprob_opts* o)
@@ -422,12 +417,13 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     const int chunks = chunks_of(o);
     const dim3 rows = row_grid(o->rows);
     if (chunks == 1) {
+        const bool once = a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes;
         if (a.vocab <= 2048 && a.top <= 32)
-            k_lp_row<T, 1><<<rows, 64, 0, s>>>(a, z);
+            once ? k_lp_row<T, 1, true><<<rows, 64, 0, s>>>(a, z) : k_lp_row<T, 1, false><<<rows, 64, 0, s>>>(a, z);
         else if (a.vocab <= 16384 && a.top <= 64)
-            k_lp_row<T, 4><<<rows, 256, 0, s>>>(a, z);
+            once ? k_lp_row<T, 4, true><<<rows, 256, 0, s>>>(a, z) : k_lp_row<T, 4, false><<<rows, 256, 0, s>>>(a, z);
         else
-            k_lp_row<T, 8><<<rows, 512, 0, s>>>(a, z);
+            once ? k_lp_row<T, 8, true><<<rows, 512, 0, s>>>(a, z) : k_lp_row<T, 8, false><<<rows, 512, 0, s>>>(a, z);
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
@@ -446,29 +442,35 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     return SGC_OK;
 }
 
-template <typename T, int NW>
+template <typename T, int NW, bool ENT>
 static int logprobs_back(const LogprobArgs& a, const T* z, const float* stats, const float* entropy,
                          const float* dlogp, const float* dentropy, T* dz, int64_t dzs, int chunk, hipStream_t s)
 {
     const int chunks = (int)cdiv(a.vocab, chunk);
     const dim3 grid = row_grid(a.rows * chunks);
-    if (dentropy)
-        k_lp_back<T, NW, true><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk, chunks);
+    if (2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes)
+        k_lp_back<T, NW, ENT, true><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk,
+                                                             chunks);
     else
-        k_lp_back<T, NW, false><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk, chunks);
+        k_lp_back<T, NW, ENT, false><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk,
+                                                              chunks);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
 
 template <typename T>
-static int logprobs_back(const sgc_logprob_opts* o, const void* z, int64_t zs, const void* tokens, const float* stats,
-                         const float* entropy, const float* dlogp, const float* dentropy, void* dz, int64_t dzs,
-                         hipStream_t s)
+static int logprobs_back(const sgc_logprob_opts* o, const void* zv, int64_t zs, const void* tokens,
+                         const float* stats, const float* entropy, const float* dlogp, const float* dentropy,
+                         void* dzv, int64_t dzs, hipStream_t s)
 {
     const LogprobArgs a = logprob_args(o, zs, tokens);
-    return a.vocab <= 2048
-               ? logprobs_back<T, 1>(a, (const T*)z, stats, entropy, dlogp, dentropy, (T*)dz, dzs, 2048, s)
-               : logprobs_back<T, 4>(a, (const T*)z, stats, entropy, dlogp, dentropy, (T*)dz, dzs, 8192, s);
+    const T* z = (const T*)zv;
+    T* dz = (T*)dzv;
+    if (a.vocab <= 2048)
+        return dentropy ? logprobs_back<T, 1, true>(a, z, stats, entropy, dlogp, dentropy, dz, dzs, 2048, s)
+                        : logprobs_back<T, 1, false>(a, z, stats, entropy, dlogp, dentropy, dz, dzs, 2048, s);
+    return dentropy ? logprobs_back<T, 4, true>(a, z, stats, entropy, dlogp, dentropy, dz, dzs, 8192, s)
+                    : logprobs_back<T, 4, false>(a, z, stats, entropy, dlogp, dentropy, dz, dzs, 8192, s);
 }
 
 }  // namespace sgc
