@@ -228,8 +228,8 @@ __device__ inline void keep_packed(Raw (&q)[NV])
 // z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
 // which the sums are freed from once a row (lm_softmax.h); a maximum far from
 // zero takes z - M first.
-template <typename T, int NW, int NV, bool TAIL, bool ONCE>
-__global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T* z, T* dz)
+template <typename T, int NW, int NV, bool TAIL, bool ONCE, bool HEAD>
+__global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(DistillArgs a, const T* z, T* dz)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
     static_assert(NT >= SGC_TOP_MAX, "one entry a thread");
@@ -238,7 +238,14 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
     const T* zr = z + r * a.zs;
+    // HEAD: vectors are counted from a 128-byte line of the output (where its
+    // row starts at a vector of one), so that the waves write whole lines.
+    T* out = dz + r * a.dzs;
     const int tid = threadIdx.x, nv = a.vocab / VL;
+    const int head = HEAD && !((uintptr_t)out & 15) ? (int)(((uintptr_t)out & 127) >> 4) : 0;
+    const int first = tid - head;
+    const auto vec = [&](int n) { return first + n * NT; };
+    const auto held = [&](int n) { return (!HEAD || n > 0 || first >= 0) && n * NT < nv - first; };
     const float g = a.dloss ? a.dloss[r] : 1.f;
     int32_t at = -1;
     float v = -INFINITY;
@@ -248,7 +255,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     }
     Raw q[NV];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) q[n] = tid + n * NT < nv ? load_row<ONCE>((const Raw*)zr + tid + n * NT) : raw_low<T>();
+    for (int n = 0; n < NV; ++n) q[n] = held(n) ? load_row<ONCE>((const Raw*)zr + vec(n)) : raw_low<T>();
     const int last = nv * VL + tid;
     const float z_last = last < a.vocab ? to_f(zr[last]) : -INFINITY;
     // the entries: marks, T and u
@@ -291,7 +298,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
         float x[VL];
         unpack<T>(q[n], x);
         if (TAIL) {
-            const uint32_t skip = tid + n * NT < nv ? vec_bits<VL>(bm, tid + n * NT) : 0u;
+            const uint32_t skip = held(n) ? vec_bits<VL>(bm, vec(n)) : 0u;
             if (skip) {
 #pragma unroll
                 for (int e = 0; e < VL; ++e) x[e] = (skip >> e) & 1u ? -INFINITY : x[e];
@@ -327,7 +334,6 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
         }
         if (bad && a.dstatus) atomicOr(a.dstatus, SGC_STATUS_CORRUPT);
     }
-    T* out = dz + r * a.dzs;
     if (skip || g == 0.f) {
         write_zeros<T, NW, ONCE>(out, 0, a.vocab);
         return;
@@ -336,7 +342,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
     factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        if (tid + n * NT < nv) {
+        if (held(n)) {
             float x[VL];
             unpack<T>(q[n], x);
             if (far) {
@@ -346,7 +352,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_held(DistillArgs a, const T
 #pragma unroll
                 for (int e = 0; e < VL; ++e) x[e] = exp2_fast(fmaf(x[e], a.c, -b)) * k_out;
             }
-            store_row<ONCE>((Raw*)out + tid + n * NT, pack<T>(x));
+            store_row<ONCE>((Raw*)out + vec(n), pack<T>(x));
         }
     }
     if (last < a.vocab) out[last] = from_f<T>(power(z_last) * k_out);
@@ -499,7 +505,7 @@ static DistillArgs distill_args(const sgc_distill_opts* o, int64_t zs, const int
 template <typename T>
 static int distill_grad(const DistillArgs& a, const float* stats, const T* z, T* dz, hipStream_t s)
 {
-    const bool once = 2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes;
+    const bool once = 2 * a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes;
     const int chunk = a.vocab <= 2048 ? 2048 : 8192, chunks = (int)cdiv(a.vocab, chunk);
     const dim3 grid = row_grid(a.rows * chunks);
     if (a.vocab <= 2048)
@@ -513,12 +519,16 @@ static int distill_grad(const DistillArgs& a, const float* stats, const T* z, T*
 }
 
 template <typename T, int NW, int NV, bool TAIL>
-static void distill_held(const DistillArgs& a, const T* z, T* dz, size_t lds, hipStream_t s)
+static void distill_held(const DistillArgs& a, const T* z, T* dz, bool head, size_t lds, hipStream_t s)
 {
-    if (2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes)
-        k_distill_held<T, NW, NV, TAIL, true><<<row_grid(a.rows), NW * 64, lds, s>>>(a, z, dz);
+    const bool once = 2 * a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes;
+    const dim3 rows = row_grid(a.rows);
+    if (once && head)
+        k_distill_held<T, NW, NV, TAIL, true, true><<<rows, NW * 64, lds, s>>>(a, z, dz);
+    else if (once)
+        k_distill_held<T, NW, NV, TAIL, true, false><<<rows, NW * 64, lds, s>>>(a, z, dz);
     else
-        k_distill_held<T, NW, NV, TAIL, false><<<row_grid(a.rows), NW * 64, lds, s>>>(a, z, dz);
+        k_distill_held<T, NW, NV, TAIL, false, false><<<rows, NW * 64, lds, s>>>(a, z, dz);
 }
 
 template <typename T, bool TAIL>
@@ -528,19 +538,21 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
     const dim3 rows = row_grid(a.rows);
     if (chunks == 1) {
         const size_t lds = (size_t)(a.vocab + 31) / 32 * 4;
-        const int nv = a.vocab / VecLen<T>::value;
+        // rows that start inside a 128-byte line have up to 7 vectors less room
+        const bool head = a.rows > 1 && a.dzs * sizeof(T) % 128 || (uintptr_t)dz % 128;
+        const int nv = a.vocab / VecLen<T>::value + (head ? 7 : 0);
         if (a.vocab <= 2048)
             k_distill_row<T, 1, TAIL><<<rows, 64, lds, s>>>(a, z, dz);
         else if (dz && nv <= 1024)
-            distill_held<T, 4, 4, TAIL>(a, z, dz, lds, s);
+            distill_held<T, 4, 4, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 2048)
-            distill_held<T, 4, 8, TAIL>(a, z, dz, lds, s);
+            distill_held<T, 4, 8, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 4096)
-            distill_held<T, 8, 8, TAIL>(a, z, dz, lds, s);
+            distill_held<T, 8, 8, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 8192)
-            distill_held<T, 8, 16, TAIL>(a, z, dz, lds, s);
+            distill_held<T, 8, 16, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 16384)
-            distill_held<T, 16, 16, TAIL>(a, z, dz, lds, s);
+            distill_held<T, 16, 16, TAIL>(a, z, dz, head, lds, s);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
         else

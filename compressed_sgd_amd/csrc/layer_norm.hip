@@ -384,7 +384,7 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
                                                                      o->eps);
     } else {
         const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
-        const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) > kCacheBytes;
+        const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
 #define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                 \
     k_norm<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, \
                                                                         cols, o->eps)
@@ -437,7 +437,7 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
         }
     } else if (dx || part) {
         const unsigned g = (unsigned)parts;
-        const bool once = (dx ? 3 : 2) * o->rows * cols * (int64_t)sizeof(T) > kCacheBytes;
+        const bool once = (dx ? 3 : 2) * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
 #define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                         \
     k_norm_back<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
                                                                              part, o->rows, cols)

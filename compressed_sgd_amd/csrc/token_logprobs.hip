@@ -417,7 +417,7 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     const int chunks = chunks_of(o);
     const dim3 rows = row_grid(o->rows);
     if (chunks == 1) {
-        const bool once = a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes;
+        const bool once = a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes;
         if (a.vocab <= 2048 && a.top <= 32)
             once ? k_lp_row<T, 1, true><<<rows, 64, 0, s>>>(a, z) : k_lp_row<T, 1, false><<<rows, 64, 0, s>>>(a, z);
         else if (a.vocab <= 16384 && a.top <= 64)
@@ -448,7 +448,7 @@ static int logprobs_back(const LogprobArgs& a, const T* z, const float* stats, c
 {
     const int chunks = (int)cdiv(a.vocab, chunk);
     const dim3 grid = row_grid(a.rows * chunks);
-    if (2 * a.rows * a.vocab * (int64_t)sizeof(T) > kCacheBytes)
+    if (2 * a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes)
         k_lp_back<T, NW, ENT, true><<<grid, NW * 64, 0, s>>>(a, stats, entropy, dlogp, dentropy, z, dz, dzs, chunk,
                                                              chunks);
     else
