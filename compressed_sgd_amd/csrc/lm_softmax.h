@@ -103,14 +103,15 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
         Raw q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
-        uint32_t skip = 0;
-        float x[U * VL];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (SKIP) skip |= vec_bits<VL>(bm, v + u * NT) << (u * VL);
-            unpack<T>(q[u], x + u * VL);
+        for (int u = 0; u < U; u += 2) {  // 16 (fp32: 8) elements at a time: 4 at a time take registers that cost a workgroup
+            float x[2 * VL];
+            unpack<T>(q[u], x);
+            unpack<T>(q[u + 1], x + VL);
+            uint32_t skip = 0;
+            if (SKIP) skip = vec_bits<VL>(bm, v + u * NT) | vec_bits<VL>(bm, v + (u + 1) * NT) << VL;
+            a.template add<2 * VL, ENT, SKIP>(x, c, skip);
         }
-        a.template add<U * VL, ENT, SKIP>(x, c, skip);
     }
     for (; v < nv; v += NT) {
         float x[VL];
@@ -177,7 +178,7 @@ __device__ inline Sums row_softmax(const T* z, int len, float c, const uint32_t*
     block_join<NW, ENT>(a, c, tmp);
     if (!is_far(a.m, c)) return {a.m, a.s, a.t};
     SoftSum<true> b;
-    stream_sums<T, NW * 64, 1, ENT, SKIP, ONCE>(z, len, c, bm, b);
+    stream_sums<T, NW * 64, 2, ENT, SKIP, ONCE>(z, len, c, bm, b);
     block_join<NW, ENT>(b, c, tmp);
     return {b.m, b.s, b.t};
 }
