@@ -173,6 +173,16 @@ __device__ inline float sum_of_lanes(float x)
     return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
+template <int N>
+__device__ inline float max_of_lanes(float x)
+{
+    if (N > 8) x = fmaxf(x, dpp_or<0x128, 0xf>(x, x));
+    if (N > 4) x = fmaxf(x, dpp_or<0x124, 0xf>(x, x));
+    if (N > 2) x = fmaxf(x, dpp_or<0x122, 0xf>(x, x));
+    if (N > 1) x = fmaxf(x, dpp_or<0x121, 0xf>(x, x));
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
 // Sum over a workgroup of NW waves, the same value in every thread; tmp
 // holds NW floats and is free again after the call.
 template <int NW>
@@ -182,9 +192,7 @@ __device__ inline float block_sum(float x, float* tmp)
     if (NW == 1) return x;
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
     __syncthreads();
-    float r = tmp[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) r += tmp[w];
+    const float r = sum_of_lanes<NW>(tmp[threadIdx.x % NW]);
     __syncthreads();
     return r;
 }
@@ -195,9 +203,7 @@ __device__ inline float block_max(float x, float* tmp)
     if (NW == 1) return x;
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
     __syncthreads();
-    float r = tmp[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) r = fmaxf(r, tmp[w]);
+    const float r = max_of_lanes<NW>(tmp[threadIdx.x % NW]);
     __syncthreads();
     return r;
 }

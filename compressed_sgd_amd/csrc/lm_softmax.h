@@ -103,6 +103,7 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
         Raw q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
+        __builtin_amdgcn_sched_barrier(0);  // all on their way before the first is waited for
 #pragma unroll
         for (int u = 0; u < U; u += 2) {  // 16 (fp32: 8) elements at a time: 4 at a time take registers that cost a workgroup
             float x[2 * VL];
@@ -143,16 +144,11 @@ __device__ inline void block_join(SoftSum<FAR>& a, float c, float (*tmp)[3])
             tmp[w][2] = t;
         }
         __syncthreads();
-        m = tmp[0][0];
-#pragma unroll
-        for (int i = 1; i < NW; ++i) m = fmaxf(m, tmp[i][0]);
-        s = t = 0.f;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const float di = SoftSum<FAR>::step(tmp[i][0], m, c), fi = exp2_fast(di);
-            s += tmp[i][1] * fi;
-            if (ENT) t += fmaf(di, tmp[i][1], tmp[i][2]) * fi;
-        }
+        const int i = threadIdx.x % NW;  // a wave's sums a lane
+        m = max_of_lanes<NW>(tmp[i][0]);
+        const float di = SoftSum<FAR>::step(tmp[i][0], m, c), fi = exp2_fast(di);
+        s = sum_of_lanes<NW>(tmp[i][1] * fi);
+        if (ENT) t = sum_of_lanes<NW>(fmaf(di, tmp[i][1], tmp[i][2]) * fi);
         __syncthreads();
     }
     if (!FAR) {

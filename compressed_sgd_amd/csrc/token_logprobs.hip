@@ -139,24 +139,26 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
         __syncthreads();
         if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
         __syncthreads();
-        // (thread, vector) pairs, and one more for its element past the vectors
-        const int per = (nv + NT - 1) / NT + 1, items = cd.threads * per;
-        for (int it = threadIdx.x; it < items; it += NT) {
-            const int f = it / per, v = it - f * per, th = (int)cd.peak[f];
-            const auto offer = [&](float x, int i) {
-                if (x >= low) {
-                    const int at = atomicAdd(&cd.n, 1);
-                    if (at < cd.kCap) cd.key[at] = order_key(x, (uint32_t)(first + i));
-                }
-            };
-            if (v == per - 1) {
-                const int i = nv * VL + th;
-                if (i < len) offer(to_f(z[i]), i);
-            } else if (th + v * NT < nv) {
-                const int at = th + v * NT;
-                const Pack<T, VL> q = ((const Pack<T, VL>*)z)[at];
+        // a wave takes a holding thread, its lanes that thread's vectors, and
+        // one more for the element past the vectors
+        const auto offer = [&](float x, int i) {
+            if (x >= low) {
+                const int at = atomicAdd(&cd.n, 1);
+                if (at < cd.kCap) cd.key[at] = order_key(x, (uint32_t)(first + i));
+            }
+        };
+        const int per = (nv + NT - 1) / NT;
+        for (int f = threadIdx.x >> 6; f < cd.threads; f += NW) {
+            const int th = (int)cd.peak[f];
+            for (int k = threadIdx.x & 63; k <= per; k += 64) {
+                const int at = th + k * NT;
+                if (k < per && at < nv) {
+                    float x[VL];
+                    unpack<T>(((const Raw*)z)[at], x);
 #pragma unroll
-                for (int e = 0; e < VL; ++e) offer(to_f(q.v[e]), at * VL + e);
+                    for (int e = 0; e < VL; ++e) offer(x[e], at * VL + e);
+                }
+                if (k == per && nv * VL + th < len) offer(to_f(z[nv * VL + th]), nv * VL + th);
             }
         }
         __syncthreads();
