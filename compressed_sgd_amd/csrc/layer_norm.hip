@@ -55,8 +55,14 @@ __device__ inline void load_weights(const W* w, int t, int cols, float none, flo
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int v = n * NTR + t;
+        if (w && (v + 1) * VL <= cols) {
+            const Pack<W, VL> q = ((const Pack<W, VL>*)w)[v];
 #pragma unroll
-        for (int e = 0; e < VL; ++e) out[n * VL + e] = w && v * VL + e < cols ? to_f(w[v * VL + e]) : none;
+            for (int e = 0; e < VL; ++e) out[n * VL + e] = to_f(q.v[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VL; ++e) out[n * VL + e] = w && v * VL + e < cols ? to_f(w[v * VL + e]) : none;
+        }
     }
 }
 

@@ -139,8 +139,7 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
         __syncthreads();
         if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
         __syncthreads();
-        // a wave takes a holding thread, its lanes that thread's vectors, and
-        // one more for the element past the vectors
+        // 2^g threads take a holding thread's vectors, and its element past them
         const auto offer = [&](float x, int i) {
             if (x >= low) {
                 const int at = atomicAdd(&cd.n, 1);
@@ -148,9 +147,11 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
             }
         };
         const int per = (nv + NT - 1) / NT;
-        for (int f = threadIdx.x >> 6; f < cd.threads; f += NW) {
+        int g = 0;
+        while (g < 6 && (1 << g) <= per) ++g;
+        for (int f = threadIdx.x >> g; f < cd.threads; f += NT >> g) {
             const int th = (int)cd.peak[f];
-            for (int k = threadIdx.x & 63; k <= per; k += 64) {
+            for (int k = threadIdx.x & ((1 << g) - 1); k <= per; k += 1 << g) {
                 const int at = th + k * NT;
                 if (k < per && at < nv) {
                     float x[VL];
@@ -251,60 +252,68 @@ __global__ __launch_bounds__(NW * 64) void k_lp_part(LogprobArgs a, const T* z, 
     }
 }
 
-// The chunks of a row joined.
+// The chunks of a row joined.  A call of few rows is a chain of trips to
+// memory: everything it may need of the first trip is asked for at once.
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, int chunks, const float* part,
                                                      const uint64_t* keys)
 {
-    constexpr int NT = NW * 64;
+    constexpr int NT = NW * 64, kFirst = 2;
     __shared__ Candidates<NW> cd;
     __shared__ float tmp[NW][3];
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
+    const uint64_t* kr = keys + r * chunks * a.top;
+    const int len = chunks * a.top;
+    uint64_t mine[kFirst];
+#pragma unroll
+    for (int e = 0; e < kFirst; ++e) mine[e] = e * NT + (int)threadIdx.x < len ? kr[e * NT + threadIdx.x] : 0;
     int64_t tok = -1;
     float z_tok = 0.f;
     if (threadIdx.x == 0 && a.logp) {
         tok = token_at(a.tokens, a.token_type, r);
         if (tok >= 0 && tok < a.vocab) z_tok = to_f(z[r * a.zs + tok]);
     }
-    const Sums sum = join_parts<NW, true>(part + 4 * r * chunks, chunks, a.c, tmp);
-    const float ln_s = logf(sum.s);
-    if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
-    if (!a.top) return;
-    // Each chunk has `top` keys that reach its last one (0 where it is short):
-    // keys below the largest of the chunks' last keys are not among the best.
-    const uint64_t* kr = keys + r * chunks * a.top;
-    const int len = chunks * a.top;
-    uint64_t bar = 0;
-    for (int k = threadIdx.x; k < chunks; k += NT) {
-        const uint64_t last = kr[(int64_t)(k + 1) * a.top - 1];
-        bar = bar > last ? bar : last;
-    }
     if (threadIdx.x == 0) {
         cd.n = 0;
         cd.floor = 0;
     }
-    __syncthreads();
-    if (bar) atomicMax((unsigned long long*)&cd.floor, (unsigned long long)bar);
-    __syncthreads();
-    bar = cd.floor;
-    for (int i = threadIdx.x; i < len; i += NT) {
-        const uint64_t k = kr[i];
-        if (k && k >= bar) {
-            const int at = atomicAdd(&cd.n, 1);
-            if (at < cd.kCap) cd.key[at] = k;
-        }
-    }
-    __syncthreads();
-    int n = cd.n;
-    if (n <= cd.kCap) {
-        rank_keys<NW>(cd, n, a.top);
-        n = n < a.top ? n : a.top;
-    } else {
+    const Sums sum = join_parts<NW, true>(part + 4 * r * chunks, chunks, a.c, tmp);
+    const float ln_s = logf(sum.s);
+    if (a.top) {
+        // Each chunk has `top` keys that reach its last one (0 where it is
+        // short): keys below the largest of the last keys are not among the best.
+        const auto is_last = [&](int i) { return i < len && (i + 1) % a.top == 0; };
+        uint64_t bar = 0;
+#pragma unroll
+        for (int e = 0; e < kFirst; ++e)
+            if (is_last(e * NT + threadIdx.x) && mine[e] > bar) bar = mine[e];
+        for (int i = kFirst * NT + threadIdx.x; i < len; i += NT)
+            if (is_last(i) && kr[i] > bar) bar = kr[i];
+        if (bar) atomicMax((unsigned long long*)&cd.floor, (unsigned long long)bar);
         __syncthreads();
-        n = top_in_order<NW>(cd, [&](int i) { return kr[i]; }, len, a.top);
+        bar = cd.floor;
+        const auto offer = [&](uint64_t k) {
+            if (k && k >= bar) {
+                const int at = atomicAdd(&cd.n, 1);
+                if (at < cd.kCap) cd.key[at] = k;
+            }
+        };
+#pragma unroll
+        for (int e = 0; e < kFirst; ++e) offer(mine[e]);
+        for (int i = kFirst * NT + threadIdx.x; i < len; i += NT) offer(kr[i]);
+        __syncthreads();
+        int n = cd.n;
+        if (n <= cd.kCap) {
+            rank_keys<NW>(cd, n, a.top);
+            n = n < a.top ? n : a.top;
+        } else {
+            __syncthreads();
+            n = top_in_order<NW>(cd, [&](int i) { return kr[i]; }, len, a.top);
+        }
+        for (int k = threadIdx.x; k < n; k += NT) write_top(a, r, k, cd.sorted[k], sum, ln_s);
     }
-    for (int k = threadIdx.x; k < n; k += NT) write_top(a, r, k, cd.sorted[k], sum, ln_s);
+    if (threadIdx.x == 0) finish_row(a, r, z_tok, tok, sum, ln_s);
 }
 
 // The gradient of a chunk of a row: e (A + B d) with d and e of the softmax's

@@ -15,7 +15,7 @@ from typing import Optional
 
 import torch
 
-from . import SGCError, _check, _on, _ptr, _stream, lib, workspace
+from . import SGCError, _check, _on, _stream, lib, workspace
 
 F32, BF16, F16 = 0, 1, 2
 NORM_ADD_GRADS = 1
@@ -60,9 +60,13 @@ def _declare(L) -> None:
 
 def _empty(stream, shape, dtype, device) -> torch.Tensor:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with _on(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
