@@ -98,8 +98,9 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
     constexpr int VL = VecLen<T>::value;
     const Raw* p = (const Raw*)z;
     const int nv = len / VL;
-    int v = threadIdx.x;
-    for (; v + (U - 1) * NT < nv; v += U * NT) {
+    int v0 = 0;  // the group's first vector
+    for (; v0 + U * NT <= nv; v0 += U * NT) {
+        const int v = v0 + threadIdx.x;
         Raw q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
@@ -114,10 +115,20 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
             a.template add<2 * VL, ENT, SKIP>(x, c, skip);
         }
     }
-    for (; v < nv; v += NT) {
-        float x[VL];
-        unpack<T>(load_row<ONCE>(p + v), x);
-        a.template add<VL, ENT, SKIP>(x, c, SKIP ? vec_bits<VL>(bm, v) : 0u);
+    if (v0 < nv) {  // fewer than U vectors a thread: one trip to memory for them too
+        const int v = v0 + threadIdx.x;
+        Raw q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = v + u * NT < nv ? load_row<ONCE>(p + v + u * NT) : raw_low<T>();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (v0 + u * NT < nv) {  // the same for all
+                float x[VL];
+                unpack<T>(q[u], x);
+                a.template add<VL, ENT, SKIP>(x, c, SKIP && v + u * NT < nv ? vec_bits<VL>(bm, v + u * NT) : 0u);
+            }
+        }
     }
     const int i = nv * VL + threadIdx.x;
     if (i < len) {
