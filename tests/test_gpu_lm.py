@@ -617,3 +617,126 @@ def test_top_list_of_a_teacher_is_what_distill_takes():
     # both sides' terms are below 16; their errors a few hundred U
     assert float(r.loss.abs().max()) < 16 * 400 * lm_ref.U
     assert float(r.dlogits.abs().max()) < 400 * lm_ref.U
+
+
+# ------------------------------------------------- large calls, many rows
+def big_rows(vocab, dtype, both=2):
+    """So many rows that a call moves more than the last-level cache holds."""
+    return (256 << 20) // (both * vocab * dtype.itemsize) + 3
+
+
+@pytest.mark.parametrize("vocab,dtype", [(5003, BF16), (20016, BF16), (50001, F16), (50008, BF16), (40004, F32),
+                                         (65536, BF16), (130072, BF16), (131072, BF16), (70001, F32)], ids=str)
+@pytest.mark.parametrize("tail", [False, True], ids=["renorm", "tail"])
+def test_large_distill(vocab, dtype, tail):
+    rows = big_rows(vocab, dtype)
+    announce(f"large distill {rows}x{vocab} {dtype} tail {tail}")
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = torch.empty(rows, vocab, dtype=dtype, device="cuda").normal_(0.0, 3.0, generator=g)
+    k, pick = 24, torch.tensor([0, 1, 2, 3, rows // 2, rows - 2, rows - 1])
+    idx, val = entries_for(z[:64].cpu(), k, 5, tail)
+    idx, val = [t.repeat(-(-rows // 64), 1)[:rows].contiguous() for t in (idx, val)]
+    dl = torch.rand(rows, generator=gen(2)) + 0.5
+    dl[2] = 0.0
+    mode = sgc.DISTILL_TAIL if tail else sgc.DISTILL_RENORM
+    r = sgc.distill(z, idx.cuda(), val.cuda(), mode=mode, dloss=dl.cuda())
+    b = sgc.distill_backward(z, idx.cuda(), val.cuda(), r.stats, dl.cuda(), mode=mode)
+    loss, d, tl, td = lm_ref.distill(z[pick].cpu(), idx[pick], val[pick], tail, 1.0, g=dl[pick])
+    close(r.loss[pick], loss, tl, "loss")
+    close(r.dlogits[pick], d, td, "dlogits", dtype)
+    close(b[pick], d, td, "dlogits of the backward call", dtype)
+    in_place = sgc.distill(z, idx.cuda(), val.cuda(), mode=mode, dloss=dl.cuda(), dlogits=z)
+    same_bits([in_place.dlogits, in_place.loss], [r.dlogits, r.loss], "in place")
+
+
+@pytest.mark.parametrize("vocab,dtype", [(1000, BF16), (20016, BF16), (50001, F16), (40004, F32), (131072, BF16)],
+                         ids=str)
+def test_large_logprobs(vocab, dtype):
+    rows = big_rows(vocab, dtype, 1)
+    announce(f"large logprobs {rows}x{vocab} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = torch.empty(rows, vocab, dtype=dtype, device="cuda").normal_(0.0, 3.0, generator=g)
+    z[1, ::2] = -INF
+    pick = torch.tensor([0, 1, 2, 3, rows // 2, rows - 2, rows - 1])
+    tok = tokens_for(rows, vocab, 3)
+    r = sgc.token_logprobs(z, tok.cuda(), top=20)
+    sm, (logp, H, at, tlp), (t_logp, t_H, t_tlp) = lm_ref.logprobs(z[pick].cpu(), tok[pick], 1.0, 20)
+    close(r.logp[pick], logp, t_logp, "logp")
+    close(r.entropy[pick], H, t_H, "entropy")
+    assert torch.equal(r.top_idx[pick].cpu().long(), at)
+    close(r.top_logp[pick], tlp, t_tlp, "top_logp")
+    gl, gh = torch.randn(rows, generator=gen(1)), torch.randn(rows, generator=gen(2))
+    gl[3] = gh[3] = 0.0
+    for h in (gh, None):
+        d = sgc.token_logprobs_backward(z, tok.cuda(), r.stats, r.entropy, gl.cuda(), None if h is None else h.cuda())
+        ref, tol = lm_ref.logprobs_backward(sm, tok[pick], gl[pick], None if h is None else h[pick])
+        close(d[pick], ref, tol, "dlogits", dtype)
+
+
+@pytest.mark.parametrize("cols,dtype", [(98, BF16), (650, F32), (1000, F16), (2048, BF16), (4099, BF16), (8192, F16),
+                                        (12000, BF16), (16384, F32), (20000, BF16)], ids=str)
+def test_large_norm(cols, dtype):
+    rows = big_rows(cols, dtype)
+    announce(f"large norm {rows}x{cols} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.empty(rows, cols, dtype=dtype, device="cuda").normal_(0.5, 1.5, generator=g)
+    dy = torch.empty(rows, cols, dtype=dtype, device="cuda").normal_(0.0, 1.0, generator=g)
+    w, b = torch.randn(cols, generator=gen(1)), torch.randn(cols, generator=gen(2))
+    pick = torch.tensor([0, 1, 2, 3, rows // 2, rows - 2, rows - 1])
+    r = sgc.layer_norm(x, w.cuda(), b.cuda())
+    (y, mean, rstd), (ty, tm, tr) = lm_ref.norm(x[pick].cpu(), w, b, 1e-5)
+    close(r.y[pick], y, ty, "y", dtype)
+    close(r.mean[pick], mean, tm, "mean")
+    close(r.rstd[pick], rstd, tr, "rstd")
+    gr = sgc.layer_norm_backward(dy, x, w.cuda(), r.mean, r.rstd)
+    (dx, _, _), (tdx, _, _) = lm_ref.norm_backward(dy[pick].cpu(), x[pick].cpu(), w, r.mean[pick], r.rstd[pick])
+    close(gr.dx[pick], dx, tdx, "dx", dtype)
+    # the sums over the rows, in 64 bits on the GPU: rows one after the other in a part, then the parts
+    dw, db, aw, ab, tw = (torch.zeros(cols, dtype=torch.float64, device="cuda") for _ in range(5))
+    for a in range(0, rows, 8192):
+        s = slice(a, a + 8192)
+        d64 = dy[s].double()
+        h = (x[s].double() - r.mean[s].double()[:, None]) * r.rstd[s].double()[:, None]
+        dw, db = dw + (d64 * h).sum(0), db + d64.sum(0)
+        aw, ab = aw + (d64 * h).abs().sum(0), ab + d64.abs().sum(0)
+        tw = tw + (d64.abs() * (2 * (x[s].double().abs() + r.mean[s].double().abs()[:, None])
+                                * r.rstd[s].double()[:, None] + h.abs())).sum(0)
+    deep = lm_ref.DEPTH + min(rows, 512) + rows // 64
+    close(gr.dweight, dw.cpu(), (lm_ref.U * ((deep + 2) * aw + tw)).cpu(), "dweight")
+    close(gr.dbias, db.cpu(), (lm_ref.U * deep * ab).cpu(), "dbias")
+    only = sgc.layer_norm_backward(dy, x, w.cuda(), r.mean, r.rstd, want_dx=False)
+    same_bits([only.dweight, only.dbias], [gr.dweight, gr.dbias], "sums alone")
+
+
+def test_more_rows_than_a_grid_line():
+    """Rows past 2^20, where the grid gets a second line; every row is checked."""
+    rows, V = (1 << 20) + 3, 5
+    announce(f"{rows} rows of {V}")
+    z = torch.randn(rows, V, generator=gen(1)) * 3
+    check_logprobs(z, tokens_for(rows, V, 2), 1.0, 2)
+    idx = torch.stack([torch.randint(0, 2, (rows,), generator=gen(3)),
+                       torch.randint(2, V, (rows,), generator=gen(4))], 1).int()
+    val = torch.log_softmax(torch.randn(rows, 3, generator=gen(5)), 1)[:, :2].contiguous()
+    check_distill(z, idx, val, True)
+    r = sgc.layer_norm(z.cuda())
+    (y, _, _), (ty, _, _) = lm_ref.norm(z, None, None, 1e-5)
+    close(r.y, y, ty, "y")
+
+
+@pytest.mark.parametrize("vocab", [98, 5003, 150001])
+def test_distill_ignores_what_absent_entries_hold(vocab):
+    rows = 600 if vocab < 6000 else 4
+    announce(f"distill: NaN and infinities in absent entries, {rows}x{vocab}")
+    z = torch.randn(rows, vocab, generator=gen(vocab)).cuda()
+    for tail in (False, True):
+        idx, val = entries_for(z.cpu(), 12, 7, tail)
+        idx[:, 5] = -1
+        mode = sgc.DISTILL_TAIL if tail else sgc.DISTILL_RENORM
+        out = []
+        for junk in (0.0, NAN, INF, -INF):
+            val[:, 5] = junk
+            r = sgc.distill(z, idx.cuda(), val.cuda(), mode=mode, dloss=torch.ones(rows, device="cuda"))
+            assert torch.isfinite(r.loss).all()
+            out.append([r.loss, r.dlogits])
+        for o in out[1:]:
+            same_bits(o, out[0], "what an absent entry holds")
