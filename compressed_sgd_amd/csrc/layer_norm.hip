@@ -356,8 +356,9 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
 struct NormShape {
     int nwr, ept, rpb;
 };
-static NormShape norm_shape(int64_t cols)
+static NormShape norm_shape(int64_t cols, int32_t dtype)
 {
+    if (dtype == SGC_F32 && cols > 512 && cols <= 768) return {1, 12, 8};
     int nwr = 1;
     while (nwr < 16 && nwr * 512 < cols) nwr *= 2;
     return {nwr, nwr * 512 < cols ? 16 : 8, nwr < 8 ? 8 / nwr : 1};
@@ -366,7 +367,7 @@ static NormShape norm_shape(int64_t cols)
 // Workgroups that share out the rows: `waves` of them a compute unit.
 static int64_t norm_groups(const sgc_norm_opts* o, int waves)
 {
-    const NormShape sh = norm_shape(o->cols);
+    const NormShape sh = norm_shape(o->cols, o->dtype);
     const int64_t most = kCus * waves / (sh.nwr * sh.rpb), need = cdiv(o->rows, sh.rpb);
     return need < most ? need : most;
 }
@@ -405,8 +406,9 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
             else SGC_NORM_RUN(NWR, EPT, RPB, false, false);      \
         }                                                        \
     } while (0)
-        const NormShape sh = norm_shape(cols);
-        if (sh.ept == 16) SGC_NORM(16, 16, 1);
+        const NormShape sh = norm_shape(cols, o->dtype);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(1, 12, 8); }
+        else if (sh.ept == 16) SGC_NORM(16, 16, 1);
         else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
         else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
         else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
@@ -447,8 +449,9 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
 #define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                         \
     k_norm_back<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
                                                                              part, o->rows, cols)
-        const NormShape sh = norm_shape(cols);
-        if (sh.ept == 16) SGC_NORM(16, 16, 1);
+        const NormShape sh = norm_shape(cols, o->dtype);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(1, 12, 8); }
+        else if (sh.ept == 16) SGC_NORM(16, 16, 1);
         else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
         else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
         else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
