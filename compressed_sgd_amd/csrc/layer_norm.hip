@@ -6,7 +6,7 @@
 //   dw = sum_rows dy xh,  db = sum_rows dy
 //
 // A row stays in registers between its sums and its output: it is read once.
-// NWR waves share a row, EPT elements a thread; RPB rows go through a
+// NTR threads share a row, EPT elements each; RPB rows go through a
 // workgroup side by side, and a workgroup takes row after row, so that its
 // columns' weights are loaded once and their gradients' sums stay in its
 // registers; the next rows are on their way while one is worked on.  Rows too
@@ -66,36 +66,52 @@ __device__ inline void load_weights(const W* w, int t, int cols, float none, flo
     }
 }
 
-// Two sums over the NWR waves of a row, one barrier; tmp is another half at
-// every other call (`turn`), so the next call may write while this one reads.
-template <int NWR, int RPB>
-__device__ inline void row_sums(float& a, float& b, float (*tmp)[RPB][NWR][2], int turn)
+// A row's place among the RPB of its workgroup.
+template <int NTR>
+__device__ inline int row_place()
 {
-    a = wave_sum(a);
-    b = wave_sum(b);
-    if (NWR == 1) return;
-    const int wave = threadIdx.x >> 6, sub = wave / NWR, w = wave % NWR;
-    if ((threadIdx.x & 63) == 0) {
-        tmp[turn][sub][w][0] = a;
-        tmp[turn][sub][w][1] = b;
-    }
-    __syncthreads();
-    a = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][0]);
-    b = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][1]);
+    const int sub = threadIdx.x / NTR;
+    return NTR < 64 ? sub : __builtin_amdgcn_readfirstlane(sub);
 }
 
-template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG, bool ONCE>
-__global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
+// Two sums over the NTR threads of a row: 16 lanes, or whole waves with one
+// barrier; tmp is another half at every other call (`turn`), so the next call
+// may write while this one reads.
+template <int NTR, int RPB>
+using RowTmp = float[2][RPB][NTR < 64 ? 1 : NTR / 64][2];
+template <int NTR, int RPB>
+__device__ inline void row_sums(float& a, float& b, RowTmp<NTR, RPB>& tmp, int turn)
+{
+    if constexpr (NTR == 16) {
+        a = row16_sum(a);
+        b = row16_sum(b);
+    } else {
+        constexpr int NWR = NTR / 64;
+        a = wave_sum(a);
+        b = wave_sum(b);
+        if (NWR == 1) return;
+        const int wave = threadIdx.x >> 6, sub = wave / NWR, w = wave % NWR;
+        if ((threadIdx.x & 63) == 0) {
+            tmp[turn][sub][w][0] = a;
+            tmp[turn][sub][w][1] = b;
+        }
+        __syncthreads();
+        a = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][0]);
+        b = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][1]);
+    }
+}
+
+template <typename T, typename W, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
+__global__ __launch_bounds__(NTR* RPB) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
                                                         int64_t ys, float* mean, float* rstd, int64_t rows, int cols,
                                                         float eps)
 {
-    constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
-    __shared__ float tmp[2][RPB][NWR][2];
-    const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / NTR), t = threadIdx.x % NTR;
+    constexpr int VL = VecLen<T>::value, NV = EPT / VL;
+    __shared__ RowTmp<NTR, RPB> tmp;
+    const int sub = row_place<NTR>(), t = threadIdx.x % NTR;
     float wf[EPT], bf[EPT];
     load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
     load_weights<W, VL, NV, NTR>(b, t, cols, 0.f, bf);
-    const float inv = 1.f / (float)cols;
     Raw next[NV] = {};
     int64_t r = (int64_t)blockIdx.x * RPB + sub;
     const int64_t step = (int64_t)gridDim.x * RPB;
@@ -114,7 +130,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
         float s = 0.f, q = 0.f, none = 0.f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) s += f[i];
-        row_sums<NWR, RPB>(s, none, tmp, 0);
+        row_sums<NTR, RPB>(s, none, tmp, 0);
         const float m = s / (float)cols;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
@@ -123,7 +139,7 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
             if ((i / VL * NTR + t) * VL + i % VL < cols) q = fmaf(d, d, q);
         }
         none = 0.f;
-        row_sums<NWR, RPB>(q, none, tmp, 1);
+        row_sums<NTR, RPB>(q, none, tmp, 1);
         const float rs = 1.f / sqrtf(q / (float)cols + eps);
         if (r < rows) {
 #pragma unroll
@@ -140,14 +156,15 @@ __global__ __launch_bounds__(NWR* RPB * 64) void k_norm(const T* x, int64_t xs, 
 
 // dx, and the workgroup's sums of dy xh and dy over its rows: part
 // [workgroups, 2, cols].
-template <typename T, typename W, int NWR, int EPT, int RPB, bool RAG, bool ONCE>
-__global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) void k_norm_back(const T* dy, int64_t dys, const T* x, int64_t xs,
-                                                             const W* w, const float* mean, const float* rstd, T* dx,
-                                                             int64_t dxs, float* part, int64_t rows, int cols)
+template <typename T, typename W, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
+__global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_norm_back(const T* dy, int64_t dys, const T* x,
+                                                                            int64_t xs, const W* w, const float* mean,
+                                                                            const float* rstd, T* dx, int64_t dxs,
+                                                                            float* part, int64_t rows, int cols)
 {
-    constexpr int VL = VecLen<T>::value, NV = EPT / VL, NTR = NWR * 64;
-    __shared__ float tmp[2][RPB][NWR][2];
-    const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / NTR), t = threadIdx.x % NTR;
+    constexpr int VL = VecLen<T>::value, NV = EPT / VL;
+    __shared__ RowTmp<NTR, RPB> tmp;
+    const int sub = row_place<NTR>(), t = threadIdx.x % NTR;
     float wf[EPT], aw[EPT], ab[EPT];
     load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
 #pragma unroll
@@ -174,7 +191,7 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
         const bool live = r < rows;
         if (!kAhead && live) fetch(r);
         float h[EPT], g[EPT];
-        const float m = nm, rs = nr;
+        const float m = live ? nm : 0.f, rs = live ? nr : 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             unpack<T>(nx[n], h + n * VL);
@@ -182,7 +199,7 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
         }
         if (!live) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) h[i] = m, g[i] = 0.f;
+            for (int i = 0; i < EPT; ++i) h[i] = g[i] = 0.f;
         }
         if (kAhead && r + step < rows) fetch(r + step);
         float s1 = 0.f, s2 = 0.f;
@@ -196,7 +213,7 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
             s2 = fmaf(g[i], h[i], s2);
         }
         if (dx) {
-            row_sums<NWR, RPB>(s1, s2, tmp, turn);
+            row_sums<NTR, RPB>(s1, s2, tmp, turn);
             const float c1 = s1 / (float)cols, c2 = s2 / (float)cols;
             if (live) {
 #pragma unroll
@@ -207,16 +224,30 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
         }
     }
     if (!part) return;
-    // the rows side by side in the workgroup, one after the other
-    constexpr int kSum = RPB > 1 ? NTR * EPT : 1;
-    __shared__ float sw[2][kSum];
-    if (RPB > 1) {
-        for (int k = RPB - 1; k > 0; --k) {
+    // the rows side by side in a wave, then those (or the waves) side by side in
+    // the workgroup, one after the other
+    constexpr bool kFold = NTR < 64;
+    constexpr int kSums = kFold ? NTR * RPB / 64 : RPB;
+    if (kFold) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+#pragma unroll
+            for (int d = NTR; d < 64; d <<= 1) {
+                aw[i] += __shfl_xor(aw[i], d, 64);
+                ab[i] += __shfl_xor(ab[i], d, 64);
+            }
+        }
+    }
+    const int at = kFold ? threadIdx.x >> 6 : sub;
+    const bool mine = !kFold || (threadIdx.x & 63) < NTR;
+    __shared__ float sw[2][kSums > 1 ? NTR * EPT : 1];
+    if (kSums > 1) {
+        for (int k = kSums - 1; k > 0; --k) {
             __syncthreads();
-            if (sub == k) {
+            if (at == k && mine) {
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) {
-                    if (k < RPB - 1) {
+                    if (k < kSums - 1) {
                         aw[i] += sw[0][i * NTR + t];
                         ab[i] += sw[1][i * NTR + t];
                     }
@@ -226,7 +257,7 @@ __global__ __launch_bounds__(NWR* RPB * 64, EPT < 16 ? kBackwardWaves / 4 : 4) v
             }
         }
         __syncthreads();
-        if (sub) return;
+        if (at || !mine) return;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             aw[i] += sw[0][i * NTR + t];
@@ -351,24 +382,26 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
 }
 
 // The shape of a workgroup for rows of `cols` held elements: 8 elements a
-// thread (16 for the longest rows), as few waves a row as that takes, at least
-// 8 waves.
+// thread, in 16 lanes up to 128 columns and else in as few waves as that
+// takes; 16 in the longest rows; 12 in fp32 rows of 513 to 768, which one wave
+// then holds (20001 x 650 backward: 39 us, by two waves 42).  At least 8 waves.
 struct NormShape {
-    int nwr, ept, rpb;
+    int ntr, ept, rpb;
 };
 static NormShape norm_shape(int64_t cols, int32_t dtype)
 {
-    if (dtype == SGC_F32 && cols > 512 && cols <= 768) return {1, 12, 8};
-    int nwr = 1;
-    while (nwr < 16 && nwr * 512 < cols) nwr *= 2;
-    return {nwr, nwr * 512 < cols ? 16 : 8, nwr < 8 ? 8 / nwr : 1};
+    if (cols <= 128) return {16, 8, 32};
+    if (dtype == SGC_F32 && cols > 512 && cols <= 768) return {64, 12, 8};
+    int ntr = 64;
+    while (ntr < 1024 && ntr * 8 < cols) ntr *= 2;
+    return {ntr, ntr * 8 < cols ? 16 : 8, ntr < 512 ? 512 / ntr : 1};
 }
 
 // Workgroups that share out the rows: `waves` of them a compute unit.
 static int64_t norm_groups(const sgc_norm_opts* o, int waves)
 {
     const NormShape sh = norm_shape(o->cols, o->dtype);
-    const int64_t most = kCus * waves / (sh.nwr * sh.rpb), need = cdiv(o->rows, sh.rpb);
+    const int64_t most = kCus * waves * 64 / (sh.ntr * sh.rpb), need = cdiv(o->rows, sh.rpb);
     return need < most ? need : most;
 }
 
@@ -392,28 +425,29 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
     } else {
         const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
         const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
-#define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                 \
-    k_norm<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, \
+#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                 \
+    k_norm<T, W, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, \
                                                                         cols, o->eps)
 // rows of whole vectors or not, past the caches or not
-#define SGC_NORM(NWR, EPT, RPB)                                  \
+#define SGC_NORM(NTR, EPT, RPB)                                  \
     do {                                                         \
         if (cols % VecLen<T>::value) {                           \
-            if (once) SGC_NORM_RUN(NWR, EPT, RPB, true, true);   \
-            else SGC_NORM_RUN(NWR, EPT, RPB, true, false);       \
+            if (once) SGC_NORM_RUN(NTR, EPT, RPB, true, true);   \
+            else SGC_NORM_RUN(NTR, EPT, RPB, true, false);       \
         } else {                                                 \
-            if (once) SGC_NORM_RUN(NWR, EPT, RPB, false, true);  \
-            else SGC_NORM_RUN(NWR, EPT, RPB, false, false);      \
+            if (once) SGC_NORM_RUN(NTR, EPT, RPB, false, true);  \
+            else SGC_NORM_RUN(NTR, EPT, RPB, false, false);      \
         }                                                        \
     } while (0)
         const NormShape sh = norm_shape(cols, o->dtype);
-        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(1, 12, 8); }
-        else if (sh.ept == 16) SGC_NORM(16, 16, 1);
-        else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
-        else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
-        else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
-        else if (sh.nwr == 2) SGC_NORM(2, 8, 4);
-        else SGC_NORM(1, 8, 8);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(64, 12, 8); }
+        else if (sh.ept == 16) SGC_NORM(1024, 16, 1);
+        else if (sh.ntr == 1024) SGC_NORM(1024, 8, 1);
+        else if (sh.ntr == 512) SGC_NORM(512, 8, 1);
+        else if (sh.ntr == 256) SGC_NORM(256, 8, 2);
+        else if (sh.ntr == 128) SGC_NORM(128, 8, 4);
+        else if (sh.ntr == 64) SGC_NORM(64, 8, 8);
+        else SGC_NORM(16, 8, 32);
 #undef SGC_NORM_RUN
     }
     SGC_LAUNCH_CHECK();
@@ -446,17 +480,18 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
     } else if (dx || part) {
         const unsigned g = (unsigned)parts;
         const bool once = (dx ? 3 : 2) * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
-#define SGC_NORM_RUN(NWR, EPT, RPB, RAG, ONCE)                                                                         \
-    k_norm_back<T, W, NWR, EPT, RPB, RAG, ONCE><<<g, NWR * RPB * 64, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
+#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                         \
+    k_norm_back<T, W, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
                                                                              part, o->rows, cols)
         const NormShape sh = norm_shape(cols, o->dtype);
-        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(1, 12, 8); }
-        else if (sh.ept == 16) SGC_NORM(16, 16, 1);
-        else if (sh.nwr == 16) SGC_NORM(16, 8, 1);
-        else if (sh.nwr == 8) SGC_NORM(8, 8, 1);
-        else if (sh.nwr == 4) SGC_NORM(4, 8, 2);
-        else if (sh.nwr == 2) SGC_NORM(2, 8, 4);
-        else SGC_NORM(1, 8, 8);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(64, 12, 8); }
+        else if (sh.ept == 16) SGC_NORM(1024, 16, 1);
+        else if (sh.ntr == 1024) SGC_NORM(1024, 8, 1);
+        else if (sh.ntr == 512) SGC_NORM(512, 8, 1);
+        else if (sh.ntr == 256) SGC_NORM(256, 8, 2);
+        else if (sh.ntr == 128) SGC_NORM(128, 8, 4);
+        else if (sh.ntr == 64) SGC_NORM(64, 8, 8);
+        else SGC_NORM(16, 8, 32);
 #undef SGC_NORM
 #undef SGC_NORM_RUN
         SGC_LAUNCH_CHECK();

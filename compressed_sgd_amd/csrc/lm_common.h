@@ -173,6 +173,15 @@ __device__ inline float sum_of_lanes(float x)
     return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
+// The sum over each row of 16 lanes, the same bits in all of them.
+__device__ inline float row16_sum(float x)
+{
+    x += dpp_or<0x128, 0xf>(0.f, x);
+    x += dpp_or<0x124, 0xf>(0.f, x);
+    x += dpp_or<0x122, 0xf>(0.f, x);
+    x += dpp_or<0x121, 0xf>(0.f, x);
+    return x;
+}
 template <int N>
 __device__ inline float max_of_lanes(float x)
 {

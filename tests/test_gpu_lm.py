@@ -38,7 +38,7 @@ def same_bits(a, b, what):
 
 
 # --------------------------------------------------------------- layer norm
-NORM_SHAPES = [(1, 1), (3, 2), (5, 7), (2, 63), (1, 64), (9, 65), (33, 98), (4, 255), (130, 512), (7, 650),
+NORM_SHAPES = [(1, 1), (3, 2), (70, 100), (2049, 128), (33, 129), (5, 768), (5, 769), (5, 7), (2, 63), (1, 64), (9, 65), (33, 98), (4, 255), (130, 512), (7, 650),
                (300, 1000), (5, 1024), (3, 2047), (2, 2049), (600, 1031), (11, 4096), (6, 4099), (3, 8192), (2, 8200),
                (4, 16384), (2, 16385), (2, 40001), (1, 131075)]
 
