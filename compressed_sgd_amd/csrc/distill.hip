@@ -12,6 +12,8 @@
 
 namespace sgc {
 
+// The most vectors a row may have to be held in a workgroup's registers.
+constexpr int kMostHeld = 16384;
 // Rows are shared out in chunks of at most kChunkMax elements a workgroup
 // (its bitmap is 16 KB).
 constexpr int kChunkMax = 131072;
@@ -465,17 +467,18 @@ static bool entries_ok(const int32_t* idx, const float* val)
     return idx && val && lm_aligned(idx, 4) && lm_aligned(val, 4);
 }
 
-// How the rows are shared out.  One workgroup a row where the rows alone fill
-// the card; else chunks, so that there are about kWantBlocks workgroups, of at
-// least kChunkMin elements each.
-constexpr int64_t kWantBlocks = 512;
+// How the rows are shared out: one workgroup a row from kManyRows rows on (with
+// the gradient, where the row is held and a second reading saved, from
+// kManyHeld on); else chunks, so that there are about kWantBlocks workgroups,
+// of at least kChunkMin elements each.
+constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kManyHeld = 128;
 constexpr int kChunkMin = 4096;
 
 static int chunks_of(const sgc_distill_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    if (o->rows >= kWantBlocks) n = 1;
+    if (o->rows >= kManyRows) n = 1;
     if (n < cdiv(o->vocab, kChunkMax)) n = cdiv(o->vocab, kChunkMax);
     return (int)n;
 }
@@ -551,7 +554,7 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
             distill_held<T, 8, 8, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 8192)
             distill_held<T, 8, 16, TAIL>(a, z, dz, head, lds, s);
-        else if (dz && nv <= 16384)
+        else if (dz && nv <= kMostHeld)
             distill_held<T, 16, 16, TAIL>(a, z, dz, head, lds, s);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
@@ -580,7 +583,8 @@ static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const i
     a.loss = loss;
     a.stats = stats;
     a.dstatus = dstatus;
-    const int chunks = chunks_of(o);
+    int chunks = chunks_of(o);
+    if (dz && o->rows >= kManyHeld && o->vocab / VecLen<T>::value + 7 <= kMostHeld) chunks = 1;
     float* part = nullptr;
     if (chunks > 1) {
         Carver c(ws);

@@ -52,7 +52,6 @@ struct Candidates {
     uint32_t peak[NT];  // the threads' maxima as order keys, then the threads that hold candidates
     int n, threads;
     uint32_t bar;
-    uint64_t floor;
 };
 
 // sorted[0 .. min(n, top)) = the largest of key[0 .. n), largest first: each
@@ -104,6 +103,32 @@ __device__ inline int top_in_order(Candidates<NW>& cd, const K& key_at, int len,
     return n < top ? n : top;
 }
 
+// The largest value of 16 leading bits that `top` of the threads' keys reach (0
+// if there are fewer threads); clears the candidates.
+template <int NW>
+__device__ inline uint32_t bar_of(Candidates<NW>& cd, uint32_t key, int top)
+{
+    cd.peak[threadIdx.x] = key;
+    if (threadIdx.x == 0) cd.n = cd.threads = 0;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        uint32_t k[NW], bar = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) k[w] = cd.peak[w * 64 + threadIdx.x];
+        if (top <= NW * 64)
+            for (int b = 31; b >= 16; --b) {
+                const uint32_t to = bar | (1u << b);
+                int reach = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) reach += __popcll(__ballot(k[w] >= to));
+                if (reach >= top) bar = to;
+            }
+        if (threadIdx.x == 0) cd.bar = bar;
+    }
+    __syncthreads();
+    return cd.bar;
+}
+
 // The `top` best elements of z[0, len) into cd.sorted as order keys with their
 // places from `first` on.  m: the thread's maximum over its elements, those of
 // stream_sums.  Returns how many.
@@ -114,29 +139,9 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
     const auto key_at = [&](int i) { return order_key(to_f(z[i]), (uint32_t)(first + i)); };
     const int nv = len / VL;
     if (!broken) {
-        cd.peak[threadIdx.x] = order_key(m);
-        if (threadIdx.x == 0) cd.n = cd.threads = 0;
-        __syncthreads();
-        if (threadIdx.x < 64) {
-            // the largest value of 16 leading bits that `top` maxima reach
-            uint32_t k[NW], bar = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) k[w] = cd.peak[w * 64 + threadIdx.x];
-            if (top <= NT)
-                for (int b = 31; b >= 16; --b) {
-                    const uint32_t to = bar | (1u << b);
-                    int reach = 0;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) reach += __popcll(__ballot(k[w] >= to));
-                    if (reach >= top) bar = to;
-                }
-            if (threadIdx.x == 0) cd.bar = bar;
-        }
-        __syncthreads();
-        const uint32_t bar = cd.bar;
+        const uint32_t bar = bar_of<NW>(cd, order_key(m), top);
         const float low = bar < 0x00800000u ? -INFINITY : key_value(bar);
         const bool holds = m >= low;
-        __syncthreads();
         if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
         __syncthreads();
         // 2^g threads take a holding thread's vectors, and its element past them
@@ -274,34 +279,28 @@ __global__ __launch_bounds__(NW * 64) void k_lp_join(LogprobArgs a, const T* z, 
         tok = token_at(a.tokens, a.token_type, r);
         if (tok >= 0 && tok < a.vocab) z_tok = to_f(z[r * a.zs + tok]);
     }
-    if (threadIdx.x == 0) {
-        cd.n = 0;
-        cd.floor = 0;
-    }
     const Sums sum = join_parts<NW, true>(part + 4 * r * chunks, chunks, a.c, tmp);
     const float ln_s = logf(sum.s);
     if (a.top) {
-        // Each chunk has `top` keys that reach its last one (0 where it is
-        // short): keys below the largest of the last keys are not among the best.
-        const auto is_last = [&](int i) { return i < len && (i + 1) % a.top == 0; };
-        uint64_t bar = 0;
+        // the chunks' keys are cut as a row's elements are
+        uint64_t most = 0;
 #pragma unroll
-        for (int e = 0; e < kFirst; ++e)
-            if (is_last(e * NT + threadIdx.x) && mine[e] > bar) bar = mine[e];
-        for (int i = kFirst * NT + threadIdx.x; i < len; i += NT)
-            if (is_last(i) && kr[i] > bar) bar = kr[i];
-        if (bar) atomicMax((unsigned long long*)&cd.floor, (unsigned long long)bar);
-        __syncthreads();
-        bar = cd.floor;
+        for (int e = 0; e < kFirst; ++e) most = mine[e] > most ? mine[e] : most;
+        for (int i = kFirst * NT + threadIdx.x; i < len; i += NT) {
+            const uint64_t k = kr[i];
+            most = k > most ? k : most;
+        }
+        const uint32_t bar = bar_of<NW>(cd, (uint32_t)(most >> 32), a.top);
         const auto offer = [&](uint64_t k) {
-            if (k && k >= bar) {
+            if (k && (uint32_t)(k >> 32) >= bar) {
                 const int at = atomicAdd(&cd.n, 1);
                 if (at < cd.kCap) cd.key[at] = k;
             }
         };
 #pragma unroll
         for (int e = 0; e < kFirst; ++e) offer(mine[e]);
-        for (int i = kFirst * NT + threadIdx.x; i < len; i += NT) offer(kr[i]);
+        if ((uint32_t)(most >> 32) >= bar)
+            for (int i = kFirst * NT + threadIdx.x; i < len; i += NT) offer(kr[i]);
         __syncthreads();
         int n = cd.n;
         if (n <= cd.kCap) {
@@ -382,17 +381,17 @@ static bool tokens_ok(const sgc_logprob_opts* o, const void* tokens)
     return tokens && lm_aligned(tokens, o->token_type == SGC_TOKEN_I64 ? 8 : 4);
 }
 
-// How the rows are shared out: one workgroup a row where the rows alone fill
-// the card; else chunks, so that there are about kWantBlocks workgroups, of at
-// least kChunkMin elements each.
-constexpr int64_t kWantBlocks = 512;
+// How the rows are shared out: one workgroup a row from kManyRows rows on, which
+// fill the card alone; else chunks, so that there are about kWantBlocks
+// workgroups, of at least kChunkMin elements each.
+constexpr int64_t kWantBlocks = 1024, kManyRows = 512;
 constexpr int kChunkMin = 4096;
 
 static int chunks_of(const sgc_logprob_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    return o->rows >= kWantBlocks ? 1 : (int)n;
+    return o->rows >= kManyRows ? 1 : (int)n;
 }
 
 // Chunks start at a multiple of 64 elements.
@@ -448,7 +447,7 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     else
         k_lp_part<T, 8><<<parts, 512, 0, s>>>(a, z, chunk, used, part, keys);
     SGC_LAUNCH_CHECK();
-    k_lp_join<T, 4><<<rows, 256, 0, s>>>(a, z, used, part, keys);
+    k_lp_join<T, 8><<<rows, 512, 0, s>>>(a, z, used, part, keys);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
