@@ -467,18 +467,19 @@ static bool entries_ok(const int32_t* idx, const float* val)
     return idx && val && lm_aligned(idx, 4) && lm_aligned(val, 4);
 }
 
-// How the rows are shared out: one workgroup a row from kManyRows rows on (with
-// the gradient, where the row is held and a second reading saved, from
-// kManyHeld on); else chunks, so that there are about kWantBlocks workgroups,
-// of at least kChunkMin elements each.
-constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kManyHeld = 128;
+// How the rows are shared out.  With the gradient a row that can be held is: one
+// launch, one reading (1 x 50000 bf16: 15 us, in chunks 23).  Else one
+// workgroup a row from kManyRows rows on, which fill the card, and for rows up
+// to kShort, which take no longer than a second launch; and chunks for the
+// rest, about kWantBlocks workgroups of at least kChunkMin elements each.
+constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kShort = 65536;
 constexpr int kChunkMin = 4096;
 
 static int chunks_of(const sgc_distill_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    if (o->rows >= kManyRows) n = 1;
+    if (o->rows >= kManyRows || o->vocab <= kShort) n = 1;
     if (n < cdiv(o->vocab, kChunkMax)) n = cdiv(o->vocab, kChunkMax);
     return (int)n;
 }
@@ -558,8 +559,10 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
             distill_held<T, 16, 16, TAIL>(a, z, dz, head, lds, s);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
-        else
+        else if (a.rows >= kManyRows)
             k_distill_row<T, 8, TAIL><<<rows, 512, lds, s>>>(a, z, dz);
+        else
+            k_distill_row<T, 16, TAIL><<<rows, 1024, lds, s>>>(a, z, dz);
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
@@ -584,7 +587,7 @@ static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const i
     a.stats = stats;
     a.dstatus = dstatus;
     int chunks = chunks_of(o);
-    if (dz && o->rows >= kManyHeld && o->vocab / VecLen<T>::value + 7 <= kMostHeld) chunks = 1;
+    if (dz && o->vocab / VecLen<T>::value + 7 <= kMostHeld) chunks = 1;
     float* part = nullptr;
     if (chunks > 1) {
         Carver c(ws);

@@ -382,16 +382,17 @@ static bool tokens_ok(const sgc_logprob_opts* o, const void* tokens)
 }
 
 // How the rows are shared out: one workgroup a row from kManyRows rows on, which
-// fill the card alone; else chunks, so that there are about kWantBlocks
-// workgroups, of at least kChunkMin elements each.
-constexpr int64_t kWantBlocks = 1024, kManyRows = 512;
+// fill the card, and for rows up to kShort, which take no longer than a second
+// launch; else chunks, about kWantBlocks workgroups of at least kChunkMin
+// elements each.
+constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kShort = 65536;
 constexpr int kChunkMin = 4096;
 
 static int chunks_of(const sgc_logprob_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    return o->rows >= kManyRows ? 1 : (int)n;
+    return o->rows >= kManyRows || o->vocab <= kShort ? 1 : (int)n;
 }
 
 // Chunks start at a multiple of 64 elements.
@@ -432,6 +433,8 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
             once ? k_lp_row<T, 1, true><<<rows, 64, 0, s>>>(a, z) : k_lp_row<T, 1, false><<<rows, 64, 0, s>>>(a, z);
         else if (a.vocab <= 16384 && a.top <= 64)
             once ? k_lp_row<T, 4, true><<<rows, 256, 0, s>>>(a, z) : k_lp_row<T, 4, false><<<rows, 256, 0, s>>>(a, z);
+        else if (a.rows < kManyRows)
+            k_lp_row<T, 16, false><<<rows, 1024, 0, s>>>(a, z);
         else
             once ? k_lp_row<T, 8, true><<<rows, 512, 0, s>>>(a, z) : k_lp_row<T, 8, false><<<rows, 512, 0, s>>>(a, z);
         SGC_LAUNCH_CHECK();
