@@ -470,8 +470,10 @@ static bool entries_ok(const int32_t* idx, const float* val)
 // How the rows are shared out.  With the gradient a row that can be held is: one
 // launch, one reading (1 x 50000 bf16: 15 us, in chunks 23).  Else one
 // workgroup a row from kManyRows rows on, which fill the card, and for rows up
-// to kShort, which take no longer than a second launch; and chunks for the
-// rest, about kWantBlocks workgroups of at least kChunkMin elements each.
+// to kShort (twice that where every row has a compute unit of its own), which
+// take no longer than a second launch; and chunks for the rest, about
+// kWantBlocks workgroups of at least kChunkMin elements each (the loss of 150
+// x 131072: 15 us so, 17.7 in chunks; of 300 x 131072 24.3 and 22).
 constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kShort = 65536;
 constexpr int kChunkMin = 4096;
 
@@ -479,7 +481,7 @@ static int chunks_of(const sgc_distill_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    if (o->rows >= kManyRows || o->vocab <= kShort) n = 1;
+    if (o->rows >= kManyRows || o->vocab <= kShort * (o->rows <= 256 ? 2 : 1)) n = 1;
     if (n < cdiv(o->vocab, kChunkMax)) n = cdiv(o->vocab, kChunkMax);
     return (int)n;
 }
