@@ -136,35 +136,46 @@ template <typename T, int NW>
 __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first, int top, float m, bool broken)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
-    const auto key_at = [&](int i) { return order_key(to_f(z[i]), (uint32_t)(first + i)); };
     const int nv = len / VL;
     if (!broken) {
+        // A short row's vectors are too few for a filter: its elements then go
+        // to the threads one by one (4756 x 440 top 64: 60 us, else 97).
+        const bool single = nv < NT && nv < 4 * top;
+        if (single) {
+            m = -INFINITY;
+            for (int i = threadIdx.x; i < len; i += NT) m = fmaxf(m, to_f(z[i]));
+        }
         const uint32_t bar = bar_of<NW>(cd, order_key(m), top);
         const float low = bar < 0x00800000u ? -INFINITY : key_value(bar);
         const bool holds = m >= low;
-        if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
-        __syncthreads();
-        // 2^g threads take a holding thread's vectors, and its element past them
         const auto offer = [&](float x, int i) {
             if (x >= low) {
                 const int at = atomicAdd(&cd.n, 1);
                 if (at < cd.kCap) cd.key[at] = order_key(x, (uint32_t)(first + i));
             }
         };
-        const int per = (nv + NT - 1) / NT;
-        int g = 0;
-        while (g < 6 && (1 << g) <= per) ++g;
-        for (int f = threadIdx.x >> g; f < cd.threads; f += NT >> g) {
-            const int th = (int)cd.peak[f];
-            for (int k = threadIdx.x & ((1 << g) - 1); k <= per; k += 1 << g) {
-                const int at = th + k * NT;
-                if (k < per && at < nv) {
-                    float x[VL];
-                    unpack<T>(((const Raw*)z)[at], x);
+        if (single) {
+            if (holds)
+                for (int i = threadIdx.x; i < len; i += NT) offer(to_f(z[i]), i);
+        } else {
+            if (holds) cd.peak[atomicAdd(&cd.threads, 1)] = threadIdx.x;
+            __syncthreads();
+            // 2^g threads take a holding thread's vectors, and its element past them
+            const int per = (nv + NT - 1) / NT;
+            int g = 0;
+            while (g < 6 && (1 << g) <= per) ++g;
+            for (int f = threadIdx.x >> g; f < cd.threads; f += NT >> g) {
+                const int th = (int)cd.peak[f];
+                for (int k = threadIdx.x & ((1 << g) - 1); k <= per; k += 1 << g) {
+                    const int at = th + k * NT;
+                    if (k < per && at < nv) {
+                        float x[VL];
+                        unpack<T>(((const Raw*)z)[at], x);
 #pragma unroll
-                    for (int e = 0; e < VL; ++e) offer(x[e], at * VL + e);
+                        for (int e = 0; e < VL; ++e) offer(x[e], at * VL + e);
+                    }
+                    if (k == per && nv * VL + th < len) offer(to_f(z[nv * VL + th]), nv * VL + th);
                 }
-                if (k == per && nv * VL + th < len) offer(to_f(z[nv * VL + th]), nv * VL + th);
             }
         }
         __syncthreads();
@@ -175,7 +186,8 @@ __device__ inline int top_of(Candidates<NW>& cd, const T* z, int len, int first,
         }
         __syncthreads();
     }
-    return top_in_order<NW>(cd, key_at, len, top);
+    return top_in_order<NW>(
+        cd, [&](int i) { return order_key(to_f(z[i]), (uint32_t)(first + i)); }, len, top);
 }
 
 // What a row's sums give: logp, entropy, stats; ln s and the base of y.
@@ -432,7 +444,7 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
         const bool once = a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes;
         if (a.vocab <= 2048 && a.top <= 32)
             once ? k_lp_row<T, 1, true><<<rows, 64, 0, s>>>(a, z) : k_lp_row<T, 1, false><<<rows, 64, 0, s>>>(a, z);
-        else if (a.vocab <= 16384 && a.top <= 64)
+        else if (a.vocab <= 16384 && a.top <= (a.vocab <= 2048 ? 128 : 64))
             once ? k_lp_row<T, 4, true><<<rows, 256, 0, s>>>(a, z) : k_lp_row<T, 4, false><<<rows, 256, 0, s>>>(a, z);
         else if (a.rows < kManyRows)
             k_lp_row<T, 16, false><<<rows, 1024, 0, s>>>(a, z);
