@@ -21,7 +21,7 @@ constexpr int64_t kCus = 256;
 constexpr int kForwardWaves = 32, kBackwardWaves = 16;
 
 // Elements [v VL, v VL + VL) of a row that ends at cols; past it 0.  RAG: cols
-// is no multiple of VL.
+// may be no multiple of VL.
 template <typename T, bool RAG, bool ONCE>
 __device__ inline Raw load_raw(const T* p, int v, int cols)
 {
@@ -49,19 +49,26 @@ __device__ inline void store_raw(T* p, int v, int cols, const float* x)
     }
 }
 // EPT columns of a thread's weights as fp32; `none` where there are none.
-template <typename W, int VL, int NV, int NTR>
-__device__ inline void load_weights(const W* w, int t, int cols, float none, float* out)
+template <typename T, int NV, int NTR>
+__device__ inline void load_weights(const void* w, bool w32, int t, int cols, float none, float* out)
 {
+    constexpr int VL = VecLen<T>::value;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int v = n * NTR + t;
-        if (w && (v + 1) * VL <= cols) {
-            const Pack<W, VL> q = ((const Pack<W, VL>*)w)[v];
+        float* x = out + n * VL;
+        if (w && (v + 1) * VL <= cols && w32) {
+            const Pack<float, VL> q = ((const Pack<float, VL>*)w)[v];
 #pragma unroll
-            for (int e = 0; e < VL; ++e) out[n * VL + e] = to_f(q.v[e]);
+            for (int e = 0; e < VL; ++e) x[e] = q.v[e];
+        } else if (w && (v + 1) * VL <= cols) {
+            unpack<T>(((const Raw*)w)[v], x);
         } else {
 #pragma unroll
-            for (int e = 0; e < VL; ++e) out[n * VL + e] = w && v * VL + e < cols ? to_f(w[v * VL + e]) : none;
+            for (int e = 0; e < VL; ++e) {
+                const int c = v * VL + e;
+                x[e] = !w || c >= cols ? none : w32 ? ((const float*)w)[c] : to_f(((const T*)w)[c]);
+            }
         }
     }
 }
@@ -101,17 +108,17 @@ __device__ inline void row_sums(float& a, float& b, RowTmp<NTR, RPB>& tmp, int t
     }
 }
 
-template <typename T, typename W, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
-__global__ __launch_bounds__(NTR* RPB) void k_norm(const T* x, int64_t xs, const W* w, const W* b, T* y,
-                                                        int64_t ys, float* mean, float* rstd, int64_t rows, int cols,
-                                                        float eps)
+template <typename T, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
+__global__ __launch_bounds__(NTR* RPB) void k_norm(const T* x, int64_t xs, const void* w, const void* b,
+                                                   bool w32, T* y, int64_t ys, float* mean, float* rstd, int64_t rows,
+                                                   int cols, float eps)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL;
     __shared__ RowTmp<NTR, RPB> tmp;
     const int sub = row_place<NTR>(), t = threadIdx.x % NTR;
     float wf[EPT], bf[EPT];
-    load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
-    load_weights<W, VL, NV, NTR>(b, t, cols, 0.f, bf);
+    load_weights<T, NV, NTR>(w, w32, t, cols, 1.f, wf);
+    load_weights<T, NV, NTR>(b, w32, t, cols, 0.f, bf);
     Raw next[NV] = {};
     int64_t r = (int64_t)blockIdx.x * RPB + sub;
     const int64_t step = (int64_t)gridDim.x * RPB;
@@ -156,17 +163,18 @@ __global__ __launch_bounds__(NTR* RPB) void k_norm(const T* x, int64_t xs, const
 
 // dx, and the workgroup's sums of dy xh and dy over its rows: part
 // [workgroups, 2, cols].
-template <typename T, typename W, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
+template <typename T, int NTR, int EPT, int RPB, bool RAG, bool ONCE>
 __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_norm_back(const T* dy, int64_t dys, const T* x,
-                                                                            int64_t xs, const W* w, const float* mean,
-                                                                            const float* rstd, T* dx, int64_t dxs,
-                                                                            float* part, int64_t rows, int cols)
+                                                                            int64_t xs, const void* w, bool w32,
+                                                                            const float* mean, const float* rstd,
+                                                                            T* dx, int64_t dxs, float* part,
+                                                                            int64_t rows, int cols)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL;
     __shared__ RowTmp<NTR, RPB> tmp;
     const int sub = row_place<NTR>(), t = threadIdx.x % NTR;
     float wf[EPT], aw[EPT], ab[EPT];
-    load_weights<W, VL, NV, NTR>(w, t, cols, 1.f, wf);
+    load_weights<T, NV, NTR>(w, w32, t, cols, 1.f, wf);
 #pragma unroll
     for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
     Raw nx[NV] = {}, ny[NV] = {};
@@ -382,9 +390,12 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
 }
 
 // The shape of a workgroup for rows of `cols` held elements: 8 elements a
-// thread, in 16 lanes up to 128 columns and else in as few waves as that
-// takes; 16 in the longest rows; 12 in fp32 rows of 513 to 768, which one wave
-// then holds (20001 x 650 backward: 39 us, by two waves 42).  At least 8 waves.
+// thread, in 16 lanes up to 128 columns and else in as few waves as that takes
+// (a power of two); 16 in the longest rows.  Where that would leave a quarter
+// of the waves idle, 16-bit rows take half the waves and 16 elements a thread
+// (46153 x 1300 bf16 backward: 151 -> 103 us; in fp32 16 elements spill), and
+// fp32 rows of 513 to 768 one wave and 12 (20001 x 650 backward: 42 -> 39).
+// At least 8 waves.
 struct NormShape {
     int ntr, ept, rpb;
 };
@@ -392,9 +403,11 @@ static NormShape norm_shape(int64_t cols, int32_t dtype)
 {
     if (cols <= 128) return {16, 8, 32};
     if (dtype == SGC_F32 && cols > 512 && cols <= 768) return {64, 12, 8};
-    int ntr = 64;
+    int ntr = 64, ept = 8;
     while (ntr < 1024 && ntr * 8 < cols) ntr *= 2;
-    return {ntr, ntr * 8 < cols ? 16 : 8, ntr < 512 ? 512 / ntr : 1};
+    if (ntr * 8 < cols) ept = 16;
+    if (dtype != SGC_F32 && ntr > 64 && cols <= ntr * 6) ntr /= 2, ept = 16;
+    return {ntr, ept, ntr < 512 ? 512 / ntr : 1};
 }
 
 // Workgroups that share out the rows: `waves` of them a compute unit.
@@ -419,29 +432,38 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
     const W *w = (const W*)wv, *b = (const W*)bv;
     T* y = (T*)yv;
     const int cols = (int)o->cols;
+    const bool w32 = o->wdtype == SGC_F32;
     if (cols > kNormHeld) {
         k_norm_long<T, W><<<row_grid(o->rows), kLongThreads, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols,
                                                                      o->eps);
     } else {
         const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
         const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
-#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                 \
-    k_norm<T, W, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, \
-                                                                        cols, o->eps)
+#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                      \
+    k_norm<T, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(x, xs, wv, bv, w32, y, ys, mean, rstd, o->rows, cols, \
+                                                                o->eps)
 // rows of whole vectors or not, past the caches or not
-#define SGC_NORM(NTR, EPT, RPB)                                  \
-    do {                                                         \
-        if (cols % VecLen<T>::value) {                           \
-            if (once) SGC_NORM_RUN(NTR, EPT, RPB, true, true);   \
-            else SGC_NORM_RUN(NTR, EPT, RPB, true, false);       \
-        } else {                                                 \
-            if (once) SGC_NORM_RUN(NTR, EPT, RPB, false, true);  \
-            else SGC_NORM_RUN(NTR, EPT, RPB, false, false);      \
-        }                                                        \
+#define SGC_NORM(NTR, EPT, RPB)                                   \
+    do {                                                          \
+        if (cols % VecLen<T>::value) {                            \
+            if (once) SGC_NORM_RUN(NTR, EPT, RPB, true, true);    \
+            else SGC_NORM_RUN(NTR, EPT, RPB, true, false);        \
+        } else {                                                  \
+            if (once) SGC_NORM_RUN(NTR, EPT, RPB, false, true);   \
+            else SGC_NORM_RUN(NTR, EPT, RPB, false, false);       \
+        }                                                         \
     } while (0)
         const NormShape sh = norm_shape(cols, o->dtype);
-        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(64, 12, 8); }
-        else if (sh.ept == 16) SGC_NORM(1024, 16, 1);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) { SGC_NORM(64, 12, 8); } }
+        else if (sh.ept == 16 && sh.ntr == 1024) SGC_NORM(1024, 16, 1);
+        else if (sh.ept == 16) {
+            if constexpr (sizeof(T) == 2) {
+                if (sh.ntr == 512) SGC_NORM(512, 16, 1);
+                else if (sh.ntr == 256) SGC_NORM(256, 16, 2);
+                else if (sh.ntr == 128) SGC_NORM(128, 16, 4);
+                else SGC_NORM(64, 16, 8);
+            }
+        }
         else if (sh.ntr == 1024) SGC_NORM(1024, 8, 1);
         else if (sh.ntr == 512) SGC_NORM(512, 8, 1);
         else if (sh.ntr == 256) SGC_NORM(256, 8, 2);
@@ -463,6 +485,7 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
     const W* w = (const W*)wv;
     T* dx = (T*)dxv;
     const int cols = (int)o->cols;
+    const bool w32 = o->wdtype == SGC_F32;
     const int64_t parts = norm_parts(o);
     if (!o->rows) {
         // nothing to read
@@ -480,12 +503,20 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
     } else if (dx || part) {
         const unsigned g = (unsigned)parts;
         const bool once = (dx ? 3 : 2) * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
-#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                         \
-    k_norm_back<T, W, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(dy, dys, x, xs, w, mean, rstd, dx, dxs, \
-                                                                             part, o->rows, cols)
+#define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                     \
+    k_norm_back<T, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(dy, dys, x, xs, wv, w32, mean, rstd, dx, dxs, \
+                                                                     part, o->rows, cols)
         const NormShape sh = norm_shape(cols, o->dtype);
-        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) SGC_NORM(64, 12, 8); }
-        else if (sh.ept == 16) SGC_NORM(1024, 16, 1);
+        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) { SGC_NORM(64, 12, 8); } }
+        else if (sh.ept == 16 && sh.ntr == 1024) SGC_NORM(1024, 16, 1);
+        else if (sh.ept == 16) {
+            if constexpr (sizeof(T) == 2) {
+                if (sh.ntr == 512) SGC_NORM(512, 16, 1);
+                else if (sh.ntr == 256) SGC_NORM(256, 16, 2);
+                else if (sh.ntr == 128) SGC_NORM(128, 16, 4);
+                else SGC_NORM(64, 16, 8);
+            }
+        }
         else if (sh.ntr == 1024) SGC_NORM(1024, 8, 1);
         else if (sh.ntr == 512) SGC_NORM(512, 8, 1);
         else if (sh.ntr == 256) SGC_NORM(256, 8, 2);
