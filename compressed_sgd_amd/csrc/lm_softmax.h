@@ -106,7 +106,7 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
         for (int u = 0; u < U; ++u) q[u] = load_row<ONCE>(p + v + u * NT);
         __builtin_amdgcn_sched_barrier(0);  // all on their way before the first is waited for
 #pragma unroll
-        for (int u = 0; u < U; u += 2) {  // 16 (fp32: 8) elements at a time: 4 at a time take registers that cost a workgroup
+        for (int u = 0; u < U; u += 2) {  // two vectors at a time: four take registers that cost a workgroup
             float x[2 * VL];
             unpack<T>(q[u], x);
             unpack<T>(q[u + 1], x + VL);

@@ -15,7 +15,7 @@ from typing import Optional
 
 import torch
 
-from . import SGCError, _check, _on, _stream, lib, workspace
+from . import SGCError, _check, _on, lib, workspace
 
 F32, BF16, F16 = 0, 1, 2
 NORM_ADD_GRADS = 1
@@ -69,6 +69,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _stream(device: torch.device, stream) -> int:
+    """The handle of the call's stream (the current one's without the Stream object around it)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
     """Checks a 2-D device tensor of rows; its row stride."""
     if not t.is_cuda:
@@ -89,8 +94,15 @@ def _vec(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _vec1(t: Optional[torch.Tensor], name: str, n: int, dtype, device) -> None:
+    """_vec for one dimension of n elements."""
+    if t is not None and (t.numel() != n or t.dim() != 1 or t.dtype != dtype or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},) on {device}")
+
+
 def _status(t: Optional[torch.Tensor], device) -> None:
-    _vec(t, "status", (1,), torch.int32, device)
+    _vec1(t, "status", 1, torch.int32, device)
 
 
 def _scratch(need: int, ws: Optional[torch.Tensor], device, slot: str, stream, what: str) -> Optional[torch.Tensor]:
@@ -116,12 +128,12 @@ class NormGrads:
     dbias: Optional[torch.Tensor]     # float32 [cols]
 
 
-def _affine(weight, bias, x) -> int:
+def _affine(weight, bias, x, cols, dev) -> int:
     wdt = weight.dtype if weight is not None else bias.dtype if bias is not None else torch.float32
     if wdt != torch.float32 and wdt != x.dtype:
         raise ValueError("weight and bias must be float32 or the type of x")
-    _vec(weight, "weight", x.shape[1:], wdt, x.device)
-    _vec(bias, "bias", x.shape[1:], wdt, x.device)
+    _vec1(weight, "weight", cols, wdt, dev)
+    _vec1(bias, "bias", cols, wdt, dev)
     return _DTYPES[wdt]
 
 
@@ -129,9 +141,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                eps: float = 1e-5, out: Optional[torch.Tensor] = None, stream=None) -> Normalized:
     """Layer norm of every row of x [rows, cols]; out may be x."""
     xs = _rows(x, "x")
-    wdt = _affine(weight, bias, x)
     rows, cols = x.shape
     dev = x.device
+    wdt = _affine(weight, bias, x, cols, dev)
     if out is None:
         y, ys = _empty(stream, (rows, cols), x.dtype, dev), cols
     else:
@@ -158,12 +170,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     where none is given.  dx may be dy or x."""
     xs = _rows(x, "x")
     dys = _rows(dy, "dy", x)
-    wdt = _affine(weight, None, x)
     rows, cols = x.shape
     dev = x.device
+    wdt = _affine(weight, None, x, cols, dev)
     for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (dweight, "dweight", cols),
                        (dbias, "dbias", cols)):
-        _vec(t, name, (n,), torch.float32, dev)
+        _vec1(t, name, n, torch.float32, dev)
     if accumulate and (dweight is None or dbias is None):
         raise ValueError("accumulate needs dweight and dbias")
     if dx is None and want_dx:
@@ -174,11 +186,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     if dbias is None:
         dbias = _empty(stream, (cols,), torch.float32, dev)
     o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
-    need = lib().sgc_layer_norm_backward_workspace(C.byref(o))
+    L = lib()
+    need = L.sgc_layer_norm_backward_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "layer_norm", stream, "sgc_layer_norm_backward_workspace")
-    _check(lib().sgc_layer_norm_backward(C.byref(o), _ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(mean),
-                                         _ptr(rstd), _ptr(dx), dxs, _ptr(dweight), _ptr(dbias), _ptr(ws),
-                                         0 if ws is None else ws.numel(), _stream(dev, stream)),
+    _check(L.sgc_layer_norm_backward(C.byref(o), _ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(mean), _ptr(rstd),
+                                     _ptr(dx), dxs, _ptr(dweight), _ptr(dbias), _ptr(ws),
+                                     0 if ws is None else ws.numel(), _stream(dev, stream)),
            "sgc_layer_norm_backward")
     return NormGrads(dx, dweight, dbias)
 
@@ -193,13 +206,14 @@ class TokenLogprobs:
     top_logp: Optional[torch.Tensor]  # float32 [rows, top]
 
 
-def _tokens(tokens: Optional[torch.Tensor], logits: torch.Tensor) -> int:
+def _tokens(tokens: Optional[torch.Tensor], rows: int, device) -> int:
     if tokens is None:
         return TOKEN_I64
-    if tokens.dtype not in (torch.int32, torch.int64):
+    dt = tokens.dtype
+    if dt != torch.int64 and dt != torch.int32:
         raise ValueError("tokens must be int32 or int64")
-    _vec(tokens, "tokens", (logits.shape[0],), tokens.dtype, logits.device)
-    return TOKEN_I64 if tokens.dtype == torch.int64 else TOKEN_I32
+    _vec1(tokens, "tokens", rows, dt, device)
+    return TOKEN_I64 if dt == torch.int64 else TOKEN_I32
 
 
 def token_logprobs_workspace_bytes(rows: int, vocab: int, *, top: int = 0, dtype: torch.dtype = torch.float32) -> int:
@@ -218,9 +232,9 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     STATUS_BAD_INPUT for a token past the vocabulary, whose logp is NaN.
     """
     zs = _rows(logits, "logits")
-    tt = _tokens(tokens, logits)
     rows, vocab = logits.shape
     dev = logits.device
+    tt = _tokens(tokens, rows, dev)
     _status(status, dev)
     f32 = torch.float32
     if out is None:
@@ -235,11 +249,12 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
                                    (out.top_logp, "out.top_logp", (rows, top), f32)):
             _vec(t, name, shape, dt, dev)
     o = LogprobOpts(rows, vocab, _DTYPES[logits.dtype], tt, top, scale)
-    need = lib().sgc_token_logprobs_workspace(C.byref(o))
+    L = lib()
+    need = L.sgc_token_logprobs_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "token_logprobs", stream, "sgc_token_logprobs")
-    _check(lib().sgc_token_logprobs(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(out.logp), _ptr(out.entropy),
-                                    _ptr(out.stats), _ptr(out.top_idx), _ptr(out.top_logp), _ptr(status), _ptr(ws),
-                                    0 if ws is None else ws.numel(), _stream(dev, stream)), "sgc_token_logprobs")
+    _check(L.sgc_token_logprobs(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(out.logp), _ptr(out.entropy),
+                                _ptr(out.stats), _ptr(out.top_idx), _ptr(out.top_logp), _ptr(status), _ptr(ws),
+                                0 if ws is None else ws.numel(), _stream(dev, stream)), "sgc_token_logprobs")
     return out
 
 
@@ -250,16 +265,18 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor]
     """Gradient of the logits from those of logp and entropy (either may be
     None); stats and entropy are the forward call's.  dlogits may be logits."""
     zs = _rows(logits, "logits")
-    tt = _tokens(tokens, logits)
     rows, vocab = logits.shape
     dev = logits.device
+    tt = _tokens(tokens, rows, dev)
     f32 = torch.float32
     _vec(stats, "stats", (rows, 2), f32, dev)
     for t, name in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
-        _vec(t, name, (rows,), f32, dev)
+        _vec1(t, name, rows, f32, dev)
+    ds = vocab
     if dlogits is None:
         dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
-    ds = _rows(dlogits, "dlogits", logits)
+    else:
+        ds = _rows(dlogits, "dlogits", logits)
     o = LogprobOpts(rows, vocab, _DTYPES[logits.dtype], tt, 0, scale)
     _check(lib().sgc_token_logprobs_backward(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(stats), _ptr(entropy),
                                              _ptr(dlogp), _ptr(dentropy), _ptr(dlogits), ds, _stream(dev, stream)),
@@ -275,13 +292,13 @@ class Distilled:
     dlogits: Optional[torch.Tensor]
 
 
-def _entries(t_idx: torch.Tensor, t_val: torch.Tensor, logits: torch.Tensor) -> int:
+def _entries(t_idx: torch.Tensor, t_val: torch.Tensor, rows: int, device) -> int:
     if t_idx.dim() != 2:
         raise ValueError("t_idx must be 2-D [rows, top]")
-    shape = (logits.shape[0], t_idx.shape[1])
-    _vec(t_idx, "t_idx", shape, torch.int32, logits.device)
-    _vec(t_val, "t_val", shape, torch.float32, logits.device)
-    return t_idx.shape[1]
+    shape = (rows, t_idx.shape[1])
+    _vec(t_idx, "t_idx", shape, torch.int32, device)
+    _vec(t_val, "t_val", shape, torch.float32, device)
+    return shape[1]
 
 
 def distill_workspace_bytes(rows: int, vocab: int, top: int, *, dtype: torch.dtype = torch.float32) -> int:
@@ -301,22 +318,25 @@ def distill(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Tensor, *, m
     [1]) collects STATUS_CORRUPT for a row with a bad or repeated index.
     """
     zs = _rows(logits, "logits")
-    top = _entries(t_idx, t_val, logits)
     rows, vocab = logits.shape
     dev = logits.device
+    top = _entries(t_idx, t_val, rows, dev)
     _status(status, dev)
-    _vec(dloss, "dloss", (rows,), torch.float32, dev)
-    if dlogits is None and dloss is not None:
+    _vec1(dloss, "dloss", rows, torch.float32, dev)
+    ds = vocab
+    if dlogits is not None:
+        ds = _rows(dlogits, "dlogits", logits)
+    elif dloss is not None:
         dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
-    ds = _rows(dlogits, "dlogits", logits) if dlogits is not None else 0
     loss = _empty(stream, (rows,), torch.float32, dev)
     stats = _empty(stream, (rows, 4), torch.float32, dev)
     o = DistillOpts(rows, vocab, _DTYPES[logits.dtype], top, mode, scale, teacher_scale, 0)
-    need = lib().sgc_distill_workspace(C.byref(o))
+    L = lib()
+    need = L.sgc_distill_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "distill", stream, "sgc_distill")
-    _check(lib().sgc_distill(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(loss), _ptr(stats),
-                             _ptr(dloss), _ptr(dlogits), ds, _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
-                             _stream(dev, stream)), "sgc_distill")
+    _check(L.sgc_distill(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(loss), _ptr(stats),
+                         _ptr(dloss), _ptr(dlogits), ds, _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
+                         _stream(dev, stream)), "sgc_distill")
     return Distilled(loss, stats, dlogits)
 
 
@@ -326,14 +346,16 @@ def distill_backward(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Ten
     """Gradient of the logits from the rows' upstream gradients (None: 1) and
     the loss call's stats.  dlogits may be logits."""
     zs = _rows(logits, "logits")
-    top = _entries(t_idx, t_val, logits)
     rows, vocab = logits.shape
     dev = logits.device
+    top = _entries(t_idx, t_val, rows, dev)
     _vec(stats, "stats", (rows, 4), torch.float32, dev)
-    _vec(dloss, "dloss", (rows,), torch.float32, dev)
+    _vec1(dloss, "dloss", rows, torch.float32, dev)
+    ds = vocab
     if dlogits is None:
         dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
-    ds = _rows(dlogits, "dlogits", logits)
+    else:
+        ds = _rows(dlogits, "dlogits", logits)
     o = DistillOpts(rows, vocab, _DTYPES[logits.dtype], top, mode, scale, teacher_scale, 0)
     _check(lib().sgc_distill_backward(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(stats),
                                       _ptr(dloss), _ptr(dlogits), ds, _stream(dev, stream)), "sgc_distill_backward")

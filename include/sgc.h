@@ -460,8 +460,8 @@ int sgc_token_logprobs_backward(const sgc_logprob_opts* opt, const void* logits,
  * With dlogits the loss call gives the gradient too (dloss known before:
  * weights of the rows); without it (NULL) the loss alone, and
  * sgc_distill_backward gives the gradient from stats [rows, 4] = {max, sum of
- * exp(scale * (z - max)), that sum outside the entries, 1 or 0 if the row is
- * skipped}.  stats may be NULL.  dlogits may be logits, at the same address
+ * exp(scale * (z - max)), that sum outside the entries (SGC_DISTILL_TAIL; else
+ * any number), 1 or 0 if the row is skipped}.  stats may be NULL.  dlogits may be logits, at the same address
  * and stride.
  * Rows without an entry of t > 0 (SGC_DISTILL_RENORM) or whose logits are
  * all -inf are skipped: loss 0, gradient 0.  A row with an index >= vocab,
