@@ -560,6 +560,8 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
             distill_held<T, 4, 8, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 4096)
             distill_held<T, 8, 8, TAIL>(a, z, dz, head, lds, s);
+        else if (dz && nv <= 6656)  // 80 registers (bf16): three workgroups a compute unit, with 16 vectors two
+            distill_held<T, 8, 13, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 8192)
             distill_held<T, 8, 16, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= kMostHeld)
