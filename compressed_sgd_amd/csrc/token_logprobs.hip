@@ -446,8 +446,14 @@ static int logprobs(const sgc_logprob_opts* o, const void* zv, int64_t zs, const
     const dim3 rows = row_grid(o->rows);
     if (chunks == 1) {
         const bool once = a.rows * a.vocab * (int64_t)sizeof(T) >= kCacheBytes;
+        // As few waves a row as keep its chain of trips short: each has its share
+        // of the joins (8192 x 10000 bf16 top 5: 44 us by two, 49 by four, 71 by
+        // eight; 4096 x 50000 90 by eight, 107 by four).  A thread for four of
+        // the alternatives at least, so that the maxima are a filter.
         if (a.vocab <= 2048 && a.top <= 32)
             once ? k_lp_row<T, 1, true><<<rows, 64, 0, s>>>(a, z) : k_lp_row<T, 1, false><<<rows, 64, 0, s>>>(a, z);
+        else if (a.rows >= kManyRows && a.vocab / VecLen<T>::value <= 1536 && a.top <= 32)
+            once ? k_lp_row<T, 2, true><<<rows, 128, 0, s>>>(a, z) : k_lp_row<T, 2, false><<<rows, 128, 0, s>>>(a, z);
         else if (a.vocab <= 16384 && a.top <= (a.vocab <= 2048 ? 128 : 64))
             once ? k_lp_row<T, 4, true><<<rows, 256, 0, s>>>(a, z) : k_lp_row<T, 4, false><<<rows, 256, 0, s>>>(a, z);
         else if (a.rows < kManyRows)
