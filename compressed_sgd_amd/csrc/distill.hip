@@ -176,7 +176,7 @@ __device__ inline void factors(const DistillArgs& a, float g, float o, float s, 
 
 // A row a workgroup, vocab <= kChunkMax: loss, and with dz the gradient; the
 // row's second reading comes from the cache.  For the loss alone, and rows too
-// long to be held.  2000 x 10001 fp16 with the tail 14 us, one row's chain of
+// long to be held.  2000 x 10001 fp16 with the tail 13.6 us, one row's chain of
 // trips and barriers; 4096 x 50000 bf16 80 us, 5.1 TB/s.
 template <typename T, int NW, bool TAIL>
 __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T* z, T* dz)
@@ -231,9 +231,10 @@ __device__ inline void keep_packed(Raw (&q)[NV])
 // past the row is -inf).  One entry a thread.  The exponent is one fma,
 // z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
 // which the sums are freed from once a row (lm_softmax.h); a maximum far from
-// zero takes z - M first.  Bound by memory: 4096 x 50000 bf16 with the tail 160
-// us, 5.1 TB/s, by two workgroups a compute unit (one of 16 waves: 232); 4096 x
-// 131072 457 us, 4.7 TB/s, where a row takes half the unit's registers.
+// zero takes z - M first.  Bound by memory: 4096 x 50000 bf16 with the tail 154
+// us, 5.3 TB/s, by three workgroups a compute unit (by two 160, by one of 16
+// waves 232); 4096 x 131072 457 us, 4.7 TB/s, where a row takes half the unit's
+// registers.
 template <typename T, int NW, int NV, bool TAIL, bool ONCE, bool HEAD>
 __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(DistillArgs a, const T* z, T* dz)
 {
@@ -560,13 +561,13 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
             distill_held<T, 4, 8, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 4096)
             distill_held<T, 8, 8, TAIL>(a, z, dz, head, lds, s);
-        else if (dz && nv <= 6656)  // 80 registers (bf16): three workgroups a compute unit, with 16 vectors two
+        else if (dz && nv <= 6656)  // 80 registers (bf16), three workgroups a unit: 154 us; two at 16: 160
             distill_held<T, 8, 13, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= 8192)
             distill_held<T, 8, 16, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= kMostHeld)
             distill_held<T, 16, 16, TAIL>(a, z, dz, head, lds, s);
-        else if (a.rows >= kManyRows && nv <= 1536)  // the loss of 8000 x 10000 bf16: 39 us, by four waves 44
+        else if (a.rows >= kManyRows && nv <= 1536)  // the loss of 8000 x 10000 bf16: 39.5 us, by four waves 45
             k_distill_row<T, 2, TAIL><<<rows, 128, lds, s>>>(a, z, dz);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);

@@ -220,7 +220,7 @@ __device__ inline void write_top(const LogprobArgs& a, int64_t r, int k, uint64_
 }
 
 // A row a workgroup.  Bound by memory for long rows (4096 x 131072 bf16 top 8:
-// 186 us, 5.8 of the 6.25 TB/s of a bare read, the vector unit 82% busy), by
+// 184 us, 5.8 of the 6.25 TB/s of a bare read, the vector unit 82% busy), by
 // one row's chain of trips and barriers for few (4 x 50000 top 20: 11.6 us).
 template <typename T, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_lp_row(LogprobArgs a, const T* z)

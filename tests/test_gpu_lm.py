@@ -740,3 +740,20 @@ def test_distill_ignores_what_absent_entries_hold(vocab):
             out.append([r.loss, r.dlogits])
         for o in out[1:]:
             same_bits(o, out[0], "what an absent entry holds")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab,k", [(2049, 32), (5003, 5), (12288, 33)], ids=str)
+@pytest.mark.parametrize("kind", ["edges", "masked", "broken"])
+def test_many_short_rows(kind, vocab, k, dtype):
+    rows = 520
+    announce(f"{kind} {rows}x{vocab} top {k} {dtype}")
+    z = logits_for(rows, vocab, dtype, vocab, kind)
+    check_logprobs(z, tokens_for(rows, vocab, 3, torch.int32), 1.5, k)
+    for tail in (False, True):
+        idx, val = entries_for(z, k, k, tail, kind)
+        if kind != "broken":
+            # a teacher gives nothing to what its student may not say
+            hidden = z.float().gather(1, idx.long().clamp(min=0)) <= LOWEST[dtype] / 2
+            val = torch.where(hidden & (idx >= 0), -INF, val)
+        check_distill(z, idx, val, tail, scale=0.75)
