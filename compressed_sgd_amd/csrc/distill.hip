@@ -7,7 +7,10 @@
 //   dz_i = scale g ((T + u) q_i - u e_i / o)    else
 // The entries of a row are bits in shared memory: one look tells the vectors
 // that hold one, so that o is summed without them and not found by
-// subtraction, which loses it where the student has learnt its teacher.
+// subtraction, which loses it where the student has learnt its teacher.  There
+// o is small besides: with the tail the outside is measured from its own
+// maximum mo, so that its sum is at least 1 however far below m it lies, and
+// joins the entries' as o 2^-D, D = (m - mo) c.
 #include "lm_softmax.h"
 
 namespace sgc {
@@ -70,6 +73,45 @@ __device__ inline void load_entries(Entries& en, const DistillArgs& a, int64_t r
     }
 }
 
+// An outside this many powers of two below the row's maximum is one that a mask
+// has removed (2^-1074 is the smallest number of 64 bits): q = 0 there.
+constexpr float kGone = 1074.f;
+// Up to here the sum outside is kept at the row's maximum.
+constexpr float kNear = 32.f;
+
+// What a row's elements add up to: s = sum e at the maximum m, and the sum
+// outside the entries at m, times 2^k (k a whole number, 0 where it is near).
+struct Mass {
+    float m, s, o, k;
+};
+__device__ inline float log_outside(const Mass& w) { return logf(w.o) - w.k * kLn2; }
+
+// o: the sum outside at its own maximum, D powers of two below the row's.
+__device__ inline void place_outside(float o, float D, Mass* w)
+{
+    w->k = D < kNear ? 0.f : floorf(D);
+    w->o = o * exp2_fast(w->k - D);
+    if (o == 0.f || D > kGone) w->o = w->k = 0.f;
+}
+
+// The outside's maximum mo and sum o there (without the tail, the whole row's)
+// joined with the entries.
+template <int NW, bool TAIL>
+__device__ inline Mass row_mass(const Entries& en, const DistillArgs& a, float mo, float o, float* tmp)
+{
+    if (!TAIL) return {mo, o, o, 0.f};
+    constexpr int NT = NW * 64;
+    float mi = -INFINITY, in = 0.f;
+    for (int j = threadIdx.x; j < a.top; j += NT) mi = fmaxf(mi, en.z[j]);
+    Mass w;
+    w.m = fmaxf(mo, block_max<NW>(mi, tmp));
+    const float base = finite_base(w.m), D = (base - mo) * a.c;  // inf if nothing is outside
+    for (int j = threadIdx.x; j < a.top; j += NT) in += exp2_fast((en.z[j] - base) * a.c);
+    w.s = o * exp2_fast(-D) + block_sum<NW>(in, tmp);
+    place_outside(o, D, &w);
+    return w;
+}
+
 // Marks the entries inside [z0, z1) in the bitmap; whether one of the row's is
 // out of range or one of these repeated.  bm holds (z1 - z0 + 31) / 32 words.
 template <int NW>
@@ -90,11 +132,28 @@ __device__ inline bool mark_entries(const Entries& en, const DistillArgs& a, int
     return __syncthreads_or(bad) != 0;
 }
 
-// The gradient of the chunk [z0, z1): e_i k_out everywhere, then the entries'
+// Factors of the gradient: of e_i 2^up outside the entries, of e_i inside, of t.
+// u / o is at most 2 u: a smaller o is taken at a larger power of two.
+struct Factors {
+    float out, up, in, t;
+};
+__device__ inline Factors factors(const DistillArgs& a, float g, const Mass& w, float total, float u)
+{
+    const float k = a.scale * g, q = (total + u) / w.s;
+    Factors f = {k * q, 0.f, k * q, k};
+    if (u > 0.f && w.o > 0.f) {
+        const int e = w.o < 1.f ? -ilogbf(w.o) : 0;
+        f.up = w.k + (float)e;
+        f.out = k * (q * exp2_fast(-f.up) - u / ldexpf(w.o, e));
+    }
+    return f;
+}
+
+// The gradient of the chunk [z0, z1): the outside's everywhere, then the entries'
 // own values over it (every thread's stores are done at the barrier).
 template <typename T, int NW, int U, bool ONCE>
 __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, const T* zr, T* out, int z0, int z1,
-                                      float m, float k_out, float k_in, float k_t)
+                                      float m, const Factors& f)
 {
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
     const Raw* p = (const Raw*)(zr + z0);
@@ -104,7 +163,7 @@ __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, c
         float x[VL];
         unpack<T>(q, x);
 #pragma unroll
-        for (int e = 0; e < VL; ++e) x[e] = exp2_fast((x[e] - m) * a.c) * k_out;
+        for (int e = 0; e < VL; ++e) x[e] = exp2_fast(fmaf(x[e] - m, a.c, f.up)) * f.out;
         store_row<ONCE>(o + v, pack<T>(x));
     };
     int v = threadIdx.x;
@@ -117,12 +176,12 @@ __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, c
     }
     for (; v < nv; v += NT) one(load_row<ONCE>(p + v), v);
     const int i = z0 + nv * VL + threadIdx.x;
-    if (i < z1) out[i] = from_f<T>(exp2_fast((to_f(zr[i]) - m) * a.c) * k_out);
+    if (i < z1) out[i] = from_f<T>(exp2_fast(fmaf(to_f(zr[i]) - m, a.c, f.up)) * f.out);
     __syncthreads();
     for (int j = threadIdx.x; j < a.top; j += NT) {
         const int32_t at = en.idx[j];
         if (at >= z0 && at < z1)
-            out[at] = from_f<T>(exp2_fast((en.z[j] - m) * a.c) * k_in - expf(en.lt[j]) * k_t);
+            out[at] = from_f<T>(exp2_fast((en.z[j] - m) * a.c) * f.in - expf(en.lt[j]) * f.t);
     }
 }
 
@@ -136,42 +195,36 @@ __device__ inline void write_zeros(T* out, int z0, int z1)
     if (i < z1) out[i] = (T)0.f;
 }
 
+__device__ inline void write_stats(const DistillArgs& a, int64_t r, const Mass& w, bool skip)
+{
+    if (!a.stats) return;
+    a.stats[4 * r] = w.m;
+    a.stats[4 * r + 1] = w.s;
+    a.stats[4 * r + 2] = w.o;
+    a.stats[4 * r + 3] = skip ? 0.f : 1.f + w.k;
+}
+
 // Loss and stats of a row from its sums; whether its gradient is zero.
 template <int NW>
-__device__ inline bool finish_row(const Entries& en, const DistillArgs& a, int64_t r, float m, float o, float s,
-                                  float total, float u, bool bad, float* tmp)
+__device__ inline bool finish_row(const Entries& en, const DistillArgs& a, int64_t r, const Mass& w, float total,
+                                  float u, bool bad, float* tmp)
 {
     constexpr int NT = NW * 64;
-    const float ln_s = logf(s), base = finite_base(m);
+    const float ln_s = logf(w.s), base = finite_base(w.m);
     float l = 0.f;
     for (int j = threadIdx.x; j < a.top; j += NT) {
         const float lt = en.lt[j], t = expf(lt);
         if (t != 0.f) l += t * (lt - ((en.z[j] - base) * a.scale - ln_s));
     }
     l = block_sum<NW>(l, tmp);
-    if (u > 0.f && o != 0.f) l += u * (logf(u) - (logf(o) - ln_s));
-    const bool skip = bad || s == 0.f || (a.mode == SGC_DISTILL_RENORM && total == 0.f);
+    if (u > 0.f && w.o != 0.f) l += u * (logf(u) - (log_outside(w) - ln_s));
+    const bool skip = bad || w.s == 0.f || (a.mode == SGC_DISTILL_RENORM && total == 0.f);
     if (threadIdx.x == 0) {
         a.loss[r] = bad ? NAN : skip ? 0.f : l;
-        if (a.stats) {
-            a.stats[4 * r] = m;
-            a.stats[4 * r + 1] = s;
-            a.stats[4 * r + 2] = o;
-            a.stats[4 * r + 3] = skip ? 0.f : 1.f;
-        }
+        write_stats(a, r, w, skip);
         if (bad && a.dstatus) atomicOr(a.dstatus, SGC_STATUS_CORRUPT);
     }
     return skip;
-}
-
-// Factors of the gradient: exp2 terms outside and inside the entries, t.
-__device__ inline void factors(const DistillArgs& a, float g, float o, float s, float total, float u, float* k_out,
-                               float* k_in, float* k_t)
-{
-    const float k = a.scale * g, q = (total + u) / s;
-    *k_in = k * q;
-    *k_out = k * (q - (u > 0.f && o > 0.f ? u / o : 0.f));
-    *k_t = k;
 }
 
 // A row a workgroup, vocab <= kChunkMax: loss, and with dz the gradient; the
@@ -193,15 +246,8 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
     const bool bad = mark_entries<NW>(en, a, 0, a.vocab, bm);
     float own;
     const Sums sum = row_softmax<T, NW, false, TAIL, false>(zr, a.vocab, a.c, bm, tmj, &own);
-    const float base = finite_base(sum.m);
-    float s = sum.s, o = sum.s;
-    if (TAIL) {
-        float in = 0.f;
-        for (int j = threadIdx.x; j < a.top; j += NW * 64)
-            if (en.idx[j] >= 0 && en.idx[j] < a.vocab) in += exp2_fast((en.z[j] - base) * a.c);
-        s += block_sum<NW>(in, tmp);
-    }
-    const bool skip = finish_row<NW>(en, a, r, sum.m, o, s, total, u, bad, tmp);
+    const Mass w = row_mass<NW, TAIL>(en, a, sum.m, sum.s, tmp);
+    const bool skip = finish_row<NW>(en, a, r, w, total, u, bad, tmp);
     if (!dz) return;
     const float g = a.dloss ? a.dloss[r] : 1.f;
     T* out = dz + r * a.dzs;
@@ -209,9 +255,7 @@ __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T*
         write_zeros<T, NW, false>(out, 0, a.vocab);
         return;
     }
-    float k_out, k_in, k_t;
-    factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
-    write_gradient<T, NW, 4, false>(en, a, zr, out, 0, a.vocab, base, k_out, k_in, k_t);
+    write_gradient<T, NW, 4, false>(en, a, zr, out, 0, a.vocab, finite_base(w.m), factors(a, g, w, total, u));
 }
 
 // The held vectors are the same 16 bytes after this, but the compiler does not
@@ -226,12 +270,29 @@ __device__ inline void keep_packed(Raw (&q)[NV])
         for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(q[n].w[i]));
 }
 
+// -inf in the elements of q with a bit in `skip`.
+template <typename T>
+__device__ inline void remove(Raw& q, uint32_t skip)
+{
+    const Raw low = raw_low<T>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t gone;
+        if (sizeof(T) == 4)
+            gone = (skip >> i) & 1u ? 0xffffffffu : 0u;
+        else
+            gone = ((skip >> (2 * i)) & 1u ? 0xffffu : 0u) | ((skip >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+        q.w[i] = (q.w[i] & ~gone) | (low.w[i] & gone);
+    }
+}
+
 // A row a workgroup with loss and gradient in one reading: NV vectors of the
 // row stay in each thread's registers from the sums to the gradient (a vector
-// past the row is -inf).  One entry a thread.  The exponent is one fma,
-// z c - M c with M c rounded to b: every e is then too large by 2^(M c - b),
-// which the sums are freed from once a row (lm_softmax.h); a maximum far from
-// zero takes z - M first.  Bound by memory: 4096 x 50000 bf16 with the tail 154
+// past the row is -inf, and with the tail so is an entry, once marked).  One
+// entry a thread.  The exponent is one fma, z c - M c with M c rounded to b (M
+// the largest held): every e is then too large by 2^(M c - b), which the sums
+// are freed from once a row (lm_softmax.h); a maximum far from zero takes z - M
+// first.  Bound by memory: 4096 x 50000 bf16 with the tail 154
 // us, 5.3 TB/s, by three workgroups a compute unit (by two 160, by one of 16
 // waves 232); 4096 x 131072 457 us, 4.7 TB/s, where a row takes half the unit's
 // registers.
@@ -241,7 +302,7 @@ __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(Distil
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
     static_assert(NT >= SGC_TOP_MAX, "one entry a thread");
     extern __shared__ uint32_t bm[];
-    __shared__ float tmp[NW];
+    __shared__ float tmp[2 * NW];
     const int64_t r = row_of_block();
     if (r >= a.rows) return;
     const T* zr = z + r * a.zs;
@@ -264,7 +325,7 @@ __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(Distil
 #pragma unroll
     for (int n = 0; n < NV; ++n) q[n] = held(n) ? load_row<ONCE>((const Raw*)zr + vec(n)) : raw_low<T>();
     const int last = nv * VL + tid;
-    const float z_last = last < a.vocab ? to_f(zr[last]) : -INFINITY;
+    float z_last = last < a.vocab ? to_f(zr[last]) : -INFINITY;
     // the entries: marks, T and u
     const bool in_row = at >= 0 && at < a.vocab;
     const float z_in = in_row ? to_f(zr[at]) : -INFINITY;
@@ -277,40 +338,46 @@ __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(Distil
     float lt = v, total, u = 0.f;
     if (TAIL) {
         total = block_sum<NW>(expf(lt), tmp);
-        u = fmaxf(0.f, 1.f - total);
+        u = in_scalar(fmaxf(0.f, 1.f - total));
     } else {
         const float base = finite_base(block_max<NW>(v, tmp));
         const float sum = block_sum<NW>(expf(v - base), tmp);
         lt = (v - base) - (sum == 0.f ? 0.f : logf(sum));
         total = sum == 0.f ? 0.f : sum != sum ? sum : 1.f;
     }
-    const float t = expf(lt);
-    // the row's maximum and sums
-    float m = z_last;
+    // the held elements' maximum and sum
+    if (TAIL) {
+        if (last < a.vocab && (bm[last >> 5] >> (last & 31)) & 1u) z_last = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const uint32_t skip = held(n) ? vec_bits<VL>(bm, vec(n)) : 0u;
+            if (skip) remove<T>(q[n], skip);
+        }
+        keep_packed(q);
+    }
+    float mo = z_last, m = z_in;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         float x[VL];
         unpack<T>(q[n], x);
 #pragma unroll
-        for (int e = 0; e < VL; ++e) m = fmaxf(m, x[e]);
+        for (int e = 0; e < VL; ++e) mo = fmaxf(mo, x[e]);
     }
-    m = block_max<NW>(m, tmp);
+    if (TAIL) {
+        block_maxima<NW>(mo, m, tmp);
+        m = fmaxf(mo, m);
+    } else {
+        m = mo = block_max<NW>(mo, tmp);
+    }
     keep_packed(q);
-    const float base = finite_base(m), b = base * a.c;
-    const bool far = is_far(m, a.c);
-    const auto power = [&](float x) { return exp2_fast(far ? (x - base) * a.c : fmaf(x, a.c, -b)); };
+    m = in_scalar(m);
+    const float base = in_scalar(finite_base(mo)), b = in_scalar(base * a.c);
+    const bool far = is_far(mo, a.c);
     float o = 0.f, o2 = 0.f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         float x[VL];
         unpack<T>(q[n], x);
-        if (TAIL) {
-            const uint32_t skip = held(n) ? vec_bits<VL>(bm, vec(n)) : 0u;
-            if (skip) {
-#pragma unroll
-                for (int e = 0; e < VL; ++e) x[e] = (skip >> e) & 1u ? -INFINITY : x[e];
-            }
-        }
         if (far) {
 #pragma unroll
             for (int e = 0; e < VL; ++e) (e & 1 ? o2 : o) += exp2_fast((x[e] - base) * a.c);
@@ -319,34 +386,39 @@ __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(Distil
             for (int e = 0; e < VL; ++e) (e & 1 ? o2 : o) += exp2_fast(fmaf(x[e], a.c, -b));
         }
     }
-    if (last < a.vocab && !(TAIL && (bm[last >> 5] >> (last & 31)) & 1u)) o += power(z_last);
+    const float e_last = exp2_fast(far ? (z_last - base) * a.c : fmaf(z_last, a.c, -b));
     keep_packed(q);
-    o = block_sum<NW>(o + o2, tmp);
-    const float e_in = power(z_in);
-    float s = o;
-    if (TAIL) s += block_sum<NW>(in_row ? e_in : 0.f, tmp);
-    // loss: ln s of the sum freed from 2^(M c - b)
+    o += o2 + e_last;
+    // joined with the entries
+    asm volatile("" : "+v"(lt));  // t is taken here, not kept in a register through the loops
+    const float t = expf(lt);
+    const float e_in = exp2_fast((z_in - finite_base(m)) * a.c);
     const float free = far ? 1.f : exp2_fast(-fmaf(base, a.c, -b));
-    const float ln_s = logf(s * free);
-    float l = block_sum<NW>(t != 0.f ? t * (lt - ((z_in - base) * a.scale - ln_s)) : 0.f, tmp);
-    if (u > 0.f && o != 0.f) l += u * (logf(u) - (logf(o) - logf(s)));
-    const bool skip = bad || s == 0.f || (!TAIL && total == 0.f);
+    const float D = TAIL ? (finite_base(m) - mo) * a.c : 0.f, down = exp2_fast(-D);
+    float in = e_in;
+    if (TAIL)
+        block_sums<NW>(o, in, tmp);
+    else
+        o = block_sum<NW>(o, tmp);
+    o *= free;
+    Mass w = {m, TAIL ? fmaf(o, down, in) : o, o, 0.f};
+    if (TAIL) place_outside(o, D, &w);
+    const float ln_s = logf(w.s);
+    float l = block_sum<NW>(t != 0.f ? t * (lt - ((z_in - finite_base(m)) * a.scale - ln_s)) : 0.f, tmp);
+    if (u > 0.f && w.o != 0.f) l += u * (logf(u) - (log_outside(w) - ln_s));
+    const bool skip = bad || w.s == 0.f || (!TAIL && total == 0.f);
     if (tid == 0) {
         a.loss[r] = bad ? NAN : skip ? 0.f : l;
-        if (a.stats) {
-            a.stats[4 * r] = m;
-            a.stats[4 * r + 1] = s * free;
-            a.stats[4 * r + 2] = o * free;
-            a.stats[4 * r + 3] = skip ? 0.f : 1.f;
-        }
+        write_stats(a, r, w, skip);
         if (bad && a.dstatus) atomicOr(a.dstatus, SGC_STATUS_CORRUPT);
     }
     if (skip || g == 0.f) {
         write_zeros<T, NW, ONCE>(out, 0, a.vocab);
         return;
     }
-    float k_out, k_in, k_t;
-    factors(a, g, o, s, total, u, &k_out, &k_in, &k_t);
+    // as factors(), for elements measured from the largest held
+    const float k = a.scale * g, k_in = k * ((total + u) / w.s);
+    const float k_out = free * (k_in * down - (u > 0.f && w.o > 0.f ? k * (u / o) : 0.f));
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         if (held(n)) {
@@ -362,45 +434,33 @@ __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(Distil
             store_row<ONCE>((Raw*)out + vec(n), pack<T>(x));
         }
     }
-    if (last < a.vocab) out[last] = from_f<T>(power(z_last) * k_out);
+    if (last < a.vocab) out[last] = from_f<T>(e_last * k_out);
     __syncthreads();
-    if (in_row) out[at] = from_f<T>(e_in * k_in - t * k_t);
+    if (in_row) out[at] = from_f<T>(e_in * k_in - t * k);
 }
 
-// A chunk of a row: its maximum, sum outside the entries, sum of the entries,
-// and whether one is bad.  part [rows, chunks, 4].
+// A chunk of a row: maximum and sum outside the entries (without the tail, of
+// all), and whether an entry is bad.  part [rows, chunks, 3].
 template <typename T, int NW, bool TAIL>
 __global__ __launch_bounds__(NW * 64) void k_distill_part(DistillArgs a, const T* z, int chunk, int chunks,
                                                           float* part)
 {
     extern __shared__ uint32_t bm[];
     __shared__ Entries en;
-    __shared__ float tmp[NW];
     __shared__ float tmj[NW][3];
     const int64_t b = row_of_block(), r = b / chunks;
     if (r >= a.rows) return;
     const int z0 = (int)(b - r * chunks) * chunk, z1 = a.vocab - z0 < chunk ? a.vocab : z0 + chunk;
     const T* zr = z + r * a.zs;
-    for (int j = threadIdx.x; j < a.top; j += NW * 64) {
-        const int32_t at = a.idx[r * a.top + j];
-        en.idx[j] = at;
-        en.z[j] = at >= z0 && at < z1 ? to_f(zr[at]) : -INFINITY;
-    }
+    for (int j = threadIdx.x; j < a.top; j += NW * 64) en.idx[j] = a.idx[r * a.top + j];
     const bool bad = mark_entries<NW>(en, a, z0, z1, bm);
     float own;
     const Sums sum = row_softmax<T, NW, false, TAIL, false>(zr + z0, z1 - z0, a.c, bm, tmj, &own);
-    float in = 0.f;
-    if (TAIL) {
-        for (int j = threadIdx.x; j < a.top; j += NW * 64)
-            in += exp2_fast((en.z[j] - finite_base(sum.m)) * a.c);
-        in = block_sum<NW>(in, tmp);
-    }
     if (threadIdx.x == 0) {
-        float* p = part + 4 * b;
+        float* p = part + 3 * b;
         p[0] = sum.m;
         p[1] = sum.s;
-        p[2] = in;
-        p[3] = bad ? 1.f : 0.f;
+        p[2] = bad ? 1.f : 0.f;
     }
 }
 
@@ -414,24 +474,20 @@ __global__ __launch_bounds__(NW * 64) void k_distill_join(DistillArgs a, const T
     if (r >= a.rows) return;
     float total, u;
     load_entries<T, NW>(en, a, r, z + r * a.zs, 0, a.vocab, tmp, &total, &u);
-    const float* p = part + 4 * r * chunks;
+    const float* p = part + 3 * r * chunks;
     float m = -INFINITY;
     int bad = 0;
     for (int k = threadIdx.x; k < chunks; k += NW * 64) {
-        m = fmaxf(m, p[4 * k]);
-        bad |= p[4 * k + 3] != 0.f;
+        m = fmaxf(m, p[3 * k]);
+        bad |= p[3 * k + 2] != 0.f;
     }
     m = block_max<NW>(m, tmp);
     bad = __syncthreads_or(bad);
-    float o = 0.f, in = 0.f;
-    for (int k = threadIdx.x; k < chunks; k += NW * 64) {
-        const float f = exp2_fast(fmaxf((p[4 * k] - finite_base(m)) * a.c, kLowD));
-        o += p[4 * k + 1] * f;
-        in += p[4 * k + 2] * f;
-    }
+    float o = 0.f;
+    for (int k = threadIdx.x; k < chunks; k += NW * 64)
+        o += p[3 * k + 1] * exp2_fast(fmaxf((p[3 * k] - finite_base(m)) * a.c, kLowD));
     o = block_sum<NW>(o, tmp);
-    in = block_sum<NW>(in, tmp);
-    finish_row<NW>(en, a, r, m, o, TAIL ? o + in : o, total, u, bad != 0, tmp);
+    finish_row<NW>(en, a, r, row_mass<NW, TAIL>(en, a, m, o, tmp), total, u, bad != 0, tmp);
 }
 
 // The gradient of a chunk of a row from the row's stats.  Bound by memory: 4096 x
@@ -452,11 +508,11 @@ __global__ __launch_bounds__(NW * 64) void k_distill_grad(DistillArgs a, const f
         write_zeros<T, NW, ONCE>(out, z0, z1);
         return;
     }
-    float total, u, k_out, k_in, k_t;
+    float total, u;
     load_entries<T, NW>(en, a, r, zr, z0, z1, tmp, &total, &u);
     __syncthreads();  // the entries' logits are read before any of the chunk's gradient is written
-    factors(a, g, stats[4 * r + 2], stats[4 * r + 1], total, u, &k_out, &k_in, &k_t);
-    write_gradient<T, NW, 4, ONCE>(en, a, zr, out, z0, z1, finite_base(stats[4 * r]), k_out, k_in, k_t);
+    const Mass w = {stats[4 * r], stats[4 * r + 1], stats[4 * r + 2], stats[4 * r + 3] - 1.f};
+    write_gradient<T, NW, 4, ONCE>(en, a, zr, out, z0, z1, finite_base(w.m), factors(a, g, w, total, u));
 }
 
 static bool distill_opts_ok(const sgc_distill_opts* o)
@@ -603,7 +659,7 @@ static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const i
     float* part = nullptr;
     if (chunks > 1) {
         Carver c(ws);
-        part = c.take<float>(4 * o->rows * chunks);
+        part = c.take<float>(3 * o->rows * chunks);
         float* own = c.take<float>(4 * o->rows);
         if (!stats) stats = own;
     }
@@ -628,7 +684,7 @@ extern "C" size_t sgc_distill_workspace(const sgc_distill_opts* o)
     const int chunks = chunks_of(o);
     if (chunks == 1) return SGC_LM_WS_NONE;
     Carver c(nullptr);
-    c.take<float>(4 * o->rows * chunks);
+    c.take<float>(3 * o->rows * chunks);
     c.take<float>(4 * o->rows);
     return c.off;
 }

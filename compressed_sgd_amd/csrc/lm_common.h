@@ -139,6 +139,12 @@ __device__ inline float dpp_or(float old, float x)
 }
 __device__ inline float last_lane(float x) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63)); }
 
+// A value that is the same in all lanes, in a scalar register.
+__device__ inline float in_scalar(float x)
+{
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
 // Every lane of the wave must be active.
 __device__ inline float wave_sum(float x)
 {
@@ -215,6 +221,37 @@ __device__ inline float block_max(float x, float* tmp)
     const float r = max_of_lanes<NW>(tmp[threadIdx.x % NW]);
     __syncthreads();
     return r;
+}
+// Two at once; tmp holds 2 NW floats.
+template <int NW>
+__device__ inline void block_sums(float& x, float& y, float* tmp)
+{
+    x = wave_sum(x);
+    y = wave_sum(y);
+    if (NW == 1) return;
+    if ((threadIdx.x & 63) == 0) {
+        tmp[threadIdx.x >> 6] = x;
+        tmp[NW + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = sum_of_lanes<NW>(tmp[threadIdx.x % NW]);
+    y = sum_of_lanes<NW>(tmp[NW + threadIdx.x % NW]);
+    __syncthreads();
+}
+template <int NW>
+__device__ inline void block_maxima(float& x, float& y, float* tmp)
+{
+    x = wave_max(x);
+    y = wave_max(y);
+    if (NW == 1) return;
+    if ((threadIdx.x & 63) == 0) {
+        tmp[threadIdx.x >> 6] = x;
+        tmp[NW + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = max_of_lanes<NW>(tmp[threadIdx.x % NW]);
+    y = max_of_lanes<NW>(tmp[NW + threadIdx.x % NW]);
+    __syncthreads();
 }
 
 // Order of values as unsigned integers: -inf lowest, both zeros alike, NaN

@@ -23,6 +23,7 @@ __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // d below this has e = 0; keeps e * d and d * s away from 0 * inf.
 constexpr float kLowD = -1000.f;
+constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ inline float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -42,10 +43,14 @@ struct SoftSum {
         return fmaxf(FAR ? (from - finite_base(to)) * c : base_of(from, c) - base_of(to, c), kLowD);
     }
 
-    // N elements; those with a bit in `skip` count for the maximum alone.
+    // N elements; those with a bit in `skip` do not count.
     template <int N, bool ENT, bool SKIP>
     __device__ void add(float* x, float c, uint32_t skip)
     {
+        if (SKIP && skip) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = (skip >> i) & 1u ? -INFINITY : x[i];
+        }
         float g = x[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) g = fmaxf(g, x[i]);
@@ -54,10 +59,6 @@ struct SoftSum {
             if (ENT) t = fmaf(d, s, t) * f;
             s *= f;
             m = g;
-        }
-        if (SKIP && skip) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = (skip >> i) & 1u ? -INFINITY : x[i];
         }
         const float base = base_of(m, c), was = t;
         float s2 = 0.f, t2 = 0.f;  // two chains of additions

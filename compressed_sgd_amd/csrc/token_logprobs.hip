@@ -15,8 +15,6 @@
 
 namespace sgc {
 
-constexpr float kLn2 = 0.693147180559945309f;
-
 struct LogprobArgs {
     int64_t rows, zs;
     int32_t vocab, top, token_type;

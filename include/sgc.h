@@ -452,17 +452,22 @@ int sgc_token_logprobs_backward(const sgc_logprob_opts* opt, const void* logits,
  *   SGC_DISTILL_TAIL: v are log probabilities over the whole vocabulary, t =
  *     exp(v) (teacher_scale 1), u = max(0, 1 - sum(t)) is the rest;
  *     loss = sum(t * (log t - log q)) + u * (log u - log(1 - Q))
- *     where the last term is 0 if u = 0 or q = 0 everywhere outside.
+ *     where the last term is 0 if u = 0 or nothing is left outside: every
+ *     logit there is -inf, or so far below the row's maximum that exp(scale *
+ *     (z - max)) < 2^-1074 (a mask at the type's lowest value).
  * A term with t = 0 counts 0.  1 - Q is summed outside the entries, not
- * subtracted.  Gradient, times the row's upstream dloss (NULL: 1):
+ * subtracted, and from the largest logit outside: neither it nor the gradient
+ * is lost where the entries hold all that fp32 sees.  Gradient, times the row's upstream dloss (NULL: 1):
  *   dlogits_i = scale * dloss * ((sum(t) + u) * q_i - t_i)              entries
  *   dlogits_i = scale * dloss * ((sum(t) + u) * q_i - u * q_i / (1 - Q))  else
  * With dlogits the loss call gives the gradient too (dloss known before:
  * weights of the rows); without it (NULL) the loss alone, and
  * sgc_distill_backward gives the gradient from stats [rows, 4] = {max, sum of
- * exp(scale * (z - max)), that sum outside the entries (SGC_DISTILL_TAIL; else
- * any number), 1 or 0 if the row is skipped}.  stats may be NULL.  dlogits may be logits, at the same address
- * and stride.
+ * exp(scale * (z - max)), that sum outside the entries times 2^k
+ * (SGC_DISTILL_TAIL; else any number), 1 + k or 0 if the row is skipped}, k a
+ * whole number: 0, or where the largest logit outside lies 2^-32 and more below
+ * the maximum, that distance.  stats may be NULL.  dlogits may be logits, at
+ * the same address and stride.
  * Rows without an entry of t > 0 (SGC_DISTILL_RENORM) or whose logits are
  * all -inf are skipped: loss 0, gradient 0.  A row with an index >= vocab,
  * below -1 or given twice is skipped too: loss NaN, gradient 0 and, where
