@@ -175,7 +175,7 @@ __device__ inline void write_gradient(const Entries& en, const DistillArgs& a, c
         for (int u = 0; u < U; ++u) one(q[u], v + u * NT);
     }
     for (; v < nv; v += NT) one(load_row<ONCE>(p + v), v);
-    const int i = z0 + nv * VL + threadIdx.x;
+    const int64_t i = (int64_t)z0 + nv * VL + threadIdx.x;  // may pass 2^31
     if (i < z1) out[i] = from_f<T>(exp2_fast(fmaf(to_f(zr[i]) - m, a.c, f.up)) * f.out);
     __syncthreads();
     for (int j = threadIdx.x; j < a.top; j += NT) {
@@ -191,7 +191,7 @@ __device__ inline void write_zeros(T* out, int z0, int z1)
     constexpr int NT = NW * 64, VL = VecLen<T>::value;
     const int nv = (z1 - z0) / VL;
     for (int v = threadIdx.x; v < nv; v += NT) store_row<ONCE>((Raw*)(out + z0) + v, Raw{{0, 0, 0, 0}});
-    const int i = z0 + nv * VL + threadIdx.x;
+    const int64_t i = (int64_t)z0 + nv * VL + threadIdx.x;
     if (i < z1) out[i] = (T)0.f;
 }
 

@@ -1,0 +1,57 @@
+"""The language-model operators at the longest rows their options take."""
+import pytest
+import torch
+
+import compressed_sgd_amd as sgc
+import lm_ref
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+V = (1 << 31) - 1
+GUARD = 1024
+# all logits but these are -inf: sums of a handful of terms, wherever they lie
+PLACES = [0, 1, 63, 200, 400, 808, 1608, 8191, 8192, 1 << 20, (1 << 30) - 1, 1 << 30, (1 << 30) + 64, (1 << 30) + 328,
+          (1 << 30) + 808, (1 << 30) + 1608, V - 8193, V - 300, V - 9, V - 8, V - 7, V - 2, V - 1]
+
+
+def longest_row():
+    """A row of V between guards, and the logits at PLACES."""
+    buf = torch.full((GUARD + V + GUARD,), -float("inf"), dtype=BF16, device="cuda")
+    z = buf[GUARD:GUARD + V][None]
+    vals = (torch.randn(len(PLACES), generator=torch.Generator().manual_seed(1)) * 2).to(BF16)
+    z[0, torch.tensor(PLACES, device="cuda")] = vals.cuda()
+    buf[:GUARD], buf[GUARD + V:] = 100.0, 100.0  # read by mistake they would be the row's maximum
+    return buf, z, vals.double()
+
+
+def check_guards(buf):
+    assert (buf[:GUARD] == 100.0).all() and (buf[GUARD + V:] == 100.0).all()
+
+
+def test_distill_longest_row():
+    announce("distill 1x(2^31 - 1) bf16")
+    buf, z, vals = longest_row()
+    listed = [2, 11, len(PLACES) - 1]
+    idx = torch.tensor([[PLACES[k] for k in listed]], dtype=torch.int32)
+    val = torch.tensor([[-1.0, -2.0, -1.5]])
+    small = vals[None].to(BF16)
+    loss, d, tl, td = lm_ref.distill(small, torch.tensor([listed], dtype=torch.int32), val, True, 1.0)
+    obuf = torch.full_like(buf, 100.0)
+    out = obuf[GUARD:GUARD + V][None]
+    kw = dict(mode=sgc.DISTILL_TAIL, dlogits=out)
+    at = torch.tensor(PLACES, device="cuda")
+    r = sgc.distill(z, idx.cuda(), val.cuda(), **kw)
+    lm_ref.close(r.loss, loss, tl, "loss")
+    lm_ref.close(out[:, at], d, td, "dlogits", BF16)
+    assert int(torch.count_nonzero(out)) == len(PLACES)
+    check_guards(obuf)
+    obuf.fill_(100.0)
+    sgc.distill_backward(z, idx.cuda(), val.cuda(), r.stats, **kw)
+    lm_ref.close(out[:, at], d, td, "dlogits of the backward call", BF16)
+    check_guards(obuf)
+    obuf.fill_(100.0)
+    sgc.distill_backward(z, idx.cuda(), val.cuda(), r.stats, torch.zeros(1, device="cuda"), **kw)
+    assert int(torch.count_nonzero(out)) == 0
+    check_guards(obuf)
+    check_guards(buf)
