@@ -399,15 +399,19 @@ static bool tokens_ok(const sgc_logprob_opts* o, const void* tokens)
 // fill the card, and for rows up to kShort (twice that where every row has a
 // compute unit of its own), which take no longer than a second launch; else
 // chunks, about kWantBlocks workgroups of at least kChunkMin elements each.
-// 1 x 131072 top 20: 16 us so, 20 in chunks; 300 x 131072: 30.7 and 30.3.
-constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kShort = 65536;
+// 1 x 131072 top 20: 16 us so, 20 in chunks; 300 x 131072: 30.7 and 30.3.  No
+// workgroup takes more than kMostElements (but for a chunk's rounding): places
+// inside its part, and those its threads step to past the end, are 32 bits.
+constexpr int64_t kWantBlocks = 1024, kManyRows = 512, kShort = 65536, kMostElements = (int64_t)1 << 30;
 constexpr int kChunkMin = 4096;
 
 static int chunks_of(const sgc_logprob_opts* o)
 {
     int64_t n = cdiv(kWantBlocks, o->rows > 0 ? o->rows : 1);
     if (n > cdiv(o->vocab, kChunkMin)) n = cdiv(o->vocab, kChunkMin);
-    return o->rows >= kManyRows || o->vocab <= kShort * (o->rows <= 256 ? 2 : 1) ? 1 : (int)n;
+    if (o->rows >= kManyRows || o->vocab <= kShort * (o->rows <= 256 ? 2 : 1)) n = 1;
+    if (n < cdiv(o->vocab, kMostElements)) n = cdiv(o->vocab, kMostElements);
+    return (int)n;
 }
 
 // Chunks start at a multiple of 64 elements.

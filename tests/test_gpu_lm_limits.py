@@ -55,3 +55,27 @@ def test_distill_longest_row():
     assert int(torch.count_nonzero(out)) == 0
     check_guards(obuf)
     check_guards(buf)
+
+
+@pytest.mark.parametrize("rows", [1, 512])
+def test_logprobs_longest_row(rows):
+    """One, and so many (the same, stride 0) that rows are not split to fill the card."""
+    announce(f"logprobs {rows}x(2^31 - 1) bf16")
+    buf, z, vals = longest_row()
+    tok = torch.tensor([PLACES[r % len(PLACES)] for r in range(rows)])
+    r = sgc.token_logprobs(z.expand(rows, V), tok.cuda(), top=5)
+    small = torch.tensor([k % len(PLACES) for k in range(rows)])
+    sm, (logp, H, idx, tlp), (t_logp, t_H, t_tlp) = lm_ref.logprobs(vals[None].expand(rows, -1), small, 1.0, 5)
+    lm_ref.close(r.logp, logp, t_logp, "logp")
+    lm_ref.close(r.entropy, H, t_H, "entropy")
+    assert torch.equal(r.top_idx.cpu().long(), torch.tensor(PLACES)[idx])
+    lm_ref.close(r.top_logp, tlp, t_tlp, "top_logp")
+    if rows == 1:
+        obuf = torch.full_like(buf, 100.0)
+        out = obuf[GUARD:GUARD + V][None]
+        g = torch.ones(1, device="cuda")
+        sgc.token_logprobs_backward(z, tok.cuda(), r.stats, r.entropy, g, g, dlogits=out)
+        d, td = lm_ref.logprobs_backward(sm, small, g.cpu(), g.cpu())
+        lm_ref.close(out[:, torch.tensor(PLACES, device="cuda")], d, td, "dlogits", BF16)
+        assert int(torch.count_nonzero(out)) == len(PLACES)
+        check_guards(obuf)
