@@ -519,8 +519,8 @@ static bool distill_opts_ok(const sgc_distill_opts* o)
 {
     return o && o->rows >= 0 && o->rows < ((int64_t)1 << 31) && o->vocab >= 1 && o->vocab < ((int64_t)1 << 31) &&
            lm_dtype(o->dtype) && o->top >= 1 && o->top <= SGC_TOP_MAX &&
-           (o->mode == SGC_DISTILL_RENORM || o->mode == SGC_DISTILL_TAIL) && o->scale > 0.f &&
-           std::isfinite(o->scale) && o->teacher_scale > 0.f && std::isfinite(o->teacher_scale) &&
+           (o->mode == SGC_DISTILL_RENORM || o->mode == SGC_DISTILL_TAIL) && scale_ok(o->scale) &&
+           o->teacher_scale > 0.f && std::isfinite(o->teacher_scale) &&
            (o->mode != SGC_DISTILL_TAIL || o->teacher_scale == 1.f) && o->reserved == 0;
 }
 
@@ -562,7 +562,7 @@ static DistillArgs distill_args(const sgc_distill_opts* o, int64_t zs, const int
     a.top = o->top;
     a.mode = o->mode;
     a.scale = o->scale;
-    a.c = (float)((double)o->scale * M_LOG2E);
+    a.c = exponent_factor(o->scale);
     a.teacher_scale = o->teacher_scale;
     a.idx = idx;
     a.val = val;

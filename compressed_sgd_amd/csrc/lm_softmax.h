@@ -27,6 +27,10 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ inline float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+// c of a scale that a call may have: positive and finite as fp32.
+inline float exponent_factor(float scale) { return (float)((double)scale * M_LOG2E); }
+inline bool scale_ok(float scale) { return scale > 0.f && std::isfinite(exponent_factor(scale)); }
+
 constexpr float kFar = 1e8f;
 __device__ inline bool is_far(float m, float c) { return fabsf(m * c) > kFar && fabsf(m) != INFINITY; }
 

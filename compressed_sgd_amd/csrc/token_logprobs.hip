@@ -387,7 +387,7 @@ static bool logprob_opts_ok(const sgc_logprob_opts* o)
 {
     return o && o->rows >= 0 && o->rows < ((int64_t)1 << 31) && o->vocab >= 1 && o->vocab < ((int64_t)1 << 31) &&
            lm_dtype(o->dtype) && (o->token_type == SGC_TOKEN_I32 || o->token_type == SGC_TOKEN_I64) && o->top >= 0 &&
-           o->top <= SGC_TOP_MAX && o->top <= o->vocab && o->scale > 0.f && std::isfinite(o->scale);
+           o->top <= SGC_TOP_MAX && o->top <= o->vocab && scale_ok(o->scale);
 }
 
 static bool tokens_ok(const sgc_logprob_opts* o, const void* tokens)
@@ -426,7 +426,7 @@ static LogprobArgs logprob_args(const sgc_logprob_opts* o, int64_t zs, const voi
     a.top = o->top;
     a.token_type = o->token_type;
     a.scale = o->scale;
-    a.c = (float)((double)o->scale * M_LOG2E);
+    a.c = exponent_factor(o->scale);
     a.tokens = tokens;
     return a;
 }

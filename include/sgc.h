@@ -411,7 +411,8 @@ int sgc_layer_norm_backward(const sgc_norm_opts* opt, const void* dy, int64_t dy
  * (top_idx: NaN before +inf before all else).
  * tokens and logp may be NULL together; entropy, stats, dstatus may be NULL;
  * top = 0 wants no alternatives (top_idx, top_logp ignored).
- * 0 <= top <= min(vocab, SGC_TOP_MAX), 1 <= vocab < 2^31, 0 < scale < inf.
+ * 0 <= top <= min(vocab, SGC_TOP_MAX), 1 <= vocab < 2^31, 0 < scale, and
+ * scale / ln 2 finite in fp32 (scale <= 2.3e38).
  * The workspace call returns 0 for bad options; a call needs at least that
  * much, and ws may be NULL where it returns SGC_LM_WS_NONE.
  *
@@ -473,7 +474,7 @@ int sgc_token_logprobs_backward(const sgc_logprob_opts* opt, const void* logits,
  * below -1 or given twice is skipped too: loss NaN, gradient 0 and, where
  * dstatus is given, SGC_STATUS_CORRUPT.  A row with dloss 0 gets zero
  * gradient, whatever its logits are.  1 <= top <= SGC_TOP_MAX; top may
- * exceed vocab; scale and teacher_scale finite and > 0.                    */
+ * exceed vocab; scale as above; teacher_scale finite and > 0.               */
 #define SGC_DISTILL_RENORM 0
 #define SGC_DISTILL_TAIL 1
 typedef struct {

@@ -17,3 +17,19 @@ def test_longest_rows_are_split_however_many_there_are(rows, vocab, dtype):
     assert sgc.lib().sgc_token_logprobs_workspace(C.byref(o)) > 2 * rows * 5 * 8
     d = lm.DistillOpts(rows, vocab, dtype, 5, lm.DISTILL_TAIL, 1.0, 1.0, 0)
     assert sgc.lib().sgc_distill_workspace(C.byref(d)) > 2 * rows * 8
+
+
+def test_a_scale_whose_powers_of_two_overflow_is_refused():
+    """The exponent's factor scale / ln 2 has to be finite in fp32."""
+    A = C.c_void_p(4096)
+    lib = sgc.lib()
+    for scale, ok in ((2.3e38, True), (2.4e38, False), (3.4e38, False)):
+        o = lm.LogprobOpts(4, 100, lm.F32, lm.TOKEN_I64, 5, scale)
+        d = lm.DistillOpts(4, 100, lm.F32, 5, lm.DISTILL_RENORM, scale, 1.0, 0)
+        assert (lib.sgc_token_logprobs_workspace(C.byref(o)) != 0) == ok
+        assert (lib.sgc_distill_workspace(C.byref(d)) != 0) == ok
+        if not ok:
+            assert lib.sgc_token_logprobs(C.byref(o), A, 100, A, A, A, A, A, A, A, A, 1 << 30, None) == sgc.EINVAL
+            assert lib.sgc_token_logprobs_backward(C.byref(o), A, 100, A, A, A, A, A, A, 100, None) == sgc.EINVAL
+            assert lib.sgc_distill(C.byref(d), A, 100, A, A, A, A, A, A, 100, A, A, 1 << 30, None) == sgc.EINVAL
+            assert lib.sgc_distill_backward(C.byref(d), A, 100, A, A, A, A, A, 100, None) == sgc.EINVAL
