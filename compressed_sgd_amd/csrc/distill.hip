@@ -530,7 +530,8 @@ static bool entries_ok(const int32_t* idx, const float* val)
 }
 
 // How the rows are shared out.  With the gradient a row that can be held is: one
-// launch, one reading (1 x 50000 bf16: 15 us, in chunks 23).  Else one
+// launch, one reading (1 x 50000 bf16: 15 us, in chunks 23; 300 x 131072 57 and
+// 56, 500 x 131072 69 and 87).  Else one
 // workgroup a row from kManyRows rows on, which fill the card, and for rows up
 // to kShort (twice that where every row has a compute unit of its own), which
 // take no longer than a second launch; and chunks for the rest, about
@@ -599,6 +600,19 @@ static void distill_held(const DistillArgs& a, const T* z, T* dz, bool head, siz
         k_distill_held<T, NW, NV, TAIL, false, false><<<rows, NW * 64, lds, s>>>(a, z, dz);
 }
 
+// Whether the gradient's rows start inside a 128-byte line: then held rows have
+// up to 7 vectors less room.
+template <typename T>
+static bool has_head(const DistillArgs& a, const T* dz)
+{
+    return dz && ((a.rows > 1 && a.dzs * sizeof(T) % 128) || (uintptr_t)dz % 128);
+}
+template <typename T>
+static int64_t held_vectors(const DistillArgs& a, const T* dz)
+{
+    return a.vocab / VecLen<T>::value + (has_head(a, dz) ? 7 : 0);
+}
+
 template <typename T, bool TAIL>
 static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, float* part, float* stats,
                         hipStream_t s)
@@ -606,9 +620,8 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
     const dim3 rows = row_grid(a.rows);
     if (chunks == 1) {
         const size_t lds = (size_t)(a.vocab + 31) / 32 * 4;
-        // rows that start inside a 128-byte line have up to 7 vectors less room
-        const bool head = a.rows > 1 && a.dzs * sizeof(T) % 128 || (uintptr_t)dz % 128;
-        const int nv = a.vocab / VecLen<T>::value + (head ? 7 : 0);
+        const bool head = has_head(a, dz);
+        const int64_t nv = held_vectors(a, dz);
         if (a.vocab <= 2048)
             k_distill_row<T, 1, TAIL><<<rows, 64, lds, s>>>(a, z, dz);
         else if (dz && nv <= 1024)
@@ -655,7 +668,7 @@ static int distill(const sgc_distill_opts* o, const void* z, int64_t zs, const i
     a.stats = stats;
     a.dstatus = dstatus;
     int chunks = chunks_of(o);
-    if (dz && o->vocab / VecLen<T>::value + 7 <= kMostHeld) chunks = 1;
+    if (dz && held_vectors(a, (const T*)dz) <= kMostHeld) chunks = 1;
     float* part = nullptr;
     if (chunks > 1) {
         Carver c(ws);

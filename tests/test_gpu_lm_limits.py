@@ -79,3 +79,25 @@ def test_logprobs_longest_row(rows):
         lm_ref.close(out[:, torch.tensor(PLACES, device="cuda")], d, td, "dlogits", BF16)
         assert int(torch.count_nonzero(out)) == len(PLACES)
         check_guards(obuf)
+
+
+@pytest.mark.parametrize("rows", [3, 300, 520])
+@pytest.mark.parametrize("vocab,dtype", [(131072, BF16), (131072, torch.float16), (65536, torch.float32)], ids=str)
+def test_longest_held_rows_are_held_however_many_there_are(rows, vocab, dtype):
+    """With the gradient the longest rows that registers hold take one launch, which needs no workspace."""
+    announce(f"held rows {rows}x{vocab} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    z = torch.empty(rows, vocab, dtype=dtype, device="cuda").normal_(0.0, 2.0, generator=g)
+    idx = torch.randperm(vocab, generator=torch.Generator().manual_seed(1))[:rows * 8].view(rows, 8).int()
+    val = torch.log_softmax(torch.randn(rows, 16, generator=torch.Generator().manual_seed(2)), 1)[:, :8].contiguous()
+    dl = torch.rand(rows, generator=torch.Generator().manual_seed(3)) + 0.5
+    ws = torch.full((sgc.distill_workspace_bytes(rows, vocab, 8, dtype=dtype) + 256,), 0x5A, dtype=torch.uint8,
+                    device="cuda")
+    out = torch.empty_like(z)
+    assert out.data_ptr() % 128 == 0
+    r = sgc.distill(z, idx.cuda(), val.cuda(), mode=sgc.DISTILL_TAIL, dloss=dl.cuda(), dlogits=out, ws=ws)
+    assert (ws == 0x5A).all()
+    pick = torch.tensor([0, rows // 2, rows - 1])
+    loss, d, tl, td = lm_ref.distill(z[pick].cpu(), idx[pick], val[pick], True, 1.0, g=dl[pick])
+    lm_ref.close(r.loss[pick], loss, tl, "loss")
+    lm_ref.close(out[pick], d, td, "dlogits", dtype)
