@@ -5,7 +5,9 @@ Thin marshalling over the C ABI (include/sgc.h), like the rest of the
 binding; the calls are re-exported by the package.  Rows are taken from 2-D
 tensors whose last dimension is contiguous; any row stride is allowed.  The
 gradients are explicit calls (no autograd): what the backward calls need is
-in the forward calls' results.
+in the forward calls' results.  A tensor that requires grad is refused while
+grad mode is on, since its gradient would be lost in silence: call under
+torch.no_grad(), from an autograd.Function, or with detached tensors.
 """
 from __future__ import annotations
 
@@ -74,6 +76,13 @@ def _stream(device: torch.device, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _no_graph(*tensors: Optional[torch.Tensor]) -> None:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("this call records no graph: call it under torch.no_grad() or with detached tensors")
+
+
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
     """Checks a 2-D device tensor of rows; its row stride."""
     if not t.is_cuda:
@@ -140,6 +149,7 @@ def _affine(weight, bias, x, cols, dev) -> int:
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
                eps: float = 1e-5, out: Optional[torch.Tensor] = None, stream=None) -> Normalized:
     """Layer norm of every row of x [rows, cols]; out may be x."""
+    _no_graph(x, weight, bias, out)
     xs = _rows(x, "x")
     rows, cols = x.shape
     dev = x.device
@@ -168,6 +178,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     """Gradients of layer_norm.  dweight and dbias (float32, e.g. slices of a
     flat gradient) are written, or with accumulate added to; new ones are made
     where none is given.  dx may be dy or x."""
+    _no_graph(dy, x, weight, mean, rstd, dx, dweight, dbias)
     xs = _rows(x, "x")
     dys = _rows(dy, "dy", x)
     rows, cols = x.shape
@@ -231,6 +242,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     A negative token is none (logp 0).  status (int32 [1]) collects
     STATUS_BAD_INPUT for a token past the vocabulary, whose logp is NaN.
     """
+    _no_graph(logits)
     zs = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.device
@@ -264,6 +276,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor]
                             dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits from those of logp and entropy (either may be
     None); stats and entropy are the forward call's.  dlogits may be logits."""
+    _no_graph(logits, stats, entropy, dlogp, dentropy, dlogits)
     zs = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.device
@@ -317,6 +330,7 @@ def distill(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Tensor, *, m
     gradient comes in the same call; dlogits may be logits.  status (int32
     [1]) collects STATUS_CORRUPT for a row with a bad or repeated index.
     """
+    _no_graph(logits, t_val, dloss, dlogits)
     zs = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.device
@@ -345,6 +359,7 @@ def distill_backward(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Ten
                      teacher_scale: float = 1.0, dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits from the rows' upstream gradients (None: 1) and
     the loss call's stats.  dlogits may be logits."""
+    _no_graph(logits, t_val, stats, dloss, dlogits)
     zs = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.device
