@@ -83,6 +83,13 @@ def _no_graph(*tensors: Optional[torch.Tensor]) -> None:
                 raise ValueError("this call records no graph: call it under torch.no_grad() or with detached tensors")
 
 
+def _written(*tensors: Optional[torch.Tensor]) -> None:
+    """Tells autograd that the caller's buffers hold other values now."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
     """Checks a 2-D device tensor of rows; its row stride."""
     if not t.is_cuda:
@@ -163,6 +170,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, eps, 0)
     _check(lib().sgc_layer_norm(C.byref(o), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean),
                                 _ptr(rstd), _stream(dev, stream)), "sgc_layer_norm")
+    _written(out)
     return Normalized(y, mean, rstd)
 
 
@@ -189,6 +197,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         _vec1(t, name, n, torch.float32, dev)
     if accumulate and (dweight is None or dbias is None):
         raise ValueError("accumulate needs dweight and dbias")
+    given = (dx, dweight, dbias)
     if dx is None and want_dx:
         dx = _empty(stream, (rows, cols), x.dtype, dev)
     dxs = _rows(dx, "dx", x) if dx is not None else 0
@@ -204,6 +213,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
                                      _ptr(dx), dxs, _ptr(dweight), _ptr(dbias), _ptr(ws),
                                      0 if ws is None else ws.numel(), _stream(dev, stream)),
            "sgc_layer_norm_backward")
+    _written(*given)
     return NormGrads(dx, dweight, dbias)
 
 
@@ -249,6 +259,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     tt = _tokens(tokens, rows, dev)
     _status(status, dev)
     f32 = torch.float32
+    given = out
     if out is None:
         out = TokenLogprobs(None if tokens is None else _empty(stream, (rows,), f32, dev),
                             _empty(stream, (rows,), f32, dev), _empty(stream, (rows, 2), f32, dev),
@@ -267,6 +278,8 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     _check(L.sgc_token_logprobs(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(out.logp), _ptr(out.entropy),
                                 _ptr(out.stats), _ptr(out.top_idx), _ptr(out.top_logp), _ptr(status), _ptr(ws),
                                 0 if ws is None else ws.numel(), _stream(dev, stream)), "sgc_token_logprobs")
+    if given is not None:
+        _written(out.logp, out.entropy, out.stats, out.top_idx, out.top_logp)
     return out
 
 
@@ -285,7 +298,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor]
     _vec(stats, "stats", (rows, 2), f32, dev)
     for t, name in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
         _vec1(t, name, rows, f32, dev)
-    ds = vocab
+    ds, given = vocab, dlogits
     if dlogits is None:
         dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
     else:
@@ -294,6 +307,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor]
     _check(lib().sgc_token_logprobs_backward(C.byref(o), _ptr(logits), zs, _ptr(tokens), _ptr(stats), _ptr(entropy),
                                              _ptr(dlogp), _ptr(dentropy), _ptr(dlogits), ds, _stream(dev, stream)),
            "sgc_token_logprobs_backward")
+    _written(given)
     return dlogits
 
 
@@ -337,7 +351,7 @@ def distill(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Tensor, *, m
     top = _entries(t_idx, t_val, rows, dev)
     _status(status, dev)
     _vec1(dloss, "dloss", rows, torch.float32, dev)
-    ds = vocab
+    ds, given = vocab, dlogits
     if dlogits is not None:
         ds = _rows(dlogits, "dlogits", logits)
     elif dloss is not None:
@@ -351,6 +365,7 @@ def distill(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Tensor, *, m
     _check(L.sgc_distill(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(loss), _ptr(stats),
                          _ptr(dloss), _ptr(dlogits), ds, _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
                          _stream(dev, stream)), "sgc_distill")
+    _written(given)
     return Distilled(loss, stats, dlogits)
 
 
@@ -366,7 +381,7 @@ def distill_backward(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Ten
     top = _entries(t_idx, t_val, rows, dev)
     _vec(stats, "stats", (rows, 4), torch.float32, dev)
     _vec1(dloss, "dloss", rows, torch.float32, dev)
-    ds = vocab
+    ds, given = vocab, dlogits
     if dlogits is None:
         dlogits = _empty(stream, (rows, vocab), logits.dtype, dev)
     else:
@@ -374,4 +389,5 @@ def distill_backward(logits: torch.Tensor, t_idx: torch.Tensor, t_val: torch.Ten
     o = DistillOpts(rows, vocab, _DTYPES[logits.dtype], top, mode, scale, teacher_scale, 0)
     _check(lib().sgc_distill_backward(C.byref(o), _ptr(logits), zs, _ptr(t_idx), _ptr(t_val), _ptr(stats),
                                       _ptr(dloss), _ptr(dlogits), ds, _stream(dev, stream)), "sgc_distill_backward")
+    _written(given)
     return dlogits
