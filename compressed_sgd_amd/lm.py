@@ -124,6 +124,8 @@ def _status(t: Optional[torch.Tensor], device) -> None:
 def _scratch(need: int, ws: Optional[torch.Tensor], device, slot: str, stream, what: str) -> Optional[torch.Tensor]:
     if need == 0:
         raise SGCError(-1, what)
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
     if need == LM_WS_NONE or ws is not None:
         return ws
     return workspace(need, device, slot, stream)

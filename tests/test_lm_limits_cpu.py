@@ -2,6 +2,7 @@
 import ctypes as C
 
 import pytest
+import torch
 
 import compressed_sgd_amd as sgc
 from compressed_sgd_amd import lm
@@ -33,3 +34,22 @@ def test_a_scale_whose_powers_of_two_overflow_is_refused():
             assert lib.sgc_token_logprobs_backward(C.byref(o), A, 100, A, A, A, A, A, A, 100, None) == sgc.EINVAL
             assert lib.sgc_distill(C.byref(d), A, 100, A, A, A, A, A, A, 100, A, A, 1 << 30, None) == sgc.EINVAL
             assert lib.sgc_distill_backward(C.byref(d), A, 100, A, A, A, A, A, 100, None) == sgc.EINVAL
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """The kernels would write to a host address, or past a view's elements."""
+    dev = torch.device("cuda", 0)
+    buf = torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="ws must be"):
+        lm._scratch(32, buf, dev, "distill", None, "sgc_distill")
+    with pytest.raises(ValueError, match="ws must be"):
+        lm._scratch(32, buf[::2], buf.device, "distill", None, "sgc_distill")
+    assert lm._scratch(32, buf, buf.device, "distill", None, "sgc_distill") is buf
+
+
+def test_few_long_rows_need_a_workspace():
+    """The split path's refusals are provoked at these sizes: it has to be the one they take."""
+    o = lm.LogprobOpts(1, 1 << 20, lm.F32, lm.TOKEN_I64, 8, 1.0)
+    d = lm.DistillOpts(1, 1 << 20, lm.F32, 8, lm.DISTILL_RENORM, 1.0, 1.0, 0)
+    assert sgc.lib().sgc_token_logprobs_workspace(C.byref(o)) > lm.LM_WS_NONE
+    assert sgc.lib().sgc_distill_workspace(C.byref(d)) > lm.LM_WS_NONE
