@@ -196,7 +196,8 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_norm_back(cons
         nr = rstd[at];
     };
     // 16 elements a thread leave no registers for the next row's (128 of them at
-    // 16 waves; fetched ahead they spill 108)
+    // 16 waves: fetched ahead they spill 108, as it is up to 43 in rows by one, two
+    // or eight waves, 16384 x 4099 bf16 140 us)
     constexpr bool kAhead = EPT < 16;
     if (kAhead && r < rows) fetch(r);
     int turn = 0;
@@ -402,15 +403,17 @@ static bool norm_opts_ok(const sgc_norm_opts* o)
 // (a power of two); 16 in the longest rows.  Where that would leave a quarter
 // of the waves idle, 16-bit rows take half the waves and 16 elements a thread
 // (46153 x 1300 bf16 backward: 151 -> 106 us; in fp32 16 elements spill), and
-// fp32 rows of 513 to 768 one wave and 12 (20001 x 650 backward: 42 -> 39).
-// At least 8 waves.
+// fp32 rows of 513 to 768 one wave and 12, backward only where a row is no
+// whole number of vectors (about 13 M elements: forward 577 23.3 -> 21.9 us,
+// 600 19.2 -> 18.5, 768 19.8; backward 515 43.2 -> 39.7, 650 39.9 -> 39.0, but
+// 600 34.2 -> 36.1 and 768 33.7 -> 36.5).  At least 8 waves.
 struct NormShape {
     int ntr, ept, rpb;
 };
-static NormShape norm_shape(int64_t cols, int32_t dtype)
+static NormShape norm_shape(int64_t cols, int32_t dtype, bool back)
 {
     if (cols <= 128) return {16, 8, 32};
-    if (dtype == SGC_F32 && cols > 512 && cols <= 768) return {64, 12, 8};
+    if (dtype == SGC_F32 && cols > 512 && cols <= 768 && (!back || cols % 4)) return {64, 12, 8};
     int ntr = 64, ept = 8;
     while (ntr < 1024 && ntr * 8 < cols) ntr *= 2;
     if (ntr * 8 < cols) ept = 16;
@@ -418,17 +421,17 @@ static NormShape norm_shape(int64_t cols, int32_t dtype)
     return {ntr, ept, ntr < 512 ? 512 / ntr : 1};
 }
 
-// Workgroups that share out the rows: `waves` of them a compute unit.
-static int64_t norm_groups(const sgc_norm_opts* o, int waves)
+// Workgroups that share out the rows.
+static int64_t norm_groups(const sgc_norm_opts* o, bool back)
 {
-    const NormShape sh = norm_shape(o->cols, o->dtype);
-    const int64_t most = kCus * waves * 64 / (sh.ntr * sh.rpb), need = cdiv(o->rows, sh.rpb);
+    const NormShape sh = norm_shape(o->cols, o->dtype, back);
+    const int64_t most = kCus * (back ? kBackwardWaves : kForwardWaves) * 64 / (sh.ntr * sh.rpb), need = cdiv(o->rows, sh.rpb);
     return need < most ? need : most;
 }
 
 static int64_t norm_parts(const sgc_norm_opts* o)
 {
-    if (o->cols <= kNormHeld) return norm_groups(o, kBackwardWaves);
+    if (o->cols <= kNormHeld) return norm_groups(o, true);
     return o->rows < 64 ? o->rows : 64;
 }
 
@@ -445,7 +448,7 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
         k_norm_long<T, W><<<row_grid(o->rows), kLongThreads, 0, s>>>(x, xs, w, b, y, ys, mean, rstd, o->rows, cols,
                                                                      o->eps);
     } else {
-        const unsigned g = (unsigned)norm_groups(o, kForwardWaves);
+        const unsigned g = (unsigned)norm_groups(o, false);
         const bool once = 2 * o->rows * cols * (int64_t)sizeof(T) >= kCacheBytes;
 #define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                      \
     k_norm<T, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(x, xs, wv, bv, w32, y, ys, mean, rstd, o->rows, cols, \
@@ -461,7 +464,7 @@ static int norm_forward(const sgc_norm_opts* o, const void* xv, int64_t xs, cons
             else SGC_NORM_RUN(NTR, EPT, RPB, false, false);       \
         }                                                         \
     } while (0)
-        const NormShape sh = norm_shape(cols, o->dtype);
+        const NormShape sh = norm_shape(cols, o->dtype, false);
         if (sh.ept == 12) { if constexpr (sizeof(T) == 4) { SGC_NORM(64, 12, 8); } }
         else if (sh.ept == 16 && sh.ntr == 1024) SGC_NORM(1024, 16, 1);
         else if (sh.ept == 16) {
@@ -514,8 +517,13 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
 #define SGC_NORM_RUN(NTR, EPT, RPB, RAG, ONCE)                                                                     \
     k_norm_back<T, NTR, EPT, RPB, RAG, ONCE><<<g, NTR * RPB, 0, s>>>(dy, dys, x, xs, wv, w32, mean, rstd, dx, dxs, \
                                                                      part, o->rows, cols)
-        const NormShape sh = norm_shape(cols, o->dtype);
-        if (sh.ept == 12) { if constexpr (sizeof(T) == 4) { SGC_NORM(64, 12, 8); } }
+        const NormShape sh = norm_shape(cols, o->dtype, true);
+        if (sh.ept == 12) {
+            if constexpr (sizeof(T) == 4) {
+                if (once) SGC_NORM_RUN(64, 12, 8, true, true);
+                else SGC_NORM_RUN(64, 12, 8, true, false);
+            }
+        }
         else if (sh.ept == 16 && sh.ntr == 1024) SGC_NORM(1024, 16, 1);
         else if (sh.ept == 16) {
             if constexpr (sizeof(T) == 2) {
