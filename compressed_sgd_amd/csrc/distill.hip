@@ -270,22 +270,6 @@ __device__ inline void keep_packed(Raw (&q)[NV])
         for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(q[n].w[i]));
 }
 
-// -inf in the elements of q with a bit in `skip`.
-template <typename T>
-__device__ inline void remove(Raw& q, uint32_t skip)
-{
-    const Raw low = raw_low<T>();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t gone;
-        if (sizeof(T) == 4)
-            gone = (skip >> i) & 1u ? 0xffffffffu : 0u;
-        else
-            gone = ((skip >> (2 * i)) & 1u ? 0xffffu : 0u) | ((skip >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
-        q.w[i] = (q.w[i] & ~gone) | (low.w[i] & gone);
-    }
-}
-
 // A row a workgroup with loss and gradient in one reading: NV vectors of the
 // row stay in each thread's registers from the sums to the gradient (a vector
 // past the row is -inf, and with the tail so is an entry, once marked).  One

@@ -47,14 +47,10 @@ struct SoftSum {
         return fmaxf(FAR ? (from - finite_base(to)) * c : base_of(from, c) - base_of(to, c), kLowD);
     }
 
-    // N elements; those with a bit in `skip` do not count.
-    template <int N, bool ENT, bool SKIP>
-    __device__ void add(float* x, float c, uint32_t skip)
+    // N elements.
+    template <int N, bool ENT>
+    __device__ void add(float* x, float c)
     {
-        if (SKIP && skip) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = (skip >> i) & 1u ? -INFINITY : x[i];
-        }
         float g = x[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) g = fmaxf(g, x[i]);
@@ -93,6 +89,22 @@ __device__ inline uint32_t vec_bits(const uint32_t* bm, int v)
     return (((const uint8_t*)bm)[v >> 1] >> ((v & 1) * 4)) & 0xfu;
 }
 
+// -inf in the elements of q with a bit in `skip`.
+template <typename T>
+__device__ inline void remove(Raw& q, uint32_t skip)
+{
+    const Raw low = raw_low<T>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t gone;
+        if (sizeof(T) == 4)
+            gone = (skip >> i) & 1u ? 0xffffffffu : 0u;
+        else
+            gone = ((skip >> (2 * i)) & 1u ? 0xffffu : 0u) | ((skip >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+        q.w[i] = (q.w[i] & ~gone) | (low.w[i] & gone);
+    }
+}
+
 // The elements [0, len) of z, by the NT threads of a workgroup: thread i takes
 // the vectors i, i + NT, ... and one element past the last whole vector.  U
 // vectors of 16 bytes are in flight for each thread.  (The next U fetched
@@ -113,11 +125,14 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
 #pragma unroll
         for (int u = 0; u < U; u += 2) {  // two vectors at a time: four take registers that cost a workgroup
             float x[2 * VL];
+            if (SKIP) {
+                const uint32_t s0 = vec_bits<VL>(bm, v + u * NT), s1 = vec_bits<VL>(bm, v + (u + 1) * NT);
+                if (s0) remove<T>(q[u], s0);
+                if (s1) remove<T>(q[u + 1], s1);
+            }
             unpack<T>(q[u], x);
             unpack<T>(q[u + 1], x + VL);
-            uint32_t skip = 0;
-            if (SKIP) skip = vec_bits<VL>(bm, v + u * NT) | vec_bits<VL>(bm, v + (u + 1) * NT) << VL;
-            a.template add<2 * VL, ENT, SKIP>(x, c, skip);
+            a.template add<2 * VL, ENT>(x, c);
         }
     }
     if (v0 < nv) {  // fewer than U vectors a thread: one trip to memory for them too
@@ -129,16 +144,20 @@ __device__ inline void stream_sums(const T* z, int len, float c, const uint32_t*
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (v0 + u * NT < nv) {  // the same for all
+                if (SKIP) {
+                    const uint32_t s0 = v + u * NT < nv ? vec_bits<VL>(bm, v + u * NT) : 0u;
+                    if (s0) remove<T>(q[u], s0);
+                }
                 float x[VL];
                 unpack<T>(q[u], x);
-                a.template add<VL, ENT, SKIP>(x, c, SKIP && v + u * NT < nv ? vec_bits<VL>(bm, v + u * NT) : 0u);
+                a.template add<VL, ENT>(x, c);
             }
         }
     }
     const int i = nv * VL + threadIdx.x;
     if (i < len) {
-        float x[1] = {to_f(z[i])};
-        a.template add<1, ENT, SKIP>(x, c, SKIP ? (bm[i >> 5] >> (i & 31)) & 1u : 0u);
+        float x[1] = {SKIP && (bm[i >> 5] >> (i & 31)) & 1u ? -INFINITY : to_f(z[i])};
+        a.template add<1, ENT>(x, c);
     }
 }
 
