@@ -229,7 +229,7 @@ __device__ inline bool finish_row(const Entries& en, const DistillArgs& a, int64
 
 // A row a workgroup, vocab <= kChunkMax: loss, and with dz the gradient; the
 // row's second reading comes from the cache.  For the loss alone, and rows too
-// long to be held.  2000 x 10001 fp16 with the tail 13.6 us, one row's chain of
+// long to be held.  2000 x 10001 fp16 with the tail 13.5 us, one row's chain of
 // trips and barriers; 4096 x 50000 bf16 80 us, 5.1 TB/s.
 template <typename T, int NW, bool TAIL>
 __global__ __launch_bounds__(NW * 64) void k_distill_row(DistillArgs a, const T* z, T* dz)
@@ -278,7 +278,7 @@ __device__ inline void keep_packed(Raw (&q)[NV])
 // are freed from once a row (lm_softmax.h); a maximum far from zero takes z - M
 // first.  Bound by memory: 4096 x 50000 bf16 with the tail 154
 // us, 5.3 TB/s, by three workgroups a compute unit (by two 160, by one of 16
-// waves 232); 4096 x 131072 457 us, 4.7 TB/s, where a row takes half the unit's
+// waves 232); 4096 x 131072 455 us, 4.7 TB/s, where a row takes half the unit's
 // registers.
 template <typename T, int NW, int NV, bool TAIL, bool ONCE, bool HEAD>
 __global__ __launch_bounds__(NW * 64, NV > 8 ? 4 : 1) void k_distill_held(DistillArgs a, const T* z, T* dz)
@@ -620,7 +620,7 @@ static int distill_mode(const DistillArgs& a, int chunks, const T* z, T* dz, flo
             distill_held<T, 8, 16, TAIL>(a, z, dz, head, lds, s);
         else if (dz && nv <= kMostHeld)
             distill_held<T, 16, 16, TAIL>(a, z, dz, head, lds, s);
-        else if (a.rows >= kManyRows && nv <= 1536)  // the loss of 8000 x 10000 bf16: 39.5 us, by four waves 45
+        else if (a.rows >= kManyRows && nv <= 1536)  // the loss of 8000 x 10000 bf16: 40 us, by four waves 45
             k_distill_row<T, 2, TAIL><<<rows, 128, lds, s>>>(a, z, dz);
         else if (a.vocab <= 16384)
             k_distill_row<T, 4, TAIL><<<rows, 256, lds, s>>>(a, z, dz);
