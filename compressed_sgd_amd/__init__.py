@@ -10,7 +10,9 @@ The entry points keep the C names without the ``sgc_`` prefix:
 ``compress``, ``binarize``, ``encode``, ``decode_accumulate``, plus the
 ``Layout`` of segment sizes shared by both ends of the exchange.  The
 operators at the loss end of a language model (``layer_norm``,
-``token_logprobs``, ``distill`` and their backward calls) are in ``lm``.
+``token_logprobs``, ``distill`` and their backward calls) are in ``lm``, those
+in 8 bits between its body and its loss (``rms_norm``, ``quantize_q8``,
+``int8_linear``, the norms' backward passes) in ``lm8``.
 """
 from __future__ import annotations
 
@@ -49,6 +51,9 @@ EXPORTED = (
     "sgc_layer_norm", "sgc_layer_norm_backward_workspace", "sgc_layer_norm_backward",
     "sgc_token_logprobs_workspace", "sgc_token_logprobs", "sgc_token_logprobs_backward",
     "sgc_distill_workspace", "sgc_distill", "sgc_distill_backward",
+    "sgc_rms_norm", "sgc_rms_norm_backward_workspace", "sgc_rms_norm_backward",
+    "sgc_quantize_q8", "sgc_dequantize_q8", "sgc_norm_backward_q8_workspace", "sgc_norm_backward_q8",
+    "sgc_int8_linear",
 )
 
 
@@ -131,6 +136,7 @@ def lib():
         L.sgc_set_pass_events.argtypes = [P, P]
         L.sgc_set_pass_events.restype = C.c_int
         lm._declare(L)
+        lm8._declare(L)
         _lib = L
     return _lib
 
@@ -612,3 +618,8 @@ from .lm import (  # noqa: E402,F401
     NormGrads, Normalized, TokenLogprobs, distill, distill_backward, distill_workspace_bytes, layer_norm,
     layer_norm_backward, layer_norm_backward_workspace_bytes, token_logprobs, token_logprobs_backward,
     token_logprobs_workspace_bytes)
+from . import lm8  # noqa: E402
+from .lm8 import (  # noqa: E402,F401
+    NORM_LAYER, NORM_RMS, NormQ8Grads, Quantized, RmsGrads, RmsNormalized, RmsQuantized, dequantize_q8, int8_linear,
+    layer_norm_backward_q8, norm_backward_q8_workspace_bytes, quantize_q8, rms_norm, rms_norm_backward,
+    rms_norm_backward_q8, rms_norm_backward_workspace_bytes, rms_norm_q8)

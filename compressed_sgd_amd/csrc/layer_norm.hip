@@ -11,102 +11,9 @@
 // columns' weights are loaded once and their gradients' sums stay in its
 // registers; the next rows are on their way while one is worked on.  Rows too
 // long for that (over kNormHeld elements) are read again for every pass.
-#include "lm_common.h"
+#include "lm_norm.h"
 
 namespace sgc {
-
-constexpr int64_t kNormHeld = 16384;
-constexpr int64_t kCus = 256;
-// Waves that a compute unit holds of the forward and the backward kernel.
-constexpr int kForwardWaves = 32, kBackwardWaves = 16;
-
-// Elements [v VL, v VL + VL) of a row that ends at cols; past it 0.  RAG: cols
-// may be no multiple of VL.
-template <typename T, bool RAG, bool ONCE>
-__device__ inline Raw load_raw(const T* p, int v, int cols)
-{
-    constexpr int VL = VecLen<T>::value;
-    if ((v + 1) * VL <= cols) return load_row<ONCE>((const Raw*)p + v);
-    Raw q = {{0, 0, 0, 0}};
-    if (RAG && v * VL < cols) {
-        float x[VL];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) x[e] = v * VL + e < cols ? to_f(p[v * VL + e]) : 0.f;
-        q = pack<T>(x);
-    }
-    return q;
-}
-template <typename T, bool RAG, bool ONCE>
-__device__ inline void store_raw(T* p, int v, int cols, const float* x)
-{
-    constexpr int VL = VecLen<T>::value;
-    if ((v + 1) * VL <= cols) {
-        store_row<ONCE>((Raw*)p + v, pack<T>(x));
-    } else if (RAG && v * VL < cols) {
-#pragma unroll
-        for (int e = 0; e < VL; ++e)
-            if (v * VL + e < cols) p[v * VL + e] = from_f<T>(x[e]);
-    }
-}
-// EPT columns of a thread's weights as fp32; `none` where there are none.
-template <typename T, int NV, int NTR>
-__device__ inline void load_weights(const void* w, bool w32, int t, int cols, float none, float* out)
-{
-    constexpr int VL = VecLen<T>::value;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int v = n * NTR + t;
-        float* x = out + n * VL;
-        if (w && (v + 1) * VL <= cols && w32) {
-            const Pack<float, VL> q = ((const Pack<float, VL>*)w)[v];
-#pragma unroll
-            for (int e = 0; e < VL; ++e) x[e] = q.v[e];
-        } else if (w && (v + 1) * VL <= cols) {
-            unpack<T>(((const Raw*)w)[v], x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VL; ++e) {
-                const int c = v * VL + e;
-                x[e] = !w || c >= cols ? none : w32 ? ((const float*)w)[c] : to_f(((const T*)w)[c]);
-            }
-        }
-    }
-}
-
-// A row's place among the RPB of its workgroup.
-template <int NTR>
-__device__ inline int row_place()
-{
-    const int sub = threadIdx.x / NTR;
-    return NTR < 64 ? sub : __builtin_amdgcn_readfirstlane(sub);
-}
-
-// Two sums over the NTR threads of a row: 16 lanes, or whole waves with one
-// barrier; tmp is another half at every other call (`turn`), so the next call
-// may write while this one reads.
-template <int NTR, int RPB>
-using RowTmp = float[2][RPB][NTR < 64 ? 1 : NTR / 64][2];
-template <int NTR, int RPB>
-__device__ inline void row_sums(float& a, float& b, RowTmp<NTR, RPB>& tmp, int turn)
-{
-    if constexpr (NTR == 16) {
-        a = row16_sum(a);
-        b = row16_sum(b);
-    } else {
-        constexpr int NWR = NTR / 64;
-        a = wave_sum(a);
-        b = wave_sum(b);
-        if (NWR == 1) return;
-        const int wave = threadIdx.x >> 6, sub = wave / NWR, w = wave % NWR;
-        if ((threadIdx.x & 63) == 0) {
-            tmp[turn][sub][w][0] = a;
-            tmp[turn][sub][w][1] = b;
-        }
-        __syncthreads();
-        a = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][0]);
-        b = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][1]);
-    }
-}
 
 // The variance is summed from the differences to the mean, which costs nothing
 // where the row is held.  Bound by memory: 16384 x 4096 bf16 51 us, 5.2 TB/s; 8
@@ -289,35 +196,9 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_norm_back(cons
         }
 }
 
-// The parts' sums: a workgroup takes 32 of the 2 cols columns, 32 threads each,
-// eight parts in flight a thread.  512 parts of 4096 columns: 4.8 us.
-constexpr int kJoinCols = 32, kJoinDeep = 32;
-__global__ __launch_bounds__(kJoinCols* kJoinDeep) void k_norm_join(const float* part, int64_t parts, int64_t cols,
-                                                                    float* dw, float* db, int add)
-{
-    __shared__ float tmp[kJoinDeep][kJoinCols];
-    const int tc = threadIdx.x % kJoinCols, td = threadIdx.x / kJoinCols;
-    const int64_t c = (int64_t)blockIdx.x * kJoinCols + tc;
-    float s = 0.f;
-    if (c < 2 * cols) {
-#pragma unroll 8
-        for (int64_t p = td; p < parts; p += kJoinDeep) s += part[2 * p * cols + c];
-    }
-    tmp[td][tc] = s;
-    __syncthreads();
-    if (td || c >= 2 * cols) return;
-#pragma unroll
-    for (int d = 1; d < kJoinDeep; ++d) s += tmp[d][tc];
-    float* out = c < cols ? dw : db;
-    const int64_t at = c < cols ? c : c - cols;
-    if (out) out[at] = add ? out[at] + s : s;
-}
-
 // ------------------------------------------------- rows that are not held
 // One workgroup of 16 waves a row, the row read again for every pass (from the
 // cache); the sums over the rows in a kernel of their own.
-constexpr int kLongThreads = 1024, kLongWaves = kLongThreads / 64;
-
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* x, int64_t xs, const W* w, const W* b, T* y,
                                                             int64_t ys, float* mean, float* rstd, int64_t rows,
@@ -387,38 +268,6 @@ __global__ __launch_bounds__(256) void k_norm_long_dw(const T* dy, int64_t dys, 
     }
     part[2 * (int64_t)blockIdx.y * cols + c] = aw;
     part[(2 * (int64_t)blockIdx.y + 1) * cols + c] = ab;
-}
-
-constexpr int64_t kNormMaxCols = (int64_t)1 << 20;
-
-static bool norm_opts_ok(const sgc_norm_opts* o)
-{
-    return o && o->rows >= 0 && o->rows < ((int64_t)1 << 31) && o->cols >= 1 && o->cols <= kNormMaxCols &&
-           lm_dtype(o->dtype) && (o->wdtype == SGC_F32 || o->wdtype == o->dtype) && o->eps >= 0.f &&
-           std::isfinite(o->eps) && (o->flags & ~SGC_NORM_ADD_GRADS) == 0;
-}
-
-// The shape of a workgroup for rows of `cols` held elements: 8 elements a
-// thread, in 16 lanes up to 128 columns and else in as few waves as that takes
-// (a power of two); 16 in the longest rows.  Where that would leave a quarter
-// of the waves idle, 16-bit rows take half the waves and 16 elements a thread
-// (46153 x 1300 bf16 backward: 151 -> 106 us; in fp32 16 elements spill), and
-// fp32 rows of 513 to 768 one wave and 12, backward only where a row is no
-// whole number of vectors (about 13 M elements: forward 577 23.3 -> 21.9 us,
-// 600 19.2 -> 18.5, 768 19.8; backward 515 43.2 -> 39.7, 650 39.9 -> 39.0, but
-// 600 34.2 -> 36.1 and 768 33.7 -> 36.5).  At least 8 waves.
-struct NormShape {
-    int ntr, ept, rpb;
-};
-static NormShape norm_shape(int64_t cols, int32_t dtype, bool back)
-{
-    if (cols <= 128) return {16, 8, 32};
-    if (dtype == SGC_F32 && cols > 512 && cols <= 768 && (!back || cols % 4)) return {64, 12, 8};
-    int ntr = 64, ept = 8;
-    while (ntr < 1024 && ntr * 8 < cols) ntr *= 2;
-    if (ntr * 8 < cols) ept = 16;
-    if (dtype != SGC_F32 && ntr > 64 && cols <= ntr * 6) ntr /= 2, ept = 16;
-    return {ntr, ept, ntr < 512 ? 512 / ntr : 1};
 }
 
 // Workgroups that share out the rows.
@@ -545,7 +394,7 @@ static int norm_backward(const sgc_norm_opts* o, const void* dyv, int64_t dys, c
     }
     if (part) {
         k_norm_join<<<(unsigned)cdiv(2 * o->cols, kJoinCols), kJoinCols * kJoinDeep, 0, s>>>(
-            part, parts, o->cols, dw, db, o->flags & SGC_NORM_ADD_GRADS);
+            part, parts, 2 * o->cols, o->cols, dw, db, o->flags & SGC_NORM_ADD_GRADS);
         SGC_LAUNCH_CHECK();
     }
     return SGC_OK;

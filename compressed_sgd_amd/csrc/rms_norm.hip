@@ -1,0 +1,156 @@
+// rms_norm.hip -- RMS norm of a residual stream with the addition before it,
+// its output in the stream's type or in 8 bits, and its backward pass.
+//
+//   s = x + residual,  rstd = (mean(s^2) + eps)^(-1/2),  y = s rstd w
+//   8 bits: p = s w, a = max |p|, q = rint(p (127 / a)), scale = (a / 127) rstd
+#include "norm_back.h"
+
+namespace sgc {
+
+struct Rms {
+    const void* x;
+    int64_t xs;
+    const void* res;
+    int64_t ress;
+    const void* w;
+    bool w32;
+    void* sum;
+    int64_t ss;
+    void* y;
+    int64_t ys;
+    int8_t* q;
+    int64_t qs;
+    float *qscale, *rstd;
+    int64_t rows;
+    int cols;
+    float eps;
+};
+
+// The largest magnitude over a workgroup of NW waves, in every thread.
+template <int NW>
+__device__ inline uint32_t block_umax(uint32_t x, uint32_t* tmp)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x = umax(x, (uint32_t)__shfl_xor((int)x, d, 64));
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < NW; ++w) x = umax(x, tmp[w]);
+    __syncthreads();
+    return x;
+}
+
+// One workgroup a row, the row read again for every pass.  Every element is
+// read and written by one thread alone, so the sum and y may take the inputs'
+// places; once the sum is written it is read instead of them.
+template <typename T>
+__global__ __launch_bounds__(kLongThreads) void k_rms_long(Rms k)
+{
+    __shared__ float tmp[kLongWaves];
+    __shared__ uint32_t utmp[kLongWaves];
+    const int64_t r = row_of_block();
+    if (r >= k.rows) return;
+    const T* x = (const T*)k.x + r * k.xs;
+    const T* res = k.res ? (const T*)k.res + r * k.ress : nullptr;
+    T* sum = k.sum ? (T*)k.sum + r * k.ss : nullptr;
+    float ss = 0.f;
+    uint32_t top = 0;
+    for (int c = threadIdx.x; c < k.cols; c += kLongThreads) {
+        const T t = res ? from_f<T>(to_f(x[c]) + to_f(res[c])) : x[c];
+        if (sum) sum[c] = t;
+        const float f = to_f(t);
+        ss = fmaf(f, f, ss);
+        if (k.q) top = umax(top, magnitude(f * weight_at<T>(k.w, k.w32, c, 1.f)));
+    }
+    const float rs = 1.f / sqrtf(block_sum<kLongWaves>(ss, tmp) / (float)k.cols + k.eps);
+    Quant u = {};
+    if (k.q) {
+        u = quant_of(block_umax<kLongWaves>(top, utmp));
+        if (threadIdx.x == 0) k.qscale[r] = u.scale * rs;
+    }
+    if (threadIdx.x == 0 && k.rstd) k.rstd[r] = rs;
+    for (int c = threadIdx.x; c < k.cols; c += kLongThreads) {
+        const T t = sum ? sum[c] : res ? from_f<T>(to_f(x[c]) + to_f(res[c])) : x[c];
+        const float w = weight_at<T>(k.w, k.w32, c, 1.f), f = to_f(t);
+        if (k.q) k.q[r * k.qs + c] = (int8_t)(quantized(f * w, u) & u.keep);
+        if (k.y) ((T*)k.y)[r * k.ys + c] = from_f<T>(f * rs * w);
+    }
+}
+
+template <typename T>
+static int rms_forward(const Rms& k, hipStream_t s)
+{
+    k_rms_long<T><<<row_grid(k.rows), kLongThreads, 0, s>>>(k);
+    SGC_LAUNCH_CHECK();
+    return SGC_OK;
+}
+
+}  // namespace sgc
+
+using namespace sgc;
+
+extern "C" int sgc_rms_norm(const sgc_norm_opts* o, const void* x, int64_t x_stride, const void* residual,
+                            int64_t r_stride, const void* weight, void* sum, int64_t s_stride, void* y,
+                            int64_t y_stride, int8_t* q, int64_t q_stride, float* qscale, float* rstd,
+                            sgc_stream_t stream)
+{
+    if (!norm_opts_ok(o) || o->flags) return SGC_EINVAL;
+    if (o->rows == 0) return SGC_OK;
+    if (!y == !q || !q != !qscale) return SGC_EINVAL;
+    const int64_t n = o->rows, c = o->cols;
+    if (!lm_rows_ok(x, x_stride, n, c, o->dtype, false)) return SGC_EINVAL;
+    if (residual && !lm_rows_ok(residual, r_stride, n, c, o->dtype, false)) return SGC_EINVAL;
+    if (sum && !lm_rows_ok(sum, s_stride, n, c, o->dtype, true)) return SGC_EINVAL;
+    if (y && (!lm_rows_ok(y, y_stride, n, c, o->dtype, true) || y == sum)) return SGC_EINVAL;
+    if (q && !q8_rows_ok(q, q_stride, n, c, true)) return SGC_EINVAL;
+    if (!lm_aligned(weight, lm_size(o->wdtype)) || !lm_aligned(qscale, 4) || !lm_aligned(rstd, 4)) return SGC_EINVAL;
+    const Rms k = {x,        x_stride, residual, r_stride, weight, o->wdtype == SGC_F32, sum, s_stride, y, y_stride, q,
+                   q_stride, qscale,   rstd,     n,        (int)c, o->eps};
+    const hipStream_t s = (hipStream_t)stream;
+    return o->dtype == SGC_F32    ? rms_forward<float>(k, s)
+           : o->dtype == SGC_BF16 ? rms_forward<bf16_t>(k, s)
+                                  : rms_forward<f16_t>(k, s);
+}
+
+extern "C" size_t sgc_rms_norm_backward_workspace(const sgc_norm_opts* o)
+{
+    if (!norm_opts_ok(o)) return 0;
+    Carver c(nullptr);
+    c.take<float>(back_parts(o->rows, o->cols, o->dtype) * o->cols);
+    return c.off;
+}
+
+extern "C" int sgc_rms_norm_backward(const sgc_norm_opts* o, const void* dy, int64_t dy_stride, const void* x,
+                                     int64_t s_stride, const void* weight, const float* rstd, const void* dsum,
+                                     int64_t dsum_stride, void* dx, int64_t dx_stride, float* dweight, void* ws,
+                                     size_t ws_bytes, sgc_stream_t stream)
+{
+    if (!norm_opts_ok(o)) return SGC_EINVAL;
+    if (!lm_aligned(dweight, 4) || !lm_aligned(weight, lm_size(o->wdtype))) return SGC_EINVAL;
+    if (o->rows) {
+        if (!lm_rows_ok(dy, dy_stride, o->rows, o->cols, o->dtype, false)) return SGC_EINVAL;
+        if (!lm_rows_ok(x, s_stride, o->rows, o->cols, o->dtype, false)) return SGC_EINVAL;
+        if (dsum && !lm_rows_ok(dsum, dsum_stride, o->rows, o->cols, o->dtype, false)) return SGC_EINVAL;
+        if (dx && !lm_rows_ok(dx, dx_stride, o->rows, o->cols, o->dtype, true)) return SGC_EINVAL;
+        if (!rstd || !lm_aligned(rstd, 4)) return SGC_EINVAL;
+    }
+    float* part = nullptr;
+    if (dweight) {
+        if (!ws || ws_bytes < sgc_rms_norm_backward_workspace(o)) return SGC_ENOSPC;
+        if (!aligned16(ws)) return SGC_EINVAL;
+        part = Carver(ws).take<float>(1);
+    }
+    const Back k = {dy, dy_stride, weight,  nullptr, o->wdtype == SGC_F32, nullptr, rstd, dsum, dsum_stride,
+                    dx, dx_stride, nullptr, 0,       part,                 o->rows, (int)o->cols};
+    const hipStream_t s = (hipStream_t)stream;
+    const bool add = o->flags & SGC_NORM_ADD_GRADS;
+    switch (o->dtype) {
+    case SGC_F32:
+        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+    case SGC_BF16:
+        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add,
+                                                      s);
+    default:
+        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+    }
+}

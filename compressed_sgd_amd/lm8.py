@@ -1,0 +1,377 @@
+"""Between a language model's body and its loss, in 8 bits: RMS norm of a
+residual stream, activations kept in 8 bits for the backward pass, and products
+of 8-bit integers.
+
+Thin marshalling over the C ABI (include/sgc.h), as in ``lm``, whose
+conventions hold here too: 2-D tensors with contiguous rows at any stride,
+gradients as explicit calls, a tensor that requires grad refused while grad
+mode is on.  Rows in 8 bits travel as ``Quantized``: what ``rms_norm_q8`` and
+``quantize_q8`` give, the backward calls and ``int8_linear`` take.  Calls run
+on the tensors' device, whichever is current.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _check, lib
+from .lm import (_DTYPES, NORM_ADD_GRADS, NormOpts, _affine, _empty, _no_graph, _ptr, _rows, _scratch, _stream, _vec,
+                 _vec1, _written)
+
+NORM_LAYER, NORM_RMS = 0, 1
+Q8_GROUPS = (0, 32, 64, 128, 256)
+
+
+class Q8Opts(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("dtype", C.c_int32), ("group", C.c_int32)]
+
+
+class NormQ8Opts(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("dtype", C.c_int32), ("wdtype", C.c_int32),
+                ("group", C.c_int32), ("kind", C.c_int32), ("flags", C.c_int32), ("reserved", C.c_int32)]
+
+
+class Int8Opts(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("width", C.c_int64), ("out", C.c_int64), ("dtype", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+def _declare(L) -> None:
+    P, i64, sz = C.c_void_p, C.c_int64, C.c_size_t
+    for name, args, res in (
+            ("sgc_rms_norm", [P, P, i64, P, i64, P, P, i64, P, i64, P, i64, P, P, P], C.c_int),
+            ("sgc_rms_norm_backward_workspace", [P], sz),
+            ("sgc_rms_norm_backward", [P, P, i64, P, i64, P, P, P, i64, P, i64, P, P, sz, P], C.c_int),
+            ("sgc_quantize_q8", [P, P, i64, P, i64, P, P], C.c_int),
+            ("sgc_dequantize_q8", [P, P, i64, P, P, i64, P], C.c_int),
+            ("sgc_norm_backward_q8_workspace", [P], sz),
+            ("sgc_norm_backward_q8", [P, P, i64, P, i64, P, P, P, P, P, P, i64, P, i64, P, i64, P, P, P, sz, P],
+             C.c_int),
+            ("sgc_int8_linear", [P, P, i64, P, P, i64, P, P, P, i64, P], C.c_int)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+
+
+def _run(name: str, device: torch.device, stream, *args) -> None:
+    """Calls the library with the device of the tensors current."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == device.index:
+        rc = f(*args, _stream(device, stream))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, _stream(device, stream))
+    _check(rc, name)
+
+
+# ------------------------------------------------------------- 8 bits
+@dataclass
+class Quantized:
+    """Rows in 8 bits: q * scale, a scale every `group` elements of a row (0: one a row)."""
+    q: torch.Tensor      # int8 [rows, cols], any row stride
+    scale: torch.Tensor  # float32 [rows, groups of a row]
+    group: int = 0
+
+
+def _groups(cols: int, group: int) -> int:
+    if group not in Q8_GROUPS:
+        raise ValueError(f"group must be one of {Q8_GROUPS}")
+    return -(-cols // group) if group else 1
+
+
+def _q8(t: Quantized, name: str, device=None, rows: Optional[int] = None, cols: Optional[int] = None) -> int:
+    """Checks 8-bit rows; their stride."""
+    q = t.q
+    if not q.is_cuda:
+        raise ValueError(f"{name}.q must be a device (HIP) tensor")
+    if q.dim() != 2 or q.dtype != torch.int8:
+        raise ValueError(f"{name}.q must be 2-D int8")
+    stride = q.stride()
+    if stride[1] != 1 and q.shape[1] > 1:
+        raise ValueError(f"{name}.q must have contiguous rows")
+    if (device is not None and q.device != device) or (rows is not None and q.shape[0] != rows) or \
+            (cols is not None and q.shape[1] != cols):
+        raise ValueError(f"{name}.q must match the call's shape and device")
+    _vec(t.scale, f"{name}.scale", (q.shape[0], _groups(q.shape[1], t.group)), torch.float32, q.device)
+    return stride[0]
+
+
+def _new_q8(stream, rows: int, cols: int, group: int, device) -> Quantized:
+    """Rows that begin at multiples of 16 bytes, which the products read fastest."""
+    q = _empty(stream, (rows, -(-cols // 16) * 16), torch.int8, device)
+    return Quantized(q if q.shape[1] == cols else q[:, :cols],
+                     _empty(stream, (rows, _groups(cols, group)), torch.float32, device), group)
+
+
+def quantize_q8(x: torch.Tensor, *, group: int = 128, out: Optional[Quantized] = None, stream=None) -> Quantized:
+    """Rows of x in 8 bits, a scale every `group` elements (32, 64, 128, 256), or one a row (0): activations kept
+    for the backward pass; weights, which int8_linear reads (group 0)."""
+    _no_graph(x)
+    xs = _rows(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    if out is None:
+        to = _new_q8(stream, rows, cols, group, dev)
+        qs = to.q.stride(0)
+    else:
+        to = out
+        if out.group != group:
+            raise ValueError("out.group must be the call's group")
+        qs = _q8(out, "out", dev, rows, cols)
+    o = Q8Opts(rows, cols, _DTYPES[x.dtype], group)
+    _run("sgc_quantize_q8", dev, stream, C.byref(o), _ptr(x), xs, _ptr(to.q), qs, _ptr(to.scale))
+    if out is not None:
+        _written(out.q, out.scale)
+    return to
+
+
+def dequantize_q8(x: Quantized, dtype: torch.dtype = torch.float32, *, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """The values that 8-bit rows stand for."""
+    _no_graph(x.scale, out)
+    qs = _q8(x, "x")
+    rows, cols = x.q.shape
+    dev = x.q.device
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    if out is None:
+        to, xs = _empty(stream, (rows, cols), dtype, dev), cols
+    else:
+        to, xs = out, _rows(out, "out")
+        if out.shape != x.q.shape or out.dtype != dtype or out.device != dev:
+            raise ValueError("out must match the rows' shape and device and the type asked for")
+    o = Q8Opts(rows, cols, _DTYPES[dtype], x.group)
+    _run("sgc_dequantize_q8", dev, stream, C.byref(o), _ptr(x.q), qs, _ptr(x.scale), _ptr(to), xs)
+    _written(out)
+    return to
+
+
+# ----------------------------------------------------------------- RMS norm
+@dataclass
+class RmsNormalized:
+    y: torch.Tensor
+    sum: torch.Tensor    # the residual stream after the addition; x where there is none
+    rstd: torch.Tensor   # float32 [rows]
+
+
+@dataclass
+class RmsQuantized:
+    q8: Quantized        # the normed rows, one scale a row
+    sum: torch.Tensor
+    rstd: torch.Tensor
+
+
+@dataclass
+class RmsGrads:
+    dx: Optional[torch.Tensor]        # of the stream: of x and of the residual
+    dweight: Optional[torch.Tensor]   # float32 [cols]
+
+
+def _rms(x, weight, residual, sum_out, eps, y, ys, q8, qs, stream):
+    xs = _rows(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    wdt = _affine(weight, None, x, cols, dev)
+    rs = 0 if residual is None else _rows(residual, "residual", x)
+    if sum_out is not None:
+        total, ss = sum_out, _rows(sum_out, "sum_out", x)
+    elif residual is not None:
+        total, ss = _empty(stream, (rows, cols), x.dtype, dev), cols
+    else:
+        total, ss = None, 0
+    rstd = _empty(stream, (rows,), torch.float32, dev)
+    o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, eps, 0)
+    _run("sgc_rms_norm", dev, stream, C.byref(o), _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(total), ss,
+         _ptr(y), ys, None if q8 is None else _ptr(q8.q), qs, None if q8 is None else _ptr(q8.scale), _ptr(rstd))
+    _written(sum_out)
+    return x if total is None else total, rstd
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+             stream=None) -> RmsNormalized:
+    """RMS norm of every row of x + residual [rows, cols]; the sum, rounded to
+    x's type, is given too.  out and sum_out may be x or residual, not the
+    same one."""
+    _no_graph(x, weight, residual, out, sum_out)
+    _rows(x, "x")
+    if out is None:
+        y, ys = _empty(stream, x.shape, x.dtype, x.device), x.shape[1]
+    else:
+        y, ys = out, _rows(out, "out", x)
+    total, rstd = _rms(x, weight, residual, sum_out, eps, y, ys, None, 0, stream)
+    _written(out)
+    return RmsNormalized(y, total, rstd)
+
+
+def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out: Optional[Quantized] = None, sum_out: Optional[torch.Tensor] = None,
+                stream=None) -> RmsQuantized:
+    """rms_norm with its output in 8 bits, a scale a row: what int8_linear takes."""
+    _no_graph(x, weight, residual, sum_out)
+    _rows(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        q8 = _new_q8(stream, rows, cols, 0, x.device)
+        qs = q8.q.stride(0)
+    else:
+        if out.group:
+            raise ValueError("out must have one scale a row (group 0)")
+        q8, qs = out, _q8(out, "out", x.device, rows, cols)
+    total, rstd = _rms(x, weight, residual, sum_out, eps, None, 0, q8, qs, stream)
+    if out is not None:
+        _written(out.q, out.scale)
+    return RmsQuantized(q8, total, rstd)
+
+
+def rms_norm_backward_workspace_bytes(rows: int, cols: int, dtype: torch.dtype = torch.float32) -> int:
+    return int(lib().sgc_rms_norm_backward_workspace(
+        C.byref(NormOpts(rows, cols, _DTYPES[dtype], _DTYPES[torch.float32], 0.0, 0))))
+
+
+def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor, *,
+                      dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                      dweight: Optional[torch.Tensor] = None, accumulate: bool = False, want_dx: bool = True,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> RmsGrads:
+    """Gradients of rms_norm at the stream s (the forward call's sum).  dsum is
+    the gradient that reaches the stream past the norm.  dweight (float32, e.g.
+    a slice of a flat gradient) is written, or with accumulate added to.  dx
+    may be dy, s or dsum."""
+    _no_graph(dy, s, weight, rstd, dsum, dx, dweight)
+    ss = _rows(s, "s")
+    dys = _rows(dy, "dy", s)
+    rows, cols = s.shape
+    dev = s.device
+    wdt = _affine(weight, None, s, cols, dev)
+    _vec1(rstd, "rstd", rows, torch.float32, dev)
+    _vec1(dweight, "dweight", cols, torch.float32, dev)
+    dss = 0 if dsum is None else _rows(dsum, "dsum", s)
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs dweight")
+    given = (dx, dweight)
+    if dx is None and want_dx:
+        dx = _empty(stream, (rows, cols), s.dtype, dev)
+    dxs = 0 if dx is None else _rows(dx, "dx", s)
+    if dweight is None:
+        dweight = _empty(stream, (cols,), torch.float32, dev)
+    o = NormOpts(rows, cols, _DTYPES[s.dtype], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
+    need = lib().sgc_rms_norm_backward_workspace(C.byref(o))
+    ws = _scratch(need, ws, dev, "rms_norm", stream, "sgc_rms_norm_backward_workspace")
+    _run("sgc_rms_norm_backward", dev, stream, C.byref(o), _ptr(dy), dys, _ptr(s), ss, _ptr(weight), _ptr(rstd),
+         _ptr(dsum), dss, _ptr(dx), dxs, _ptr(dweight), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    _written(*given)
+    return RmsGrads(dx, dweight)
+
+
+# ------------------------------------------- norms from activations in 8 bits
+@dataclass
+class NormQ8Grads:
+    dx: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]   # float32 [cols]
+    dbias: Optional[torch.Tensor]     # float32 [cols]; None for an RMS norm
+    y: Optional[torch.Tensor]         # the norm's output from the 8 bits, where wanted
+
+
+def norm_backward_q8_workspace_bytes(rows: int, cols: int, *, kind: int = NORM_RMS, group: int = 128,
+                                     dtype: torch.dtype = torch.float32) -> int:
+    """Workspace bytes of one rms_norm_backward_q8 (NORM_RMS) or layer_norm_backward_q8 (NORM_LAYER) call."""
+    return int(lib().sgc_norm_backward_q8_workspace(
+        C.byref(NormQ8Opts(rows, cols, _DTYPES[dtype], _DTYPES[torch.float32], group, kind, 0, 0))))
+
+
+def _backward_q8(kind, dy, x, weight, bias, mean, rstd, dsum, dx, dweight, dbias, accumulate, want_dx, want_y, y, ws,
+                 stream) -> NormQ8Grads:
+    _no_graph(dy, x.scale, weight, bias, mean, rstd, dsum, dx, dweight, dbias, y)
+    layer = kind == NORM_LAYER
+    dys = _rows(dy, "dy")
+    rows, cols = dy.shape
+    dev = dy.device
+    qs = _q8(x, "x", dev, rows, cols)
+    wdt = _affine(weight, bias, dy, cols, dev)
+    for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (dweight, "dweight", cols),
+                       (dbias, "dbias", cols)):
+        _vec1(t, name, n, torch.float32, dev)
+    dss = 0 if dsum is None else _rows(dsum, "dsum", dy)
+    if accumulate and (dweight is None or (layer and dbias is None)):
+        raise ValueError("accumulate needs dweight" + (" and dbias" if layer else ""))
+    given = (dx, dweight, dbias, y)
+    if dx is None and want_dx:
+        dx = _empty(stream, (rows, cols), dy.dtype, dev)
+    dxs = 0 if dx is None else _rows(dx, "dx", dy)
+    if y is None and want_y:
+        y = _empty(stream, (rows, cols), dy.dtype, dev)
+    ys = 0 if y is None else _rows(y, "y", dy)
+    if dweight is None:
+        dweight = _empty(stream, (cols,), torch.float32, dev)
+    if dbias is None and layer:
+        dbias = _empty(stream, (cols,), torch.float32, dev)
+    o = NormQ8Opts(rows, cols, _DTYPES[dy.dtype], wdt, x.group, kind, NORM_ADD_GRADS if accumulate else 0, 0)
+    need = lib().sgc_norm_backward_q8_workspace(C.byref(o))
+    ws = _scratch(need, ws, dev, "norm_q8", stream, "sgc_norm_backward_q8_workspace")
+    _run("sgc_norm_backward_q8", dev, stream, C.byref(o), _ptr(dy), dys, _ptr(x.q), qs, _ptr(x.scale), _ptr(weight),
+         _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dsum), dss, _ptr(dx), dxs, _ptr(y), ys, _ptr(dweight), _ptr(dbias),
+         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    _written(*given)
+    return NormQ8Grads(dx, dweight, dbias, y)
+
+
+def rms_norm_backward_q8(dy: torch.Tensor, x: Quantized, weight: Optional[torch.Tensor], rstd: torch.Tensor, *,
+                         dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         dweight: Optional[torch.Tensor] = None, accumulate: bool = False, want_dx: bool = True,
+                         want_y: bool = False, y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                         stream=None) -> NormQ8Grads:
+    """rms_norm_backward with the stream kept in 8 bits; with want_y (or a
+    buffer y) the norm's output too, which the next product's weight gradient
+    reads.  dx may be dy or dsum."""
+    return _backward_q8(NORM_RMS, dy, x, weight, None, None, rstd, dsum, dx, dweight, None, accumulate, want_dx,
+                        want_y, y, ws, stream)
+
+
+def layer_norm_backward_q8(dy: torch.Tensor, x: Quantized, weight: Optional[torch.Tensor],
+                           bias: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor, *,
+                           dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                           dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                           accumulate: bool = False, want_dx: bool = True, want_y: bool = False,
+                           y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                           stream=None) -> NormQ8Grads:
+    """layer_norm_backward with the norm's input kept in 8 bits; the rest as in
+    rms_norm_backward_q8.  bias is read for y alone."""
+    if mean is None:
+        raise ValueError("a layer norm's backward pass needs mean")
+    return _backward_q8(NORM_LAYER, dy, x, weight, bias, mean, rstd, dsum, dx, dweight, dbias, accumulate, want_dx,
+                        want_y, y, ws, stream)
+
+
+# ------------------------------------------------------ products in 8 bits
+def int8_linear(x: Quantized, w: Quantized, bias: Optional[torch.Tensor] = None, *,
+                dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Product of rows in 8 bits [rows, width] with weights in 8 bits [out,
+    width], each with one scale a row, plus bias [out] float32.  For scoring and
+    serving: it has no gradient.  Rows that begin at multiples of 16 bytes, as
+    quantize_q8 and rms_norm_q8 lay them out, are read fastest."""
+    _no_graph(x.scale, w.scale, bias, out)
+    if x.group or w.group:
+        raise ValueError("a product takes one scale a row (group 0)")
+    xs = _q8(x, "x")
+    rows, width = x.q.shape
+    dev = x.q.device
+    wst = _q8(w, "w", dev, None, width)
+    n = w.q.shape[0]
+    _vec1(bias, "bias", n, torch.float32, dev)
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    if out is None:
+        y, ys = _empty(stream, (rows, n), dtype, dev), n
+    else:
+        y, ys = out, _rows(out, "out")
+        if out.shape != (rows, n) or out.dtype != dtype or out.device != dev:
+            raise ValueError("out must match the product's shape and device and the type asked for")
+    o = Int8Opts(rows, width, n, _DTYPES[dtype], 0)
+    _run("sgc_int8_linear", dev, stream, C.byref(o), _ptr(x.q), xs, _ptr(x.scale), _ptr(w.q), wst, _ptr(w.scale),
+         _ptr(bias), _ptr(y), ys)
+    _written(out)
+    return y

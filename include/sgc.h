@@ -496,6 +496,102 @@ int sgc_distill_backward(const sgc_distill_opts* opt, const void* logits, int64_
                          const float* t_val, const float* stats, const float* dloss, void* dlogits, int64_t dstride,
                          sgc_stream_t stream);
 
+/* RMS norm of a residual stream, with the addition before it.
+ *   s = x + residual, added in fp32, rounded to dtype (residual NULL: s = x)
+ *   rstd = (sum(s^2) / cols + eps)^(-1/2);  y = s * rstd * weight
+ * sum receives s, y the normed rows, q and qscale [rows] the normed rows in 8
+ * bits, with p = s * weight and a = max |p| over the row, each fp32:
+ *   q = rint(p * r), r = 127 / a;  qscale = (a / 127) * rstd;
+ * q * qscale stands for y.  rstd is left out of q: it cancels, so q does not
+ * depend on how the squares were summed.  A row with a = 0 has q = 0 and
+ * qscale 0, one with a p that is not finite q = 0 and qscale NaN.  Squares whose
+ * sum passes fp32's range leave rstd 0, as the formula does.  Either of y and
+ * q may be NULL, not both; sum, qscale (only without q), rstd [rows fp32] and
+ * weight (NULL: 1) may be NULL.  sum and y may be x or residual, not the same
+ * one, at the same address and stride; no other overlap.  Options as for the
+ * layer norm; flags 0.
+ *
+ * Backward, with h = s * rstd, v = dy * weight, and dsum the gradient that
+ * reaches s past the norm (NULL: none):
+ *   dx = rstd * (v - h * mean(v * h)) + dsum;  dweight = sum over the rows of dy * h
+ * dx is the gradient of s, so of x and of residual.  dweight as in
+ * sgc_layer_norm_backward, SGC_NORM_ADD_GRADS too.  dx and dweight may each be
+ * NULL; dx may be dy, s or dsum, at the same address and stride.          */
+int sgc_rms_norm(const sgc_norm_opts* opt, const void* x, int64_t x_stride, const void* residual, int64_t r_stride,
+                 const void* weight, void* sum, int64_t s_stride, void* y, int64_t y_stride, int8_t* q,
+                 int64_t q_stride, float* qscale, float* rstd, sgc_stream_t stream);
+size_t sgc_rms_norm_backward_workspace(const sgc_norm_opts* opt);
+int sgc_rms_norm_backward(const sgc_norm_opts* opt, const void* dy, int64_t dy_stride, const void* s,
+                          int64_t s_stride, const void* weight, const float* rstd, const void* dsum,
+                          int64_t dsum_stride, void* dx, int64_t dx_stride, float* dweight, void* ws, size_t ws_bytes,
+                          sgc_stream_t stream);
+
+/* Rows kept in 8 bits: q [rows, cols] int8 and a scale for every `group`
+ * elements of a row (the last group may be short), or for the whole row
+ * (group 0); scale [rows, ceil(cols / group)] fp32, contiguous.  With a = max |x|
+ * over the group, each step rounded to fp32:
+ *   q = rint(x * r), r = 127 / a;  scale = a / 127;  q * scale stands for x
+ * (where a < 2^-100, x and a are multiplied by 2^100 before q is taken).  A group
+ * of zeros has q = 0 and scale 0, one that holds a value that is not finite q =
+ * 0 and scale NaN.  group: 0, 32, 64, 128 or 256; 1 <= cols <= 2^20.
+ * sgc_dequantize_q8 writes q * scale, rounded to dtype.                    */
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int32_t dtype; /* x */
+    int32_t group;
+} sgc_q8_opts;
+
+int sgc_quantize_q8(const sgc_q8_opts* opt, const void* x, int64_t x_stride, int8_t* q, int64_t q_stride,
+                    float* scale, sgc_stream_t stream);
+int sgc_dequantize_q8(const sgc_q8_opts* opt, const int8_t* q, int64_t q_stride, const float* scale, void* x,
+                      int64_t x_stride, sgc_stream_t stream);
+
+/* The backward pass of a norm whose input was kept in 8 bits: that of
+ * sgc_layer_norm_backward (SGC_NORM_LAYER; mean and rstd the forward call's) or
+ * of sgc_rms_norm_backward (SGC_NORM_RMS; rstd alone, no mean, no dbias), with
+ * x = q * scale, and with y, the norm's output from x (weight, and
+ * bias for a layer norm), which the next product's weight gradient reads.  dsum
+ * (may be NULL) is added to dx in both kinds.  dx, y, dweight and dbias may
+ * each be NULL; dx may be dy or dsum, at the same address and stride.      */
+#define SGC_NORM_LAYER 0
+#define SGC_NORM_RMS 1
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int32_t dtype;  /* dy, dsum, dx, y */
+    int32_t wdtype; /* weight, bias: SGC_F32, or dtype */
+    int32_t group;
+    int32_t kind;   /* SGC_NORM_LAYER | SGC_NORM_RMS */
+    int32_t flags;  /* 0 | SGC_NORM_ADD_GRADS */
+    int32_t reserved; /* 0 */
+} sgc_norm_q8_opts;
+
+size_t sgc_norm_backward_q8_workspace(const sgc_norm_q8_opts* opt);
+int sgc_norm_backward_q8(const sgc_norm_q8_opts* opt, const void* dy, int64_t dy_stride, const int8_t* q,
+                         int64_t q_stride, const float* scale, const void* weight, const void* bias,
+                         const float* mean, const float* rstd, const void* dsum, int64_t dsum_stride, void* dx,
+                         int64_t dx_stride, void* y, int64_t y_stride, float* dweight, float* dbias, void* ws,
+                         size_t ws_bytes, sgc_stream_t stream);
+
+/* Product of 8-bit rows, tokens and channels each with a scale:
+ *   y[r, o] = sum over i of xq[r, i] * wq[o, i] * xscale[r] * wscale[o] + bias[o]
+ * The sum is a whole number, exact in 32 bits (hence width < 2^17), the rest
+ * fp32, rounded once to dtype.  xq, wq may hold -128 too.  bias [out fp32] may
+ * be NULL.  No overlap.  1 <= width < 2^17, 1 <= out < 2^31.  Rows of xq and
+ * wq that begin at multiples of 16 bytes are read fastest.                  */
+typedef struct {
+    int64_t rows;
+    int64_t width;
+    int64_t out;
+    int32_t dtype;    /* y */
+    int32_t reserved; /* 0 */
+} sgc_int8_opts;
+
+int sgc_int8_linear(const sgc_int8_opts* opt, const int8_t* xq, int64_t xq_stride, const float* xscale,
+                    const int8_t* wq, int64_t wq_stride, const float* wscale, const float* bias, void* y,
+                    int64_t y_stride, sgc_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Measurement hook (benchmarks only).  While set, every sgc_compress call
  * (modes SGC_EXACT and SGC_SAMPLED) records `start` on its stream just
