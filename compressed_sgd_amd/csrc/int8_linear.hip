@@ -1,5 +1,11 @@
 // int8_linear.hip -- product of 8-bit rows with a scale for each token and each
 // channel: y = (sum xq wq) xscale wscale + bias.
+//
+// Both operands lie along the sum, 16 of a row's bytes in a lane are one
+// operand of a matrix instruction, and the order within the sum is free as long
+// as both sides take the same.  The weights' rows are the instruction's first
+// operand: a lane then holds four neighbouring channels of one token, which it
+// stores together.
 #include "lm_q8.h"
 
 namespace sgc {
@@ -17,33 +23,272 @@ struct Product {
     int width;
 };
 
-// The sum is a whole number below 2^31; one fp32 rounding of it, one for each
-// scale, one for the bias, one to the output's type.
-template <typename T>
-__device__ inline T product_out(int32_t sum, float xscale, float wscale, float bias)
+typedef int Int4 __attribute__((ext_vector_type(4)));
+typedef int Int16 __attribute__((ext_vector_type(16)));
+// 16 bytes of a row, at any address.
+typedef int Bytes16 __attribute__((ext_vector_type(4), aligned(1)));
+
+// Bytes [at, at + 16) of a row of `width`; past it 0.
+__device__ inline Int4 load16(const int8_t* row, int at, int width)
 {
-    return from_f<T>((float)sum * xscale * wscale + bias);
+    if (at + 16 <= width) return *(const Bytes16*)(row + at);
+    Int4 v = {0, 0, 0, 0};
+    if (at < width) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (at + i < width) v[i / 4] |= (int)(uint8_t)row[at + i] << (i % 4 * 8);
+    }
+    return v;
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_product(Product k)
+// The sum is a whole number below 2^31: one fp32 rounding of it, one for each
+// scale, one for the bias, one to the output's type.
+__device__ inline float product_out(int32_t sum, float xscale, float wscale, float bias)
 {
-    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (o >= k.out) return;
-    for (int64_t r = blockIdx.y; r < k.rows; r += gridDim.y) {
-        int32_t sum = 0;
-        for (int i = 0; i < k.width; ++i) sum += (int)k.x[r * k.xs + i] * (int)k.w[o * k.ws + i];
-        ((T*)k.y)[r * k.ys + o] = product_out<T>(sum, k.xscale[r], k.wscale[o], k.bias ? k.bias[o] : 0.f);
+    return (float)sum * xscale * wscale + bias;
+}
+// Four neighbouring channels of one token.
+template <typename T>
+__device__ inline void store4(const Product& k, int64_t r, int64_t o, const float* v)
+{
+    T* y = (T*)k.y + r * k.ys + o;
+    if (o + 4 <= k.out) {
+        Pack<T, 4> p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.v[i] = from_f<T>(v[i]);
+        *(Pack<T, 4>*)y = p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (o + i < k.out) y[i] = from_f<T>(v[i]);
     }
+}
+__device__ inline void channel4(const Product& k, int64_t o, float* scale, float* bias)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = o + i < k.out ? o + i : k.out - 1;
+        scale[i] = k.wscale[at];
+        bias[i] = k.bias ? k.bias[at] : 0.f;
+    }
+}
+
+// --------------------------------------------------------------- tiles
+// A workgroup takes TM tokens x TN channels, its WM x WN waves a part each; 128
+// bytes of every row go through shared memory at a time, the next ones on their
+// way in registers while the matrix units work.  A row's 16-byte pieces lie in
+// shared memory at piece ^ (row mod 8): eight rows' same piece, which lanes
+// read together, and one row's eight pieces, which they write together, both
+// lie in all banks once.
+constexpr int kStep = 128;
+template <typename T, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m, int tiles_n)
+{
+    constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 32, PN = TN / WN / 32;
+    constexpr int CX = TM * 8 / kThreads, CW = TN * 8 / kThreads, kRows = kThreads / 8;
+    __shared__ Int4 sx[2][TM * 8], sw[2][TN * 8];
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
+    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * TM, n0 = (int64_t)(blockIdx.x / tiles_m) * TN;
+    // rows past the last one read the last one; what they give is not written
+    const int piece = t & 7, row = t >> 3, put = row * 8 + (piece ^ (row & 7));
+    const int8_t *px[CX], *pw[CW];
+#pragma unroll
+    for (int i = 0; i < CX; ++i) {
+        const int64_t r = m0 + row + i * kRows;
+        px[i] = k.x + (r < k.rows ? r : k.rows - 1) * k.xs;
+    }
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        const int64_t r = n0 + row + i * kRows;
+        pw[i] = k.w + (r < k.out ? r : k.out - 1) * k.ws;
+    }
+    Int4 rx[CX], rw[CW];
+    const auto fetch = [&](int step) {
+        const int at = step * kStep + piece * 16;
+        if ((step + 1) * kStep <= k.width) {
+#pragma unroll
+            for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + at);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CX; ++i) rx[i] = load16(px[i], at, k.width);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) rw[i] = load16(pw[i], at, k.width);
+        }
+    };
+    const auto deposit = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < CX; ++i) sx[b][put + i * kRows * 8] = rx[i];
+#pragma unroll
+        for (int i = 0; i < CW; ++i) sw[b][put + i * kRows * 8] = rw[i];
+    };
+    Int16 acc[PN][PM];
+#pragma unroll
+    for (int i = 0; i < PN; ++i)
+#pragma unroll
+        for (int j = 0; j < PM; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+    const int steps = (k.width + kStep - 1) / kStep;
+    const int lr = lane & 31, half = lane >> 5;
+    const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
+    fetch(0);
+    deposit(0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        const int b = s & 1;
+        if (s + 1 < steps) fetch(s + 1);
+#pragma unroll
+        for (int kk = 0; kk < kStep / 32; ++kk) {
+            const int p = (kk * 2 + half) ^ (lr & 7);
+            Int4 fx[PM], fw[PN];
+#pragma unroll
+            for (int j = 0; j < PM; ++j) fx[j] = sx[b][ax + j * 256 + p];
+#pragma unroll
+            for (int i = 0; i < PN; ++i) fw[i] = sw[b][aw + i * 256 + p];
+#pragma unroll
+            for (int i = 0; i < PN; ++i)
+#pragma unroll
+                for (int j = 0; j < PM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fx[j], acc[i][j], 0, 0, 0);
+        }
+        if (s + 1 < steps) deposit(b ^ 1);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < PM; ++j) {
+        const int64_t r = m0 + (wm * PM + j) * 32 + lr;
+        if (r >= k.rows) continue;
+        const float xscale = k.xscale[r];
+#pragma unroll
+        for (int i = 0; i < PN; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int64_t o = n0 + (wn * PN + i) * 32 + e * 2 + half * 4;
+                if (o >= k.out) continue;
+                float ws[4], bias[4], v[4];
+                channel4(k, o, ws, bias);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = product_out(acc[i][j][e + c], xscale, ws[c], bias[c]);
+                store4<T>(k, r, o, v);
+            }
+    }
+}
+
+// ------------------------------------------------------------- few tokens
+// A wave takes 16 channels x 16 B tokens and a share of the sum, straight from
+// memory into the matrix instruction; the S waves of the same channels join
+// their sums in shared memory.
+constexpr int kFewWaves = 8, kFewDeep = 8;
+template <typename T, int B>
+__global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
+{
+    __shared__ Int4 part[kFewWaves][B][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int share = wave % split, per = kFewWaves / split;
+    const int64_t n0 = ((int64_t)blockIdx.x * per + wave / split) * 16;
+    const int64_t m0 = (int64_t)blockIdx.y * 16 * B;
+    const int lr = lane & 15, quarter = lane >> 4;
+    Int4 acc[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) acc[j] = Int4{0, 0, 0, 0};
+    if (n0 < k.out) {
+        const int64_t o = n0 + lr < k.out ? n0 + lr : k.out - 1;
+        const int8_t* pw = k.w + o * k.ws;
+        const int8_t* px[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const int64_t r = m0 + j * 16 + lr;
+            px[j] = k.x + (r < k.rows ? r : k.rows - 1) * k.xs;
+        }
+        const int steps = (k.width + 63) / 64, each = (steps + split - 1) / split;
+        const int from = share * each, to = from + each < steps ? from + each : steps;
+        for (int s = from; s < to; s += kFewDeep) {
+            Int4 fw[kFewDeep], fx[kFewDeep][B];
+            if (s + kFewDeep <= to && (s + kFewDeep) * 64 <= k.width) {
+#pragma unroll
+                for (int d = 0; d < kFewDeep; ++d) {
+                    const int at = (s + d) * 64 + quarter * 16;
+                    fw[d] = *(const Bytes16*)(pw + at);
+#pragma unroll
+                    for (int j = 0; j < B; ++j) fx[d][j] = *(const Bytes16*)(px[j] + at);
+                }
+            } else {
+#pragma unroll
+                for (int d = 0; d < kFewDeep; ++d) {
+                    const int at = s + d < to ? (s + d) * 64 + quarter * 16 : k.width;
+                    fw[d] = load16(pw, at, k.width);
+#pragma unroll
+                    for (int j = 0; j < B; ++j) fx[d][j] = load16(px[j], at, k.width);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kFewDeep; ++d)
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[d], fx[d][j], acc[j], 0, 0, 0);
+        }
+    }
+    if (split > 1) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) part[wave][j][lane] = acc[j];
+        __syncthreads();
+        if (share) return;
+        for (int d = 1; d < split; ++d)
+#pragma unroll
+            for (int j = 0; j < B; ++j) acc[j] += part[wave + d][j][lane];
+    }
+    const int64_t o = n0 + quarter * 4;
+    if (o >= k.out) return;
+    float ws[4], bias[4], v[4];
+    channel4(k, o, ws, bias);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+        const int64_t r = m0 + j * 16 + lr;
+        if (r >= k.rows) continue;
+        const float xscale = k.xscale[r];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = product_out(acc[j][c], xscale, ws[c], bias[c]);
+        store4<T>(k, r, o, v);
+    }
+}
+
+template <typename T, int B>
+static void few(const Product& k, hipStream_t s)
+{
+    int split = 1;
+    while (split < kFewWaves && cdiv(k.out, 16) * split < 256 * 8 && k.width > split * 64 * kFewDeep) split *= 2;
+    const dim3 grid((unsigned)cdiv(cdiv(k.out, 16), kFewWaves / split), (unsigned)cdiv(k.rows, 16 * B));
+    k_few<T, B><<<grid, 64 * kFewWaves, 0, s>>>(k, split);
+}
+
+template <typename T, int TM, int TN, int WM, int WN>
+static int tiles(const Product& k, hipStream_t s)
+{
+    const int64_t tm = cdiv(k.rows, TM), tn = cdiv(k.out, TN);
+    if (tm * tn >= ((int64_t)1 << 31) / (64 * WM * WN)) return SGC_EUNSUPPORTED;
+    k_tile<T, TM, TN, WM, WN><<<(unsigned)(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
+    SGC_LAUNCH_CHECK();
+    return SGC_OK;
 }
 
 template <typename T>
 static int product(const Product& k, hipStream_t s)
 {
-    const dim3 grid((unsigned)cdiv(k.out, 256), (unsigned)(k.rows < 65535 ? k.rows : 65535));
-    k_product<T><<<grid, 256, 0, s>>>(k);
-    SGC_LAUNCH_CHECK();
-    return SGC_OK;
+    if (k.rows <= 16) {
+        few<T, 1>(k, s);
+        SGC_LAUNCH_CHECK();
+        return SGC_OK;
+    }
+    if (k.rows <= 32) {
+        few<T, 2>(k, s);
+        SGC_LAUNCH_CHECK();
+        return SGC_OK;
+    }
+    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256) return tiles<T, 256, 256, 2, 4>(k, s);
+    return tiles<T, 128, 128, 2, 2>(k, s);
 }
 
 }  // namespace sgc
