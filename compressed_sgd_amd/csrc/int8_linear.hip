@@ -81,15 +81,38 @@ __device__ inline void channel4(const Product& k, int64_t o, float* scale, float
 // read together, and one row's eight pieces, which they write together, both
 // lie in all banks once.
 constexpr int kStep = 128;
+constexpr int kBand = 8, kChips = 8;
+// Workgroups go to the chips in turn; each chip takes consecutive tiles.
+__device__ inline int64_t tile_of_block(int64_t tiles)
+{
+    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (id >= tiles) return -1;
+    const int64_t chip = id % kChips, each = tiles / kChips, more = tiles % kChips;
+    return chip * each + (chip < more ? chip : more) + id / kChips;
+}
 template <typename T, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m, int tiles_n)
 {
     constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 32, PN = TN / WN / 32;
     constexpr int CX = TM * 8 / kThreads, CW = TN * 8 / kThreads, kRows = kThreads / 8;
-    __shared__ Int4 sx[2][TM * 8], sw[2][TN * 8];
+    // the rows of a step, twice; later 32 tokens of each wave's results, a row's
+    // pitch 16 bytes past its length
+    constexpr int kPitch = PN * 32 * (int)sizeof(T) + 16;
+    __shared__ union {
+        struct {
+            Int4 x[2][TM * 8], w[2][TN * 8];
+        };
+        char out[WM * WN][32 * kPitch];
+    } pool;
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
-    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * TM, n0 = (int64_t)(blockIdx.x / tiles_m) * TN;
+    const int64_t at_tile = tile_of_block((int64_t)tiles_m * tiles_n);
+    if (at_tile < 0) return;
+    // kBand tiles of tokens side by side: the workgroups that run together on a chip
+    // share rows of both operands in its L2
+    const int64_t band = at_tile / ((int64_t)kBand * tiles_n), in_band = at_tile - band * kBand * tiles_n;
+    const int high = tiles_m - band * kBand < kBand ? (int)(tiles_m - band * kBand) : kBand;
+    const int64_t m0 = (band * kBand + in_band % high) * TM, n0 = in_band / high * TN;
     // rows past the last one read the last one; what they give is not written
     const int piece = t & 7, row = t >> 3, put = row * 8 + (piece ^ (row & 7));
     const int8_t *px[CX], *pw[CW];
@@ -120,9 +143,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     };
     const auto deposit = [&](int b) {
 #pragma unroll
-        for (int i = 0; i < CX; ++i) sx[b][put + i * kRows * 8] = rx[i];
+        for (int i = 0; i < CX; ++i) pool.x[b][put + i * kRows * 8] = rx[i];
 #pragma unroll
-        for (int i = 0; i < CW; ++i) sw[b][put + i * kRows * 8] = rw[i];
+        for (int i = 0; i < CW; ++i) pool.w[b][put + i * kRows * 8] = rw[i];
     };
     Int16 acc[PN][PM];
 #pragma unroll
@@ -145,9 +168,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
             const int p = (kk * 2 + half) ^ (lr & 7);
             Int4 fx[PM], fw[PN];
 #pragma unroll
-            for (int j = 0; j < PM; ++j) fx[j] = sx[b][ax + j * 256 + p];
+            for (int j = 0; j < PM; ++j) fx[j] = pool.x[b][ax + j * 256 + p];
 #pragma unroll
-            for (int i = 0; i < PN; ++i) fw[i] = sw[b][aw + i * 256 + p];
+            for (int i = 0; i < PN; ++i) fw[i] = pool.w[b][aw + i * 256 + p];
 #pragma unroll
             for (int i = 0; i < PN; ++i)
 #pragma unroll
@@ -157,23 +180,47 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         if (s + 1 < steps) deposit(b ^ 1);
         __syncthreads();
     }
+    // 32 tokens of a wave at a time through its own part of shared memory, so that
+    // rows are written in long pieces
+    constexpr int kPiece = 16 / (int)sizeof(T);
+    char* mine = pool.out[wave];
+    const int64_t on = n0 + wn * PN * 32;
 #pragma unroll
     for (int j = 0; j < PM; ++j) {
-        const int64_t r = m0 + (wm * PM + j) * 32 + lr;
-        if (r >= k.rows) continue;
-        const float xscale = k.xscale[r];
+        const int64_t rm = m0 + (wm * PM + j) * 32, r = rm + lr;
+        const float xscale = k.xscale[r < k.rows ? r : k.rows - 1];
 #pragma unroll
         for (int i = 0; i < PN; ++i)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-                const int64_t o = n0 + (wn * PN + i) * 32 + e * 2 + half * 4;
-                if (o >= k.out) continue;
-                float ws[4], bias[4], v[4];
-                channel4(k, o, ws, bias);
+                const int c0 = i * 32 + e * 2 + half * 4;
+                float ws[4], bias[4];
+                channel4(k, on + c0, ws, bias);
+                Pack<T, 4> p;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = product_out(acc[i][j][e + c], xscale, ws[c], bias[c]);
-                store4<T>(k, r, o, v);
+                for (int c = 0; c < 4; ++c) p.v[c] = from_f<T>(product_out(acc[i][j][e + c], xscale, ws[c], bias[c]));
+                *(Pack<T, 4>*)(mine + lr * kPitch + c0 * (int)sizeof(T)) = p;
             }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kPieces = PN * 32 / kPiece, kAtOnce = 64 / kPieces;
+#pragma unroll
+        for (int a = 0; a < 32; a += kAtOnce) {
+            const int rr = a + lane / kPieces, c0 = lane % kPieces * kPiece;
+            const Raw q = *(const Raw*)(mine + rr * kPitch + c0 * (int)sizeof(T));
+            if (rm + rr >= k.rows) continue;
+            T* y = (T*)k.y + (rm + rr) * k.ys + on + c0;
+            if (on + c0 + kPiece <= k.out) {
+                *(Raw*)y = q;
+            } else {
+                const T* v = (const T*)(mine + rr * kPitch) + c0;
+#pragma unroll
+                for (int c = 0; c < kPiece; ++c)
+                    if (on + c0 + c < k.out) y[c] = v[c];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -268,8 +315,7 @@ template <typename T, int TM, int TN, int WM, int WN>
 static int tiles(const Product& k, hipStream_t s)
 {
     const int64_t tm = cdiv(k.rows, TM), tn = cdiv(k.out, TN);
-    if (tm * tn >= ((int64_t)1 << 31) / (64 * WM * WN)) return SGC_EUNSUPPORTED;
-    k_tile<T, TM, TN, WM, WN><<<(unsigned)(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
+    k_tile<T, TM, TN, WM, WN><<<row_grid(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
@@ -287,7 +333,7 @@ static int product(const Product& k, hipStream_t s)
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
-    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256) return tiles<T, 256, 256, 2, 4>(k, s);
+    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256) return tiles<T, 256, 256, 4, 2>(k, s);
     return tiles<T, 128, 128, 2, 2>(k, s);
 }
 
