@@ -104,6 +104,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         };
         char out[WM * WN][32 * kPitch];
     } pool;
+    __shared__ alignas(16) float channels[2][TN];  // their scales and biases
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
     const int64_t at_tile = tile_of_block((int64_t)tiles_m * tiles_n);
@@ -113,6 +114,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     const int64_t band = at_tile / ((int64_t)kBand * tiles_n), in_band = at_tile - band * kBand * tiles_n;
     const int high = tiles_m - band * kBand < kBand ? (int)(tiles_m - band * kBand) : kBand;
     const int64_t m0 = (band * kBand + in_band % high) * TM, n0 = in_band / high * TN;
+    for (int c = t; c < TN; c += kThreads) {
+        const int64_t o = n0 + c < k.out ? n0 + c : k.out - 1;
+        channels[0][c] = k.wscale[o];
+        channels[1][c] = k.bias ? k.bias[o] : 0.f;
+    }
     // rows past the last one read the last one; what they give is not written
     const int piece = t & 7, row = t >> 3, put = row * 8 + (piece ^ (row & 7));
     const int8_t *px[CX], *pw[CW];
@@ -129,23 +135,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     Int4 rx[CX], rw[CW];
     const auto fetch = [&](int step) {
         const int at = step * kStep + piece * 16;
-        if ((step + 1) * kStep <= k.width) {
 #pragma unroll
-            for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + at);
+        for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + at);
 #pragma unroll
-            for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + at);
-        } else {
-#pragma unroll
-            for (int i = 0; i < CX; ++i) rx[i] = load16(px[i], at, k.width);
-#pragma unroll
-            for (int i = 0; i < CW; ++i) rw[i] = load16(pw[i], at, k.width);
-        }
+        for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + at);
     };
     const auto deposit = [&](int b) {
 #pragma unroll
         for (int i = 0; i < CX; ++i) pool.x[b][put + i * kRows * 8] = rx[i];
 #pragma unroll
         for (int i = 0; i < CW; ++i) pool.w[b][put + i * kRows * 8] = rw[i];
+    };
+    // the last step of a width that is no multiple of 128, byte by byte where it ends
+    const auto deposit_end = [&](int step, int b) {
+        const int at = step * kStep + piece * 16;
+#pragma unroll 1
+        for (int i = 0; i < CX + CW; ++i) {
+            const bool of_x = i < CX;
+            const int place = row + (of_x ? i : i - CX) * kRows;
+            const int64_t r = (of_x ? m0 : n0) + place, last = (of_x ? k.rows : k.out) - 1;
+            const int8_t* p = (of_x ? k.x : k.w) + (r < last ? r : last) * (of_x ? k.xs : k.ws);
+            (of_x ? pool.x[b] : pool.w[b])[place * 8 + (piece ^ (row & 7))] = load16(p, at, k.width);
+        }
     };
     Int16 acc[PN][PM];
 #pragma unroll
@@ -154,32 +165,53 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         for (int j = 0; j < PM; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-    const int steps = (k.width + kStep - 1) / kStep;
+    const int steps = (k.width + kStep - 1) / kStep, whole = k.width / kStep;
     const int lr = lane & 31, half = lane >> 5;
     const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
-    fetch(0);
-    deposit(0);
+    if (whole) {
+        fetch(0);
+        deposit(0);
+    } else {
+        deposit_end(0, 0);
+    }
     __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        const int b = s & 1;
-        if (s + 1 < steps) fetch(s + 1);
+    // the next operands are on their way from shared memory while one step's are multiplied
+    Int4 fx[2][PM], fw[2][PN];
+    const auto read = [&](int b, int kk) {
+        const int p = (kk * 2 + half) ^ (lr & 7);
+#pragma unroll
+        for (int j = 0; j < PM; ++j) fx[kk & 1][j] = pool.x[b][ax + j * 256 + p];
+#pragma unroll
+        for (int i = 0; i < PN; ++i) fw[kk & 1][i] = pool.w[b][aw + i * 256 + p];
+    };
+    const auto multiply = [&](int b) {
+        read(b, 0);
 #pragma unroll
         for (int kk = 0; kk < kStep / 32; ++kk) {
-            const int p = (kk * 2 + half) ^ (lr & 7);
-            Int4 fx[PM], fw[PN];
-#pragma unroll
-            for (int j = 0; j < PM; ++j) fx[j] = pool.x[b][ax + j * 256 + p];
-#pragma unroll
-            for (int i = 0; i < PN; ++i) fw[i] = pool.w[b][aw + i * 256 + p];
+            if (kk + 1 < kStep / 32) read(b, kk + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < PN; ++i)
 #pragma unroll
                 for (int j = 0; j < PM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fx[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][i], fx[kk & 1][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (s + 1 < steps) deposit(b ^ 1);
+    };
+    for (int s = 0; s + 1 < whole; ++s) {
+        fetch(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s & 1);
+        deposit(s & 1 ^ 1);
         __syncthreads();
     }
+    if (whole && whole < steps) {
+        multiply(whole & 1 ^ 1);
+        deposit_end(whole, whole & 1);
+        __syncthreads();
+    }
+    multiply(steps & 1 ^ 1);
+    __syncthreads();
     // 32 tokens of a wave at a time through its own part of shared memory, so that
     // rows are written in long pieces
     constexpr int kPiece = 16 / (int)sizeof(T);
@@ -194,12 +226,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const int c0 = i * 32 + e * 2 + half * 4;
-                float ws[4], bias[4];
-                channel4(k, on + c0, ws, bias);
+                const float4 ws = *(const float4*)&channels[0][wn * PN * 32 + c0];
+                const float4 bias = *(const float4*)&channels[1][wn * PN * 32 + c0];
                 Pack<T, 4> p;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) p.v[c] = from_f<T>(product_out(acc[i][j][e + c], xscale, ws[c], bias[c]));
+                p.v[0] = from_f<T>(product_out(acc[i][j][e], xscale, ws.x, bias.x));
+                p.v[1] = from_f<T>(product_out(acc[i][j][e + 1], xscale, ws.y, bias.y));
+                p.v[2] = from_f<T>(product_out(acc[i][j][e + 2], xscale, ws.z, bias.z));
+                p.v[3] = from_f<T>(product_out(acc[i][j][e + 3], xscale, ws.w, bias.w));
                 *(Pack<T, 4>*)(mine + lr * kPitch + c0 * (int)sizeof(T)) = p;
+                __builtin_amdgcn_sched_barrier(0);
             }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
