@@ -168,13 +168,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     const int steps = (k.width + kStep - 1) / kStep, whole = k.width / kStep;
     const int lr = lane & 31, half = lane >> 5;
     const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
-    if (whole) {
-        fetch(0);
-        deposit(0);
-    } else {
-        deposit_end(0, 0);
-    }
-    __syncthreads();
+    // a step's rows: into registers, into shared memory a step later
+    const auto put_step = [&](int s) {
+        if (s < whole) deposit(s & 1);
+        else if (s < steps) deposit_end(s, s & 1);
+    };
     // the next operands are on their way from shared memory while one step's are multiplied
     Int4 fx[2][PM], fw[2][PN];
     const auto read = [&](int b, int kk) {
@@ -184,33 +182,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
 #pragma unroll
         for (int i = 0; i < PN; ++i) fw[kk & 1][i] = pool.w[b][aw + i * 256 + p];
     };
-    const auto multiply = [&](int b) {
-        read(b, 0);
-#pragma unroll
-        for (int kk = 0; kk < kStep / 32; ++kk) {
-            if (kk + 1 < kStep / 32) read(b, kk + 1);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < PN; ++i)
-#pragma unroll
-                for (int j = 0; j < PM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][i], fx[kk & 1][j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    for (int s = 0; s + 1 < whole; ++s) {
-        fetch(s + 1);
+    const auto multiply = [&](int kk) {
         __builtin_amdgcn_sched_barrier(0);
-        multiply(s & 1);
-        deposit(s & 1 ^ 1);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < PN; ++i)
+#pragma unroll
+            for (int j = 0; j < PM; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][i], fx[kk & 1][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // One barrier a step, before its last products: what is read of this step's rows
+    // has been read, and the next step's lie ready, whose first operands are
+    // read while the last products run.
+    if (whole) fetch(0);
+    put_step(0);
+    if (whole > 1) fetch(1);
+    __syncthreads();
+    read(0, 0);
+    for (int s = 0; s < steps; ++s) {
+        const int b = s & 1;
+        put_step(s + 1);
+        if (s + 2 < whole) fetch(s + 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kk = 0; kk + 1 < kStep / 32; ++kk) {
+            read(b, kk + 1);
+            multiply(kk);
+        }
         __syncthreads();
+        if (s + 1 < steps) read(b ^ 1, 0);
+        multiply(kStep / 32 - 1);
     }
-    if (whole && whole < steps) {
-        multiply(whole & 1 ^ 1);
-        deposit_end(whole, whole & 1);
-        __syncthreads();
-    }
-    multiply(steps & 1 ^ 1);
     __syncthreads();
     // 32 tokens of a wave at a time through its own part of shared memory, so that
     // rows are written in long pieces
