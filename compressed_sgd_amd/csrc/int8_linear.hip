@@ -90,20 +90,24 @@ __device__ inline int64_t tile_of_block(int64_t tiles)
     const int64_t chip = id % kChips, each = tiles / kChips, more = tiles % kChips;
     return chip * each + (chip < more ? chip : more) + id / kChips;
 }
-template <typename T, int TM, int TN, int WM, int WN>
+// 16 bytes for every lane of a wave from memory into shared memory, without
+// registers between: lane l's go to `to` + l.  p at multiples of 16 bytes.
+__device__ inline void into_shared(const int8_t* p, Int4* to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+template <typename T, int TM, int TN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m, int tiles_n)
 {
     constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 32, PN = TN / WN / 32;
     constexpr int CX = TM * 8 / kThreads, CW = TN * 8 / kThreads, kRows = kThreads / 8;
-    // the rows of a step, twice; later 32 tokens of each wave's results, a row's
-    // pitch 16 bytes past its length
-    constexpr int kPitch = PN * 32 * (int)sizeof(T) + 16;
-    __shared__ union {
-        struct {
-            Int4 x[2][TM * 8], w[2][TN * 8];
-        };
-        char out[WM * WN][32 * kPitch];
-    } pool;
+    // Two steps' rows, in arrays of their own: the compiler then knows that rows on
+    // their way into one are not what is read from the other.  Later 32 tokens of
+    // each wave's results, a row's pitch 16 bytes past its length.
+    constexpr int kPitch = PN * 32 * (int)sizeof(T) + 16, kOut = WM * WN / 4 * 2 * kPitch;
+    constexpr int kX = TM * 8 > kOut ? TM * 8 : kOut, kW = TN * 8 > kOut ? TN * 8 : kOut;
+    __shared__ Int4 x0[kX], x1[kX], w0[kW], w1[kW];
     __shared__ alignas(16) float channels[2][TN];  // their scales and biases
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
@@ -119,43 +123,56 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         channels[0][c] = k.wscale[o];
         channels[1][c] = k.bias ? k.bias[o] : 0.f;
     }
-    // rows past the last one read the last one; what they give is not written
-    const int piece = t & 7, row = t >> 3, put = row * 8 + (piece ^ (row & 7));
+    // rows past the last one read the last one; what they give is not written.  Thread
+    // t fills piece t of shared memory's kThreads, which is piece (t ^ row) mod 8 of its row.
+    const int row = t >> 3, piece = (t ^ row) & 7;
     const int8_t *px[CX], *pw[CW];
 #pragma unroll
     for (int i = 0; i < CX; ++i) {
         const int64_t r = m0 + row + i * kRows;
-        px[i] = k.x + (r < k.rows ? r : k.rows - 1) * k.xs;
+        px[i] = k.x + (r < k.rows ? r : k.rows - 1) * k.xs + piece * 16;
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
         const int64_t r = n0 + row + i * kRows;
-        pw[i] = k.w + (r < k.out ? r : k.out - 1) * k.ws;
+        pw[i] = k.w + (r < k.out ? r : k.out - 1) * k.ws + piece * 16;
     }
+    const int steps = (k.width + kStep - 1) / kStep, whole = k.width / kStep;
     Int4 rx[CX], rw[CW];
-    const auto fetch = [&](int step) {
-        const int at = step * kStep + piece * 16;
+    const auto fetch = [&](int s) {
+        if (DIRECT || s >= whole) return;
 #pragma unroll
-        for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + at);
+        for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + s * kStep);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + at);
+        for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + s * kStep);
     };
-    const auto deposit = [&](int b) {
+    // Step s into shared memory; the last one of a width that is no multiple of 128
+    // byte by byte where it ends.
+    const auto put = [&](Int4* x, Int4* w, int s) {
+        if (s < whole) {
 #pragma unroll
-        for (int i = 0; i < CX; ++i) pool.x[b][put + i * kRows * 8] = rx[i];
+            for (int i = 0; i < CX; ++i) {
+                if constexpr (DIRECT)
+                    into_shared(px[i] + s * kStep, x + wave * 64 + i * kThreads);
+                else
+                    x[t + i * kThreads] = rx[i];
+            }
 #pragma unroll
-        for (int i = 0; i < CW; ++i) pool.w[b][put + i * kRows * 8] = rw[i];
-    };
-    // the last step of a width that is no multiple of 128, byte by byte where it ends
-    const auto deposit_end = [&](int step, int b) {
-        const int at = step * kStep + piece * 16;
+            for (int i = 0; i < CW; ++i) {
+                if constexpr (DIRECT)
+                    into_shared(pw[i] + s * kStep, w + wave * 64 + i * kThreads);
+                else
+                    w[t + i * kThreads] = rw[i];
+            }
+        } else if (s < steps) {
 #pragma unroll 1
-        for (int i = 0; i < CX + CW; ++i) {
-            const bool of_x = i < CX;
-            const int place = row + (of_x ? i : i - CX) * kRows;
-            const int64_t r = (of_x ? m0 : n0) + place, last = (of_x ? k.rows : k.out) - 1;
-            const int8_t* p = (of_x ? k.x : k.w) + (r < last ? r : last) * (of_x ? k.xs : k.ws);
-            (of_x ? pool.x[b] : pool.w[b])[place * 8 + (piece ^ (row & 7))] = load16(p, at, k.width);
+            for (int i = 0; i < CX + CW; ++i) {
+                const bool of_x = i < CX;
+                const int place = of_x ? i : i - CX;
+                const int64_t r = (of_x ? m0 : n0) + row + place * kRows, last = (of_x ? k.rows : k.out) - 1;
+                const int8_t* p = (of_x ? k.x : k.w) + (r < last ? r : last) * (of_x ? k.xs : k.ws);
+                (of_x ? x : w)[t + place * kThreads] = load16(p, s * kStep + piece * 16, k.width);
+            }
         }
     };
     Int16 acc[PN][PM];
@@ -165,22 +182,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         for (int j = 0; j < PM; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-    const int steps = (k.width + kStep - 1) / kStep, whole = k.width / kStep;
     const int lr = lane & 31, half = lane >> 5;
     const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
-    // a step's rows: into registers, into shared memory a step later
-    const auto put_step = [&](int s) {
-        if (s < whole) deposit(s & 1);
-        else if (s < steps) deposit_end(s, s & 1);
-    };
-    // the next operands are on their way from shared memory while one step's are multiplied
     Int4 fx[2][PM], fw[2][PN];
-    const auto read = [&](int b, int kk) {
+    const auto read = [&](const Int4* x, const Int4* w, int kk) {
         const int p = (kk * 2 + half) ^ (lr & 7);
 #pragma unroll
-        for (int j = 0; j < PM; ++j) fx[kk & 1][j] = pool.x[b][ax + j * 256 + p];
+        for (int j = 0; j < PM; ++j) fx[kk & 1][j] = x[ax + j * 256 + p];
 #pragma unroll
-        for (int i = 0; i < PN; ++i) fw[kk & 1][i] = pool.w[b][aw + i * 256 + p];
+        for (int i = 0; i < PN; ++i) fw[kk & 1][i] = w[aw + i * 256 + p];
     };
     const auto multiply = [&](int kk) {
         __builtin_amdgcn_sched_barrier(0);
@@ -193,33 +203,43 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One barrier a step, before its last products: what is read of this step's rows
-    // has been read, and the next step's lie ready, whose first operands are
-    // read while the last products run.
-    if (whole) fetch(0);
-    put_step(0);
-    if (whole > 1) fetch(1);
-    __syncthreads();
-    read(0, 0);
-    for (int s = 0; s < steps; ++s) {
-        const int b = s & 1;
-        put_step(s + 1);
-        if (s + 2 < whole) fetch(s + 2);
-        __builtin_amdgcn_sched_barrier(0);
+    // what this wave has on its way into shared memory (a barrier alone does not wait for it)
+    const auto arrived = [] {
+        if (DIRECT) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    };
+    // The operands of the next products are read while one step's run.  One barrier a
+    // step, before its last products: what is read of this step's rows has been
+    // read, and the step after next takes their place; the next step's lie ready.
+    const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w) {
 #pragma unroll
         for (int kk = 0; kk + 1 < kStep / 32; ++kk) {
-            read(b, kk + 1);
+            read(x, w, kk + 1);
             multiply(kk);
         }
+        arrived();
         __syncthreads();
-        if (s + 1 < steps) read(b ^ 1, 0);
+        put(x, w, s + 2);
+        fetch(s + 3);
+        if (s + 1 < steps) read(next_x, next_w, 0);
         multiply(kStep / 32 - 1);
+    };
+    fetch(0);
+    put(x0, w0, 0);
+    fetch(1);
+    put(x1, w1, 1);
+    fetch(2);
+    arrived();
+    __syncthreads();
+    read(x0, w0, 0);
+    for (int s = 0; s < steps; s += 2) {
+        step(s, x0, w0, x1, w1);
+        if (s + 1 < steps) step(s + 1, x1, w1, x0, w0);
     }
     __syncthreads();
     // 32 tokens of a wave at a time through its own part of shared memory, so that
     // rows are written in long pieces
     constexpr int kPiece = 16 / (int)sizeof(T);
-    char* mine = pool.out[wave];
+    char* mine = (char*)((wave & 2) ? (wave & 1) ? w1 : w0 : (wave & 1) ? x1 : x0) + (wave >> 2) * 32 * kPitch;
     const int64_t on = n0 + wn * PN * 32;
 #pragma unroll
     for (int j = 0; j < PM; ++j) {
@@ -350,11 +370,11 @@ static void few(const Product& k, hipStream_t s)
     k_few<T, B><<<grid, 64 * kFewWaves, 0, s>>>(k, split);
 }
 
-template <typename T, int TM, int TN, int WM, int WN>
+template <typename T, int TM, int TN, int WM, int WN, bool DIRECT>
 static int tiles(const Product& k, hipStream_t s)
 {
     const int64_t tm = cdiv(k.rows, TM), tn = cdiv(k.out, TN);
-    k_tile<T, TM, TN, WM, WN><<<row_grid(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
+    k_tile<T, TM, TN, WM, WN, DIRECT><<<row_grid(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
@@ -372,8 +392,10 @@ static int product(const Product& k, hipStream_t s)
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
-    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256) return tiles<T, 256, 256, 4, 2>(k, s);
-    return tiles<T, 128, 128, 2, 2>(k, s);
+    const bool direct = aligned16(k.x) && aligned16(k.w) && k.xs % 16 == 0 && k.ws % 16 == 0;
+    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256)
+        return direct ? tiles<T, 256, 256, 4, 2, true>(k, s) : tiles<T, 256, 256, 4, 2, false>(k, s);
+    return direct ? tiles<T, 128, 128, 2, 2, true>(k, s) : tiles<T, 128, 128, 2, 2, false>(k, s);
 }
 
 }  // namespace sgc
