@@ -17,7 +17,18 @@ struct AsIs {
     const T* p;
     int64_t stride;
     __device__ float at(int64_t r, int c) const { return to_f(p[r * stride + c]); }
+    // a vector of a row on its way, and its values
+    struct Held {
+        Raw v;
+    };
+    template <bool RAG>
+    __device__ Held load(int64_t r, int v, int cols, bool once) const
+    {
+        return {load_vec<T, RAG>(p + r * stride, v, cols, once)};
+    }
+    __device__ static void values(const Held& h, float* x) { unpack<T>(h.v, x); }
 };
+template <typename T>
 struct As8Bits {
     const int8_t* q;
     int64_t stride;
@@ -27,6 +38,22 @@ struct As8Bits {
     __device__ float at(int64_t r, int c) const
     {
         return (float)q[r * stride + c] * scale[r * groups + (c >> shift)];
+    }
+    // groups are of 32 or more: a vector has one scale
+    static constexpr int VL = VecLen<T>::value;
+    struct Held {
+        Bytes<VL> b;
+        float scale;
+    };
+    template <bool RAG>
+    __device__ Held load(int64_t r, int v, int cols, bool once) const
+    {
+        return {load_bytes<VL, RAG>(q + r * stride, v, cols), v * VL < cols ? scale[r * groups + (v * VL >> shift)] : 0.f};
+    }
+    __device__ static void values(const Held& h, float* x)
+    {
+#pragma unroll
+        for (int e = 0; e < VL; ++e) x[e] = byte_of(h.b.w[e / 4], e % 4) * h.scale;
     }
 };
 
@@ -52,6 +79,151 @@ template <typename T>
 __device__ inline float weight_at(const void* w, bool w32, int c, float none)
 {
     return !w ? none : w32 ? ((const float*)w)[c] : to_f(((const T*)w)[c]);
+}
+
+// ------------------------------------------------------- rows in registers
+// As the layer norm's backward kernel: a workgroup takes row after row, its
+// columns' weights and their gradients' sums in registers; part [workgroups,
+// sums, cols].
+template <typename T, typename X, bool LAYER, int NTR, int EPT, int RPB, bool RAG>
+__global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back k, bool once)
+{
+    constexpr int VL = VecLen<T>::value, NV = EPT / VL;
+    __shared__ RowTmp<NTR, RPB> tmp;
+    const int sub = row_place<NTR>(), t = threadIdx.x % NTR, cols = k.cols;
+    float wf[EPT], aw[EPT], ab[EPT];
+    load_weights<T, NV, NTR>(k.w, k.w32, t, cols, 1.f, wf);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
+    typename X::Held nx[NV] = {};
+    Raw ny[NV] = {}, ns[NV] = {};
+    float nm = 0.f, nr = 0.f;
+    int64_t r = (int64_t)blockIdx.x * RPB + sub;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    const auto fetch = [&](int64_t at) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            nx[n] = x.template load<RAG>(at, n * NTR + t, cols, once);
+            ny[n] = load_vec<T, RAG>((const T*)k.dy + at * k.dys, n * NTR + t, cols, once);
+        }
+        if (k.dsum) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+                ns[n] = load_vec<T, RAG>((const T*)k.dsum + at * k.dss, n * NTR + t, cols, once);
+        }
+        if (LAYER) nm = k.mean[at];
+        nr = k.rstd[at];
+    };
+    constexpr bool kAhead = EPT < 16;
+    if (kAhead && r < k.rows) fetch(r);
+    int turn = 0;
+    for (; r - sub < k.rows; r += step, turn ^= 1) {
+        const bool live = r < k.rows;
+        if (!kAhead && live) fetch(r);
+        float h[EPT], g[EPT];
+        Raw ds[NV];
+        const float m = live && LAYER ? nm : 0.f, rs = live ? nr : 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            X::values(nx[n], h + n * VL);
+            unpack<T>(ny[n], g + n * VL);
+            ds[n] = ns[n];
+        }
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) h[i] = g[i] = 0.f;
+        }
+        if (kAhead && r + step < k.rows) fetch(r + step);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {  // past cols dy is 0
+            h[i] = (LAYER ? h[i] - m : h[i]) * rs;
+            aw[i] = fmaf(g[i], h[i], aw[i]);
+            if (LAYER) ab[i] += g[i];
+            g[i] *= wf[i];
+            if (LAYER) s1 += g[i];
+            s2 = fmaf(g[i], h[i], s2);
+        }
+        if (k.y && live) {
+            float y[EPT];
+            if (LAYER) load_weights<T, NV, NTR>(k.b, k.w32, t, cols, 0.f, y);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) y[i] = LAYER ? fmaf(h[i], wf[i], y[i]) : h[i] * wf[i];
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+                store_vec<T, RAG>((T*)k.y + r * k.ys, n * NTR + t, cols, y + n * VL, once);
+        }
+        if (k.dx) {
+            row_sums<NTR, RPB>(s1, s2, tmp, turn);
+            const float c1 = LAYER ? s1 / (float)cols : 0.f, c2 = s2 / (float)cols;
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) g[i] = rs * (g[i] - fmaf(h[i], c2, c1));
+                if (k.dsum) {
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        float d[VL];
+                        unpack<T>(ds[n], d);
+#pragma unroll
+                        for (int e = 0; e < VL; ++e) g[n * VL + e] += d[e];
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+                    store_vec<T, RAG>((T*)k.dx + r * k.dxs, n * NTR + t, cols, g + n * VL, once);
+            }
+        }
+    }
+    if (!k.part) return;
+    // the rows side by side in a wave, then those (or the waves) side by side in
+    // the workgroup, one after the other
+    constexpr bool kFold = NTR < 64;
+    constexpr int kSide = kFold ? NTR * RPB / 64 : RPB, kSums = LAYER ? 2 : 1;
+    if (kFold) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+#pragma unroll
+            for (int d = NTR; d < 64; d <<= 1) {
+                aw[i] += __shfl_xor(aw[i], d, 64);
+                if (LAYER) ab[i] += __shfl_xor(ab[i], d, 64);
+            }
+        }
+    }
+    const int at = kFold ? threadIdx.x >> 6 : sub;
+    const bool mine = !kFold || (threadIdx.x & 63) < NTR;
+    __shared__ float sw[kSums][kSide > 1 ? NTR * EPT : 1];
+    if (kSide > 1) {
+        for (int o = kSide - 1; o > 0; --o) {
+            __syncthreads();
+            if (at == o && mine) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) {
+                    if (o < kSide - 1) {
+                        aw[i] += sw[0][i * NTR + t];
+                        if (LAYER) ab[i] += sw[kSums - 1][i * NTR + t];
+                    }
+                    sw[0][i * NTR + t] = aw[i];
+                    if (LAYER) sw[kSums - 1][i * NTR + t] = ab[i];
+                }
+            }
+        }
+        __syncthreads();
+        if (at || !mine) return;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            aw[i] += sw[0][i * NTR + t];
+            if (LAYER) ab[i] += sw[kSums - 1][i * NTR + t];
+        }
+    }
+    float* p = k.part + kSums * (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int e = 0; e < VL; e += 4) {
+            const int v = (n * NTR + t) * (VL / 4) + e / 4;
+            store_raw<float, RAG, false>(p, v, cols, aw + n * VL + e);
+            if (LAYER) store_raw<float, RAG, false>(p + cols, v, cols, ab + n * VL + e);
+        }
 }
 
 // ------------------------------------------------- rows that are not held
@@ -105,14 +277,24 @@ __global__ __launch_bounds__(256) void k_back_long_dw(X x, Back k)
 
 inline int64_t back_parts(int64_t rows, int64_t cols, int32_t dtype)
 {
-    return rows < 64 ? rows : 64;
+    if (cols > kNormHeld) return rows < 64 ? rows : 64;
+    const NormShape sh = norm_shape(cols, dtype, true);
+    const int64_t most = kCus * kBackwardWaves * 64 / (sh.ntr * sh.rpb), need = cdiv(rows, sh.rpb);
+    return need < most ? need : most;
+}
+
+template <typename T, typename X, bool LAYER, int NTR, int EPT, int RPB>
+static void back_held(const X& x, const Back& k, unsigned g, bool once, hipStream_t s)
+{
+    if (k.cols % VecLen<T>::value) k_back<T, X, LAYER, NTR, EPT, RPB, true><<<g, NTR * RPB, 0, s>>>(x, k, once);
+    else k_back<T, X, LAYER, NTR, EPT, RPB, false><<<g, NTR * RPB, 0, s>>>(x, k, once);
 }
 
 template <typename T, typename X, bool LAYER>
 static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float* db, bool add, hipStream_t s)
 {
     const int64_t parts = back_parts(k.rows, k.cols, dtype);
-    if (k.rows) {
+    if (k.rows && k.cols > kNormHeld) {
         if (k.part) {  // before dx, which may take dy's or the input's place
             k_back_long_dw<T, X, LAYER><<<dim3((unsigned)cdiv(k.cols, 256), (unsigned)parts), 256, 0, s>>>(x, k);
             SGC_LAUNCH_CHECK();
@@ -121,6 +303,28 @@ static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float*
             k_back_long<T, X, LAYER><<<row_grid(k.rows), kLongThreads, 0, s>>>(x, k);
             SGC_LAUNCH_CHECK();
         }
+    } else if (k.rows && (k.part || k.dx || k.y)) {
+        const unsigned g = (unsigned)parts;
+        const int64_t moved = 2 + (k.dsum != nullptr) + (k.dx != nullptr) + (k.y != nullptr);
+        const bool once = k.rows * k.cols * moved * (int64_t)sizeof(T) >= kCacheBytes;
+        const NormShape sh = norm_shape(k.cols, dtype, true);
+        const int shape = sh.ntr * 100 + sh.ept;
+        if constexpr (sizeof(T) == 4) {
+            if (shape == 6412) back_held<T, X, LAYER, 64, 12, 8>(x, k, g, once, s);
+        } else {
+            if (shape == 51216) back_held<T, X, LAYER, 512, 16, 1>(x, k, g, once, s);
+            else if (shape == 25616) back_held<T, X, LAYER, 256, 16, 2>(x, k, g, once, s);
+            else if (shape == 12816) back_held<T, X, LAYER, 128, 16, 4>(x, k, g, once, s);
+            else if (shape == 6416) back_held<T, X, LAYER, 64, 16, 8>(x, k, g, once, s);
+        }
+        if (shape == 102416) back_held<T, X, LAYER, 1024, 16, 1>(x, k, g, once, s);
+        else if (shape == 102408) back_held<T, X, LAYER, 1024, 8, 1>(x, k, g, once, s);
+        else if (shape == 51208) back_held<T, X, LAYER, 512, 8, 1>(x, k, g, once, s);
+        else if (shape == 25608) back_held<T, X, LAYER, 256, 8, 2>(x, k, g, once, s);
+        else if (shape == 12808) back_held<T, X, LAYER, 128, 8, 4>(x, k, g, once, s);
+        else if (shape == 6408) back_held<T, X, LAYER, 64, 8, 8>(x, k, g, once, s);
+        else if (shape == 1608) back_held<T, X, LAYER, 16, 8, 32>(x, k, g, once, s);
+        SGC_LAUNCH_CHECK();
     }
     if (k.part) {
         const int64_t width = (LAYER ? 2 : 1) * (int64_t)k.cols;

@@ -13,11 +13,13 @@ static bool norm_q8_ok(const sgc_norm_q8_opts* o)
 }
 
 template <typename T>
-static int norm_back_8(const sgc_norm_q8_opts* o, const As8Bits& x, const Back& k, float* dw, float* db, hipStream_t s)
+static int norm_back_8(const sgc_norm_q8_opts* o, const int8_t* q, int64_t qs, const float* scale, const Back& k,
+                       float* dw, float* db, hipStream_t s)
 {
+    const As8Bits<T> x = {q, qs, scale, q8_groups(o->cols, o->group), q8_shift(o->group)};
     const bool add = o->flags & SGC_NORM_ADD_GRADS;
-    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits, true>(x, k, o->dtype, dw, db, add, s)
-                                     : norm_back<T, As8Bits, false>(x, k, o->dtype, dw, db, add, s);
+    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits<T>, true>(x, k, o->dtype, dw, db, add, s)
+                                     : norm_back<T, As8Bits<T>, false>(x, k, o->dtype, dw, db, add, s);
 }
 
 }  // namespace sgc
@@ -61,11 +63,10 @@ extern "C" int sgc_norm_backward_q8(const sgc_norm_q8_opts* o, const void* dy, i
         if (!aligned16(ws)) return SGC_EINVAL;
         part = Carver(ws).take<float>(1);
     }
-    const As8Bits x = {q, q_stride, scale, q8_groups(o->cols, o->group), q8_shift(o->group)};
     const Back k = {dy, dy_stride, weight, bias,     o->wdtype == SGC_F32, mean,    rstd, dsum, dsum_stride,
                     dx, dx_stride, y,      y_stride, part,                 o->rows, (int)o->cols};
     const hipStream_t s = (hipStream_t)stream;
-    return o->dtype == SGC_F32    ? norm_back_8<float>(o, x, k, dweight, dbias, s)
-           : o->dtype == SGC_BF16 ? norm_back_8<bf16_t>(o, x, k, dweight, dbias, s)
-                                  : norm_back_8<f16_t>(o, x, k, dweight, dbias, s);
+    return o->dtype == SGC_F32    ? norm_back_8<float>(o, q, q_stride, scale, k, dweight, dbias, s)
+           : o->dtype == SGC_BF16 ? norm_back_8<bf16_t>(o, q, q_stride, scale, k, dweight, dbias, s)
+                                  : norm_back_8<f16_t>(o, q, q_stride, scale, k, dweight, dbias, s);
 }
