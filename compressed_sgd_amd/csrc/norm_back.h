@@ -26,7 +26,12 @@ struct AsIs {
     {
         return {load_vec<T, RAG>(p + r * stride, v, cols, once)};
     }
-    __device__ static void values(const Held& h, float* x) { unpack<T>(h.v, x); }
+    template <bool RAG>
+    __device__ static void values(Held& h, int v, int cols, float* x)
+    {
+        settle<T, RAG>(h.v, v, cols);
+        unpack<T>(h.v, x);
+    }
 };
 template <typename T>
 struct As8Bits {
@@ -50,8 +55,10 @@ struct As8Bits {
     {
         return {load_bytes<VL, RAG>(q + r * stride, v, cols), v * VL < cols ? scale[r * groups + (v * VL >> shift)] : 0.f};
     }
-    __device__ static void values(const Held& h, float* x)
+    template <bool RAG>
+    __device__ static void values(Held& h, int v, int cols, float* x)
     {
+        settle<VL, RAG>(h.b, v, cols);
 #pragma unroll
         for (int e = 0; e < VL; ++e) x[e] = byte_of(h.b.w[e / 4], e % 4) * h.scale;
     }
@@ -85,31 +92,56 @@ __device__ inline float weight_at(const void* w, bool w32, int c, float none)
 // As the layer norm's backward kernel: a workgroup takes row after row, its
 // columns' weights and their gradients' sums in registers; part [workgroups,
 // sums, cols].
-template <typename T, typename X, bool LAYER, int NTR, int EPT, int RPB, bool RAG>
-__global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back k, bool once)
+// MOST: threads of a workgroup at most.  Up to 512 a layer norm's kernel has 12
+// waves a compute unit, not 16, and room for the bias.  Longer rows' kernels
+// have 128 registers, which the bias and, at 16 elements a thread, the weights
+// no longer fit: those lie in shared memory, each thread's own, and are read
+// again in every row (volatile: else they move back into registers).
+typedef float Four __attribute__((ext_vector_type(4)));
+template <typename T, typename X, bool LAYER, int LANES, int EPT, bool RAG, int MOST>
+__global__ __launch_bounds__(MOST, LAYER && MOST == 512 ? 3 : 4) void k_back(X x, Back k, int waves, int side,
+                                                                             bool once)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL;
-    __shared__ RowTmp<NTR, RPB> tmp;
-    const int sub = row_place<NTR>(), t = threadIdx.x % NTR, cols = k.cols;
-    float wf[EPT], aw[EPT], ab[EPT];
-    load_weights<T, NV, NTR>(k.w, k.w32, t, cols, 1.f, wf);
+    __shared__ RowJoin tmp;
+    if (LANES == 64 && waves > 1) clear_join(tmp);
+    const RowPlace<LANES> place(waves);
+    const int sub = place.sub, t = place.t, across = place.across, cols = k.cols;
+    constexpr bool kW = EPT == 16, kB = LAYER && MOST == 1024;
+    __shared__ Four ws[kW ? EPT / 4 : 1][kW ? MOST : 1], bs[kB ? EPT / 4 : 1][kB ? MOST : 1];
+    float wh[EPT], bh[EPT], aw[EPT], ab[EPT];
+    row_weights<T, NV>(k.w, k.w32, across, t, cols, 1.f, wh);
+    if (LAYER) row_weights<T, NV>(k.b, k.w32, across, t, cols, 0.f, bh);
+#pragma unroll
+    for (int i = 0; i < EPT; i += 4) {
+        if constexpr (kW) ws[i / 4][threadIdx.x] = Four{wh[i], wh[i + 1], wh[i + 2], wh[i + 3]};
+        if constexpr (kB) bs[i / 4][threadIdx.x] = Four{bh[i], bh[i + 1], bh[i + 2], bh[i + 3]};
+    }
+    const auto weights = [&](int i) {
+        if constexpr (kW) return *(volatile Four*)&ws[i / 4][threadIdx.x];
+        else return Four{wh[i], wh[i + 1], wh[i + 2], wh[i + 3]};
+    };
+    const auto biases = [&](int i) {
+        if constexpr (kB) return *(volatile Four*)&bs[i / 4][threadIdx.x];
+        else return Four{bh[i], bh[i + 1], bh[i + 2], bh[i + 3]};
+    };
 #pragma unroll
     for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
     typename X::Held nx[NV] = {};
     Raw ny[NV] = {}, ns[NV] = {};
     float nm = 0.f, nr = 0.f;
-    int64_t r = (int64_t)blockIdx.x * RPB + sub;
-    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * side + sub;
+    const int64_t step = (int64_t)gridDim.x * side;
     const auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            nx[n] = x.template load<RAG>(at, n * NTR + t, cols, once);
-            ny[n] = load_vec<T, RAG>((const T*)k.dy + at * k.dys, n * NTR + t, cols, once);
+            nx[n] = x.template load<RAG>(at, n * across + t, cols, once);
+            ny[n] = load_vec<T, RAG>((const T*)k.dy + at * k.dys, n * across + t, cols, once);
         }
         if (k.dsum) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                ns[n] = load_vec<T, RAG>((const T*)k.dsum + at * k.dss, n * NTR + t, cols, once);
+                ns[n] = load_vec<T, RAG>((const T*)k.dsum + at * k.dss, n * across + t, cols, once);
         }
         if (LAYER) nm = k.mean[at];
         nr = k.rstd[at];
@@ -125,7 +157,8 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
         const float m = live && LAYER ? nm : 0.f, rs = live ? nr : 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            X::values(nx[n], h + n * VL);
+            X::template values<RAG>(nx[n], n * across + t, cols, h + n * VL);
+            settle<T, RAG>(ny[n], n * across + t, cols);
             unpack<T>(ny[n], g + n * VL);
             ds[n] = ns[n];
         }
@@ -135,26 +168,30 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
         }
         if (kAhead && r + step < k.rows) fetch(r + step);
         float s1 = 0.f, s2 = 0.f;
+        float y[EPT];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {  // past cols dy is 0
-            h[i] = (LAYER ? h[i] - m : h[i]) * rs;
-            aw[i] = fmaf(g[i], h[i], aw[i]);
-            if (LAYER) ab[i] += g[i];
-            g[i] *= wf[i];
-            if (LAYER) s1 += g[i];
-            s2 = fmaf(g[i], h[i], s2);
+        for (int i = 0; i < EPT; i += 4) {  // past cols dy is 0
+            const Four w = weights(i);
+            Four b = {0.f, 0.f, 0.f, 0.f};
+            if (LAYER && k.y) b = biases(i);
+#pragma unroll
+            for (int e = i; e < i + 4; ++e) {
+                h[e] = (LAYER ? h[e] - m : h[e]) * rs;
+                y[e] = LAYER ? fmaf(h[e], w[e - i], b[e - i]) : h[e] * w[e - i];
+                aw[e] = fmaf(g[e], h[e], aw[e]);
+                if (LAYER) ab[e] += g[e];
+                g[e] *= w[e - i];
+                if (LAYER) s1 += g[e];
+                s2 = fmaf(g[e], h[e], s2);
+            }
         }
         if (k.y && live) {
-            float y[EPT];
-            if (LAYER) load_weights<T, NV, NTR>(k.b, k.w32, t, cols, 0.f, y);
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) y[i] = LAYER ? fmaf(h[i], wf[i], y[i]) : h[i] * wf[i];
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                store_vec<T, RAG>((T*)k.y + r * k.ys, n * NTR + t, cols, y + n * VL, once);
+                store_vec<T, RAG>((T*)k.y + r * k.ys, n * across + t, cols, y + n * VL, once);
         }
         if (k.dx) {
-            row_sums<NTR, RPB>(s1, s2, tmp, turn);
+            row_join<false, LANES>(s1, s2, tmp, turn, waves, sub);
             const float c1 = LAYER ? s1 / (float)cols : 0.f, c2 = s2 / (float)cols;
             if (live) {
 #pragma unroll
@@ -163,6 +200,7 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
 #pragma unroll
                     for (int n = 0; n < NV; ++n) {
                         float d[VL];
+                        settle<T, RAG>(ds[n], n * across + t, cols);
                         unpack<T>(ds[n], d);
 #pragma unroll
                         for (int e = 0; e < VL; ++e) g[n * VL + e] += d[e];
@@ -170,40 +208,41 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
                 }
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
-                    store_vec<T, RAG>((T*)k.dx + r * k.dxs, n * NTR + t, cols, g + n * VL, once);
+                    store_vec<T, RAG>((T*)k.dx + r * k.dxs, n * across + t, cols, g + n * VL, once);
             }
         }
     }
     if (!k.part) return;
     // the rows side by side in a wave, then those (or the waves) side by side in
     // the workgroup, one after the other
-    constexpr bool kFold = NTR < 64;
-    constexpr int kSide = kFold ? NTR * RPB / 64 : RPB, kSums = LAYER ? 2 : 1;
+    constexpr bool kFold = LANES < 64;
+    constexpr int kSums = LAYER ? 2 : 1;
     if (kFold) {
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
 #pragma unroll
-            for (int d = NTR; d < 64; d <<= 1) {
+            for (int d = LANES; d < 64; d <<= 1) {
                 aw[i] += __shfl_xor(aw[i], d, 64);
                 if (LAYER) ab[i] += __shfl_xor(ab[i], d, 64);
             }
         }
     }
-    const int at = kFold ? threadIdx.x >> 6 : sub;
-    const bool mine = !kFold || (threadIdx.x & 63) < NTR;
-    __shared__ float sw[kSums][kSide > 1 ? NTR * EPT : 1];
-    if (kSide > 1) {
-        for (int o = kSide - 1; o > 0; --o) {
+    const int at = kFold ? threadIdx.x >> 6 : sub, beside = kFold ? 8 : side;
+    const bool mine = !kFold || (threadIdx.x & 63) < LANES;
+    // rows side by side have 4 waves at most
+    __shared__ float sw[kSums][EPT * (kFold ? LANES : EPT == 8 ? 256 : 1)];
+    if (beside > 1) {
+        for (int o = beside - 1; o > 0; --o) {
             __syncthreads();
             if (at == o && mine) {
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) {
-                    if (o < kSide - 1) {
-                        aw[i] += sw[0][i * NTR + t];
-                        if (LAYER) ab[i] += sw[kSums - 1][i * NTR + t];
+                    if (o < beside - 1) {
+                        aw[i] += sw[0][i * across + t];
+                        if (LAYER) ab[i] += sw[kSums - 1][i * across + t];
                     }
-                    sw[0][i * NTR + t] = aw[i];
-                    if (LAYER) sw[kSums - 1][i * NTR + t] = ab[i];
+                    sw[0][i * across + t] = aw[i];
+                    if (LAYER) sw[kSums - 1][i * across + t] = ab[i];
                 }
             }
         }
@@ -211,8 +250,8 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
         if (at || !mine) return;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-            aw[i] += sw[0][i * NTR + t];
-            if (LAYER) ab[i] += sw[kSums - 1][i * NTR + t];
+            aw[i] += sw[0][i * across + t];
+            if (LAYER) ab[i] += sw[kSums - 1][i * across + t];
         }
     }
     float* p = k.part + kSums * (int64_t)blockIdx.x * cols;
@@ -220,7 +259,7 @@ __global__ __launch_bounds__(NTR* RPB, kBackwardWaves / 4) void k_back(X x, Back
     for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int e = 0; e < VL; e += 4) {
-            const int v = (n * NTR + t) * (VL / 4) + e / 4;
+            const int v = (n * across + t) * (VL / 4) + e / 4;
             store_raw<float, RAG, false>(p, v, cols, aw + n * VL + e);
             if (LAYER) store_raw<float, RAG, false>(p + cols, v, cols, ab + n * VL + e);
         }
@@ -275,25 +314,34 @@ __global__ __launch_bounds__(256) void k_back_long_dw(X x, Back k)
     if (LAYER) p[k.cols] = ab;
 }
 
-inline int64_t back_parts(int64_t rows, int64_t cols, int32_t dtype)
+inline int64_t back_parts(int64_t rows, int64_t cols, bool layer)
 {
     if (cols > kNormHeld) return rows < 64 ? rows : 64;
-    const NormShape sh = norm_shape(cols, dtype, true);
-    const int64_t most = kCus * kBackwardWaves * 64 / (sh.ntr * sh.rpb), need = cdiv(rows, sh.rpb);
-    return need < most ? need : most;
+    const RowShape sh = row_shape(cols);
+    return row_groups(sh, rows, layer && sh.threads() <= 512 ? 12 : kBackwardWaves);
 }
 
-template <typename T, typename X, bool LAYER, int NTR, int EPT, int RPB>
-static void back_held(const X& x, const Back& k, unsigned g, bool once, hipStream_t s)
+template <typename T, typename X, bool LAYER, int LANES, int EPT>
+static void back_held(const X& x, const Back& k, const RowShape& sh, unsigned g, bool once, hipStream_t s)
 {
-    if (k.cols % VecLen<T>::value) k_back<T, X, LAYER, NTR, EPT, RPB, true><<<g, NTR * RPB, 0, s>>>(x, k, once);
-    else k_back<T, X, LAYER, NTR, EPT, RPB, false><<<g, NTR * RPB, 0, s>>>(x, k, once);
+    const bool rag = k.cols % VecLen<T>::value;
+    if constexpr (EPT == 8) {
+        if (sh.threads() <= 512) {
+            if (rag) k_back<T, X, LAYER, LANES, EPT, true, 512><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
+            else k_back<T, X, LAYER, LANES, EPT, false, 512><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
+            return;
+        }
+    }
+    if constexpr (LANES == 64) {
+        if (rag) k_back<T, X, LAYER, LANES, EPT, true, 1024><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
+        else k_back<T, X, LAYER, LANES, EPT, false, 1024><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
+    }
 }
 
 template <typename T, typename X, bool LAYER>
-static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float* db, bool add, hipStream_t s)
+static int norm_back(const X& x, const Back& k, float* dw, float* db, bool add, hipStream_t s)
 {
-    const int64_t parts = back_parts(k.rows, k.cols, dtype);
+    const int64_t parts = back_parts(k.rows, k.cols, LAYER);
     if (k.rows && k.cols > kNormHeld) {
         if (k.part) {  // before dx, which may take dy's or the input's place
             k_back_long_dw<T, X, LAYER><<<dim3((unsigned)cdiv(k.cols, 256), (unsigned)parts), 256, 0, s>>>(x, k);
@@ -307,23 +355,11 @@ static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float*
         const unsigned g = (unsigned)parts;
         const int64_t moved = 2 + (k.dsum != nullptr) + (k.dx != nullptr) + (k.y != nullptr);
         const bool once = k.rows * k.cols * moved * (int64_t)sizeof(T) >= kCacheBytes;
-        const NormShape sh = norm_shape(k.cols, dtype, true);
-        const int shape = sh.ntr * 100 + sh.ept;
-        if constexpr (sizeof(T) == 4) {
-            if (shape == 6412) back_held<T, X, LAYER, 64, 12, 8>(x, k, g, once, s);
-        } else {
-            if (shape == 51216) back_held<T, X, LAYER, 512, 16, 1>(x, k, g, once, s);
-            else if (shape == 25616) back_held<T, X, LAYER, 256, 16, 2>(x, k, g, once, s);
-            else if (shape == 12816) back_held<T, X, LAYER, 128, 16, 4>(x, k, g, once, s);
-            else if (shape == 6416) back_held<T, X, LAYER, 64, 16, 8>(x, k, g, once, s);
-        }
-        if (shape == 102416) back_held<T, X, LAYER, 1024, 16, 1>(x, k, g, once, s);
-        else if (shape == 102408) back_held<T, X, LAYER, 1024, 8, 1>(x, k, g, once, s);
-        else if (shape == 51208) back_held<T, X, LAYER, 512, 8, 1>(x, k, g, once, s);
-        else if (shape == 25608) back_held<T, X, LAYER, 256, 8, 2>(x, k, g, once, s);
-        else if (shape == 12808) back_held<T, X, LAYER, 128, 8, 4>(x, k, g, once, s);
-        else if (shape == 6408) back_held<T, X, LAYER, 64, 8, 8>(x, k, g, once, s);
-        else if (shape == 1608) back_held<T, X, LAYER, 16, 8, 32>(x, k, g, once, s);
+        const RowShape sh = row_shape(k.cols);
+        if (sh.lanes == 16) back_held<T, X, LAYER, 16, 8>(x, k, sh, g, once, s);
+        else if (sh.lanes == 32) back_held<T, X, LAYER, 32, 8>(x, k, sh, g, once, s);
+        else if (sh.ept == 8) back_held<T, X, LAYER, 64, 8>(x, k, sh, g, once, s);
+        else back_held<T, X, LAYER, 64, 16>(x, k, sh, g, once, s);
         SGC_LAUNCH_CHECK();
     }
     if (k.part) {

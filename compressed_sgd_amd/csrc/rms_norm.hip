@@ -26,49 +26,27 @@ struct Rms {
     float eps;
 };
 
-// The sum and the largest magnitude over the NTR threads of a row, as row_sums.
-template <int NTR, int RPB>
-__device__ inline void row_sum_umax(float& a, uint32_t& m, RowTmp<NTR, RPB>& tmp, int turn)
-{
-    if constexpr (NTR == 16) {
-        a = row16_sum(a);
-        m = lanes_umax<16>(m);
-    } else {
-        constexpr int NWR = NTR / 64;
-        a = wave_sum(a);
-        m = wave_umax(m);
-        if (NWR == 1) return;
-        const int wave = threadIdx.x >> 6, sub = wave / NWR, w = wave % NWR;
-        if ((threadIdx.x & 63) == 0) {
-            tmp[turn][sub][w][0] = a;
-            tmp[turn][sub][w][1] = __uint_as_float(m);
-        }
-        __syncthreads();
-        a = sum_of_lanes<NWR>(tmp[turn][sub][threadIdx.x % NWR][0]);
-        m = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)lanes_umax<NWR>(__float_as_uint(tmp[turn][sub][threadIdx.x % NWR][1])));
-    }
-}
-
 // Rows in registers, as the layer norm's.  E8: 8 bits out.
-template <typename T, int NTR, int EPT, int RPB, bool RAG, bool E8>
-__global__ __launch_bounds__(NTR* RPB) void k_rms(Rms k, bool once)
+template <typename T, int LANES, int EPT, bool RAG, bool E8>
+__global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int waves, int side, bool once)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL;
-    __shared__ RowTmp<NTR, RPB> tmp;
-    const int sub = row_place<NTR>(), t = threadIdx.x % NTR, cols = k.cols;
+    __shared__ RowJoin tmp;
+    if (LANES == 64 && waves > 1) clear_join(tmp);
+    const RowPlace<LANES> place(waves);
+    const int sub = place.sub, t = place.t, across = place.across, cols = k.cols;
     float wf[EPT];
-    load_weights<T, NV, NTR>(k.w, k.w32, t, cols, 1.f, wf);
+    row_weights<T, NV>(k.w, k.w32, across, t, cols, 1.f, wf);
     Raw nx[NV] = {}, nr[NV] = {};
-    int64_t r = (int64_t)blockIdx.x * RPB + sub;
-    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * side + sub;
+    const int64_t step = (int64_t)gridDim.x * side;
     const auto fetch = [&](int64_t at) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) nx[n] = load_vec<T, RAG>((const T*)k.x + at * k.xs, n * NTR + t, cols, once);
+        for (int n = 0; n < NV; ++n) nx[n] = load_vec<T, RAG>((const T*)k.x + at * k.xs, n * across + t, cols, once);
         if (k.res) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                nr[n] = load_vec<T, RAG>((const T*)k.res + at * k.ress, n * NTR + t, cols, once);
+                nr[n] = load_vec<T, RAG>((const T*)k.res + at * k.ress, n * across + t, cols, once);
         }
     };
     if (r < k.rows) fetch(r);
@@ -76,11 +54,15 @@ __global__ __launch_bounds__(NTR* RPB) void k_rms(Rms k, bool once)
     for (; r - sub < k.rows; r += step, turn ^= 1) {
         float f[EPT];
 #pragma unroll
-        for (int n = 0; n < NV; ++n) unpack<T>(nx[n], f + n * VL);
+        for (int n = 0; n < NV; ++n) {
+            settle<T, RAG>(nx[n], n * across + t, cols);
+            unpack<T>(nx[n], f + n * VL);
+        }
         if (k.res) {
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 float g[VL];
+                settle<T, RAG>(nr[n], n * across + t, cols);
                 unpack<T>(nr[n], g);
 #pragma unroll
                 for (int e = 0; e < VL; ++e) f[n * VL + e] += g[e];
@@ -92,25 +74,23 @@ __global__ __launch_bounds__(NTR* RPB) void k_rms(Rms k, bool once)
         if (k.sum && live) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                store_vec<T, RAG>((T*)k.sum + r * k.ss, n * NTR + t, cols, f + n * VL, once);
+                store_vec<T, RAG>((T*)k.sum + r * k.ss, n * across + t, cols, f + n * VL, once);
         }
-        float ss = 0.f, none = 0.f;
-        uint32_t top = 0;
+        float ss = 0.f, most = 0.f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             ss = fmaf(f[i], f[i], ss);
             if (E8) {
                 f[i] *= wf[i];
                 // past the end 0 times the 1 that stands for a weight there
-                top = umax(top, magnitude(f[i]));
+                most = __uint_as_float(umax(__float_as_uint(most), magnitude(f[i])));
             }
         }
-        if (E8) row_sum_umax<NTR, RPB>(ss, top, tmp, turn);
-        else row_sums<NTR, RPB>(ss, none, tmp, turn);
+        row_join<E8, LANES>(ss, most, tmp, turn, waves, sub);
         const float rs = 1.f / sqrtf(ss / (float)cols + k.eps);
         if (!live) continue;
         if (E8) {
-            const Quant u = quant_of(top);
+            const Quant u = quant_of(__float_as_uint(most));
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 uint32_t q[VL];
@@ -119,7 +99,7 @@ __global__ __launch_bounds__(NTR* RPB) void k_rms(Rms k, bool once)
                 Bytes<VL> b;
 #pragma unroll
                 for (int e = 0; e < VL; e += 4) b.w[e / 4] = four_bytes(q[e], q[e + 1], q[e + 2], q[e + 3]) & u.keep;
-                store_bytes<VL, RAG>(k.q + r * k.qs, n * NTR + t, cols, b);
+                store_bytes<VL, RAG>(k.q + r * k.qs, n * across + t, cols, b);
             }
             if (t == 0) k.qscale[r] = u.scale * rs;
         } else {
@@ -127,7 +107,7 @@ __global__ __launch_bounds__(NTR* RPB) void k_rms(Rms k, bool once)
             for (int i = 0; i < EPT; ++i) f[i] = f[i] * rs * wf[i];
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                store_vec<T, RAG>((T*)k.y + r * k.ys, n * NTR + t, cols, f + n * VL, once);
+                store_vec<T, RAG>((T*)k.y + r * k.ys, n * across + t, cols, f + n * VL, once);
         }
         if (t == 0 && k.rstd) k.rstd[r] = rs;
     }
@@ -182,16 +162,16 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(Rms k)
     }
 }
 
-template <typename T, int NTR, int EPT, int RPB>
-static void rms_held(const Rms& k, unsigned g, bool once, hipStream_t s)
+template <typename T, int LANES, int EPT>
+static void rms_held(const Rms& k, const RowShape& sh, unsigned g, bool once, hipStream_t s)
 {
     const bool rag = k.cols % VecLen<T>::value;
     if (k.q) {
-        if (rag) k_rms<T, NTR, EPT, RPB, true, true><<<g, NTR * RPB, 0, s>>>(k, once);
-        else k_rms<T, NTR, EPT, RPB, false, true><<<g, NTR * RPB, 0, s>>>(k, once);
+        if (rag) k_rms<T, LANES, EPT, true, true><<<g, sh.threads(), 0, s>>>(k, sh.waves, sh.rows, once);
+        else k_rms<T, LANES, EPT, false, true><<<g, sh.threads(), 0, s>>>(k, sh.waves, sh.rows, once);
     } else {
-        if (rag) k_rms<T, NTR, EPT, RPB, true, false><<<g, NTR * RPB, 0, s>>>(k, once);
-        else k_rms<T, NTR, EPT, RPB, false, false><<<g, NTR * RPB, 0, s>>>(k, once);
+        if (rag) k_rms<T, LANES, EPT, true, false><<<g, sh.threads(), 0, s>>>(k, sh.waves, sh.rows, once);
+        else k_rms<T, LANES, EPT, false, false><<<g, sh.threads(), 0, s>>>(k, sh.waves, sh.rows, once);
     }
 }
 
@@ -203,27 +183,14 @@ static int rms_forward(const Rms& k, int32_t dtype, hipStream_t s)
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
-    const NormShape sh = norm_shape(k.cols, dtype, false);
-    const int64_t need = cdiv(k.rows, sh.rpb), most = kCus * kForwardWaves * 64 / (sh.ntr * sh.rpb);
-    const unsigned g = (unsigned)(need < most ? need : most);
+    const RowShape sh = row_shape(k.cols);
+    const unsigned g = (unsigned)row_groups(sh, k.rows, kForwardWaves);
     const int64_t moved = (1 + (k.res != nullptr) + (k.sum != nullptr)) * (int64_t)sizeof(T) + (k.q ? 1 : sizeof(T));
     const bool once = k.rows * k.cols * moved >= kCacheBytes;
-    const int shape = sh.ntr * 100 + sh.ept;
-    if constexpr (sizeof(T) == 4) {
-        if (shape == 6412) rms_held<T, 64, 12, 8>(k, g, once, s);
-    } else {
-        if (shape == 51216) rms_held<T, 512, 16, 1>(k, g, once, s);
-        else if (shape == 25616) rms_held<T, 256, 16, 2>(k, g, once, s);
-        else if (shape == 12816) rms_held<T, 128, 16, 4>(k, g, once, s);
-        else if (shape == 6416) rms_held<T, 64, 16, 8>(k, g, once, s);
-    }
-    if (shape == 102416) rms_held<T, 1024, 16, 1>(k, g, once, s);
-    else if (shape == 102408) rms_held<T, 1024, 8, 1>(k, g, once, s);
-    else if (shape == 51208) rms_held<T, 512, 8, 1>(k, g, once, s);
-    else if (shape == 25608) rms_held<T, 256, 8, 2>(k, g, once, s);
-    else if (shape == 12808) rms_held<T, 128, 8, 4>(k, g, once, s);
-    else if (shape == 6408) rms_held<T, 64, 8, 8>(k, g, once, s);
-    else if (shape == 1608) rms_held<T, 16, 8, 32>(k, g, once, s);
+    if (sh.lanes == 16) rms_held<T, 16, 8>(k, sh, g, once, s);
+    else if (sh.lanes == 32) rms_held<T, 32, 8>(k, sh, g, once, s);
+    else if (sh.ept == 8) rms_held<T, 64, 8>(k, sh, g, once, s);
+    else rms_held<T, 64, 16>(k, sh, g, once, s);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
@@ -259,7 +226,7 @@ extern "C" size_t sgc_rms_norm_backward_workspace(const sgc_norm_opts* o)
 {
     if (!norm_opts_ok(o)) return 0;
     Carver c(nullptr);
-    c.take<float>(back_parts(o->rows, o->cols, o->dtype) * o->cols);
+    c.take<float>(back_parts(o->rows, o->cols, false) * o->cols);
     return c.off;
 }
 
@@ -289,11 +256,11 @@ extern "C" int sgc_rms_norm_backward(const sgc_norm_opts* o, const void* dy, int
     const bool add = o->flags & SGC_NORM_ADD_GRADS;
     switch (o->dtype) {
     case SGC_F32:
-        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, dweight, nullptr, add, s);
     case SGC_BF16:
-        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add,
+        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, dweight, nullptr, add,
                                                       s);
     default:
-        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, dweight, nullptr, add, s);
     }
 }
