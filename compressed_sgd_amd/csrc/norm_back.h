@@ -99,7 +99,7 @@ __device__ inline float weight_at(const void* w, bool w32, int c, float none)
 // again in every row (volatile: else they move back into registers).
 typedef float Four __attribute__((ext_vector_type(4)));
 template <typename T, typename X, bool LAYER, int LANES, int EPT, bool RAG, int MOST>
-__global__ __launch_bounds__(MOST, LAYER && MOST == 512 ? 3 : 4) void k_back(X x, Back k, int waves, int side,
+__global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int side,
                                                                              bool once)
 {
     constexpr int VL = VecLen<T>::value, NV = EPT / VL;
@@ -318,7 +318,7 @@ inline int64_t back_parts(int64_t rows, int64_t cols, bool layer)
 {
     if (cols > kNormHeld) return rows < 64 ? rows : 64;
     const RowShape sh = row_shape(cols);
-    return row_groups(sh, rows, layer && sh.threads() <= 512 ? 12 : kBackwardWaves);
+    return row_groups(sh, rows, kBackwardWaves);
 }
 
 template <typename T, typename X, bool LAYER, int LANES, int EPT>
