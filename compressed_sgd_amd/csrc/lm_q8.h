@@ -71,6 +71,18 @@ __device__ inline uint32_t lanes_umax(uint32_t x)
     return x;
 }
 
+// The largest magnitude over a workgroup of NW waves, in every thread.
+template <int NW>
+__device__ inline uint32_t block_umax(uint32_t x, uint32_t* tmp)
+{
+    x = wave_umax(x);
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = (uint32_t)__builtin_amdgcn_readfirstlane((int)lanes_umax<NW>(tmp[threadIdx.x % NW]));
+    __syncthreads();
+    return x;
+}
+
 // ------------------------------------------------------ ends of ragged rows
 // Four words (or two, or one) without their first `drop` bytes, zeros behind.
 __device__ inline void drop_bytes(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d, int drop)
@@ -311,13 +323,15 @@ __device__ inline void row_weights(const void* w, bool w32, int across, int t, i
     }
 }
 
-// 8 elements a thread, in 16 or 32 lanes, or in as many waves as that takes; 16
-// in rows that are longer than 16 waves hold so.
-inline RowShape row_shape(int64_t cols)
+// 8 elements a thread, in 16 or 32 lanes, or in as many waves as that takes; 4
+// (a vector of fp32) where 8 waves hold a row so (8000 x 4001 fp32 backward 98 ->
+// 91 us with them, 20001 x 650 from 8 bits 40.5 -> 35.8, but by 16 waves the
+// layer norm's 88 -> 97), 16 in rows that are longer than 16 waves hold with 8.
+inline RowShape row_shape(int64_t cols, int32_t dtype)
 {
     if (cols <= 128) return {16, 8, 1, 32};
     if (cols <= 256) return {32, 8, 1, 16};
-    const int ept = cols <= 8192 ? 8 : 16, waves = (int)cdiv(cols, 64 * ept);
+    const int ept = cols <= 2048 && dtype == SGC_F32 ? 4 : cols <= 8192 ? 8 : 16, waves = (int)cdiv(cols, 64 * ept);
     return {64, ept, waves, waves < 8 ? 8 / waves : 1};
 }
 

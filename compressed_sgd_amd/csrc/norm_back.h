@@ -230,7 +230,7 @@ __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int si
     const int at = kFold ? threadIdx.x >> 6 : sub, beside = kFold ? 8 : side;
     const bool mine = !kFold || (threadIdx.x & 63) < LANES;
     // rows side by side have 4 waves at most
-    __shared__ float sw[kSums][EPT * (kFold ? LANES : EPT == 8 ? 256 : 1)];
+    __shared__ float sw[kSums][EPT * (kFold ? LANES : EPT <= 8 ? 256 : 1)];
     if (beside > 1) {
         for (int o = beside - 1; o > 0; --o) {
             __syncthreads();
@@ -314,10 +314,10 @@ __global__ __launch_bounds__(256) void k_back_long_dw(X x, Back k)
     if (LAYER) p[k.cols] = ab;
 }
 
-inline int64_t back_parts(int64_t rows, int64_t cols, bool layer)
+inline int64_t back_parts(int64_t rows, int64_t cols, int32_t dtype)
 {
     if (cols > kNormHeld) return rows < 64 ? rows : 64;
-    const RowShape sh = row_shape(cols);
+    const RowShape sh = row_shape(cols, dtype);
     return row_groups(sh, rows, kBackwardWaves);
 }
 
@@ -325,7 +325,7 @@ template <typename T, typename X, bool LAYER, int LANES, int EPT>
 static void back_held(const X& x, const Back& k, const RowShape& sh, unsigned g, bool once, hipStream_t s)
 {
     const bool rag = k.cols % VecLen<T>::value;
-    if constexpr (EPT == 8) {
+    if constexpr (EPT <= 8) {
         if (sh.threads() <= 512) {
             if (rag) k_back<T, X, LAYER, LANES, EPT, true, 512><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
             else k_back<T, X, LAYER, LANES, EPT, false, 512><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
@@ -339,9 +339,9 @@ static void back_held(const X& x, const Back& k, const RowShape& sh, unsigned g,
 }
 
 template <typename T, typename X, bool LAYER>
-static int norm_back(const X& x, const Back& k, float* dw, float* db, bool add, hipStream_t s)
+static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float* db, bool add, hipStream_t s)
 {
-    const int64_t parts = back_parts(k.rows, k.cols, LAYER);
+    const int64_t parts = back_parts(k.rows, k.cols, dtype);
     if (k.rows && k.cols > kNormHeld) {
         if (k.part) {  // before dx, which may take dy's or the input's place
             k_back_long_dw<T, X, LAYER><<<dim3((unsigned)cdiv(k.cols, 256), (unsigned)parts), 256, 0, s>>>(x, k);
@@ -355,10 +355,13 @@ static int norm_back(const X& x, const Back& k, float* dw, float* db, bool add, 
         const unsigned g = (unsigned)parts;
         const int64_t moved = 2 + (k.dsum != nullptr) + (k.dx != nullptr) + (k.y != nullptr);
         const bool once = k.rows * k.cols * moved * (int64_t)sizeof(T) >= kCacheBytes;
-        const RowShape sh = row_shape(k.cols);
+        const RowShape sh = row_shape(k.cols, dtype);
         if (sh.lanes == 16) back_held<T, X, LAYER, 16, 8>(x, k, sh, g, once, s);
         else if (sh.lanes == 32) back_held<T, X, LAYER, 32, 8>(x, k, sh, g, once, s);
         else if (sh.ept == 8) back_held<T, X, LAYER, 64, 8>(x, k, sh, g, once, s);
+        else if (sh.ept == 4) {
+            if constexpr (sizeof(T) == 4) back_held<T, X, LAYER, 64, 4>(x, k, sh, g, once, s);
+        }
         else back_held<T, X, LAYER, 64, 16>(x, k, sh, g, once, s);
         SGC_LAUNCH_CHECK();
     }

@@ -18,8 +18,8 @@ static int norm_back_8(const sgc_norm_q8_opts* o, const int8_t* q, int64_t qs, c
 {
     const As8Bits<T> x = {q, qs, scale, q8_groups(o->cols, o->group), q8_shift(o->group)};
     const bool add = o->flags & SGC_NORM_ADD_GRADS;
-    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits<T>, true>(x, k, dw, db, add, s)
-                                     : norm_back<T, As8Bits<T>, false>(x, k, dw, db, add, s);
+    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits<T>, true>(x, k, o->dtype, dw, db, add, s)
+                                     : norm_back<T, As8Bits<T>, false>(x, k, o->dtype, dw, db, add, s);
 }
 
 }  // namespace sgc
@@ -30,7 +30,7 @@ extern "C" size_t sgc_norm_backward_q8_workspace(const sgc_norm_q8_opts* o)
 {
     if (!norm_q8_ok(o)) return 0;
     Carver c(nullptr);
-    c.take<float>(back_parts(o->rows, o->cols, o->kind == SGC_NORM_LAYER) * o->cols * (o->kind == SGC_NORM_LAYER ? 2 : 1));
+    c.take<float>(back_parts(o->rows, o->cols, o->dtype) * o->cols * (o->kind == SGC_NORM_LAYER ? 2 : 1));
     return c.off;
 }
 

@@ -113,18 +113,6 @@ __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int wave
     }
 }
 
-// The largest magnitude over a workgroup of NW waves, in every thread.
-template <int NW>
-__device__ inline uint32_t block_umax(uint32_t x, uint32_t* tmp)
-{
-    x = wave_umax(x);
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = (uint32_t)__builtin_amdgcn_readfirstlane((int)lanes_umax<NW>(tmp[threadIdx.x % NW]));
-    __syncthreads();
-    return x;
-}
-
 // One workgroup a row, the row read again for every pass.  Every element is
 // read and written by one thread alone, so the sum and y may take the inputs'
 // places; once the sum is written it is read instead of them.
@@ -183,13 +171,16 @@ static int rms_forward(const Rms& k, int32_t dtype, hipStream_t s)
         SGC_LAUNCH_CHECK();
         return SGC_OK;
     }
-    const RowShape sh = row_shape(k.cols);
+    const RowShape sh = row_shape(k.cols, dtype);
     const unsigned g = (unsigned)row_groups(sh, k.rows, kForwardWaves);
     const int64_t moved = (1 + (k.res != nullptr) + (k.sum != nullptr)) * (int64_t)sizeof(T) + (k.q ? 1 : sizeof(T));
     const bool once = k.rows * k.cols * moved >= kCacheBytes;
     if (sh.lanes == 16) rms_held<T, 16, 8>(k, sh, g, once, s);
     else if (sh.lanes == 32) rms_held<T, 32, 8>(k, sh, g, once, s);
     else if (sh.ept == 8) rms_held<T, 64, 8>(k, sh, g, once, s);
+    else if (sh.ept == 4) {
+        if constexpr (sizeof(T) == 4) rms_held<T, 64, 4>(k, sh, g, once, s);
+    }
     else rms_held<T, 64, 16>(k, sh, g, once, s);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
@@ -226,7 +217,7 @@ extern "C" size_t sgc_rms_norm_backward_workspace(const sgc_norm_opts* o)
 {
     if (!norm_opts_ok(o)) return 0;
     Carver c(nullptr);
-    c.take<float>(back_parts(o->rows, o->cols, false) * o->cols);
+    c.take<float>(back_parts(o->rows, o->cols, o->dtype) * o->cols);
     return c.off;
 }
 
@@ -256,11 +247,11 @@ extern "C" int sgc_rms_norm_backward(const sgc_norm_opts* o, const void* dy, int
     const bool add = o->flags & SGC_NORM_ADD_GRADS;
     switch (o->dtype) {
     case SGC_F32:
-        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, dweight, nullptr, add, s);
+        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
     case SGC_BF16:
-        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, dweight, nullptr, add,
+        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add,
                                                       s);
     default:
-        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, dweight, nullptr, add, s);
+        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
     }
 }
