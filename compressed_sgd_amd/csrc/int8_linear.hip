@@ -28,16 +28,25 @@ typedef int Int16 __attribute__((ext_vector_type(16)));
 // 16 bytes of a row, at any address.
 typedef int Bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
-// Bytes [at, at + 16) of a row of `width`; past it 0.
+// Bytes [at, at + 16) of a row of `width`; past it 0.  The row's end is read with
+// what lies before it, in one access; rows shorter than that byte by byte.
 __device__ inline Int4 load16(const int8_t* row, int at, int width)
 {
-    if (at + 16 <= width) return *(const Bytes16*)(row + at);
     Int4 v = {0, 0, 0, 0};
-    if (at < width) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (at + i < width) v[i / 4] |= (int)(uint8_t)row[at + i] << (i % 4 * 8);
+    if (at >= width) return v;
+    if (width >= 16) {
+        const int over = at + 16 - width;
+        v = *(const Bytes16*)(row + at - (over > 0 ? over : 0));
+        if (over > 0) {
+            uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
+            drop_bytes(w0, w1, w2, w3, over);
+            v = {(int)w0, (int)w1, (int)w2, (int)w3};
+        }
+        return v;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < width) v[i / 4] |= (int)(uint8_t)row[i] << (i % 4 * 8);
     return v;
 }
 
@@ -97,17 +106,19 @@ __device__ inline void into_shared(const int8_t* p, Int4* to)
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
                                      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
-template <typename T, int TM, int TN, int WM, int WN, bool DIRECT>
+template <typename T, int TM, int TN, int WM, int WN, int STAGES, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m, int tiles_n)
 {
     constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 32, PN = TN / WN / 32;
     constexpr int CX = TM * 8 / kThreads, CW = TN * 8 / kThreads, kRows = kThreads / 8;
-    // Two steps' rows, in arrays of their own: the compiler then knows that rows on
-    // their way into one are not what is read from the other.  Later 32 tokens of
+    // Each step's rows in an array of its own: the compiler then knows that rows on
+    // their way into one are not what is read from another.  Later 32 tokens of
     // each wave's results, a row's pitch 16 bytes past its length.
     constexpr int kPitch = PN * 32 * (int)sizeof(T) + 16, kOut = WM * WN / 4 * 2 * kPitch;
     constexpr int kX = TM * 8 > kOut ? TM * 8 : kOut, kW = TN * 8 > kOut ? TN * 8 : kOut;
     __shared__ Int4 x0[kX], x1[kX], w0[kW], w1[kW];
+    __shared__ Int4 x2[STAGES > 2 ? TM * 8 : 1], x3[STAGES > 2 ? TM * 8 : 1];
+    __shared__ Int4 w2[STAGES > 2 ? TN * 8 : 1], w3[STAGES > 2 ? TN * 8 : 1];
     __shared__ alignas(16) float channels[2][TN];  // their scales and biases
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
@@ -137,43 +148,47 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         const int64_t r = n0 + row + i * kRows;
         pw[i] = k.w + (r < k.out ? r : k.out - 1) * k.ws + piece * 16;
     }
-    const int steps = (k.width + kStep - 1) / kStep, whole = k.width / kStep;
+    // where the width is no multiple of 128 its end is step 0 (the order within the sum
+    // is free), which is cheapest there: nothing else is in registers yet
+    const int steps = (k.width + kStep - 1) / kStep, part = k.width % kStep ? 1 : 0;
     Int4 rx[CX], rw[CW];
-    const auto fetch = [&](int s) {
-        if (DIRECT || s >= whole) return;
+    const auto fetch = [&](int s) __attribute__((always_inline)) {
+        if (DIRECT || s < part || s >= steps) return;
+        const int at = (s - part) * kStep;
 #pragma unroll
-        for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + s * kStep);
+        for (int i = 0; i < CX; ++i) rx[i] = *(const Bytes16*)(px[i] + at);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + s * kStep);
+        for (int i = 0; i < CW; ++i) rw[i] = *(const Bytes16*)(pw[i] + at);
     };
-    // Step s into shared memory; the last one of a width that is no multiple of 128
-    // byte by byte where it ends.
-    const auto put = [&](Int4* x, Int4* w, int s) {
-        if (s < whole) {
+    // Step s, whole, into shared memory.
+    const auto put = [&](Int4* x, Int4* w, int s) __attribute__((always_inline)) {
+        if (s >= steps) return;
+        const int at = (s - part) * kStep;
 #pragma unroll
-            for (int i = 0; i < CX; ++i) {
-                if constexpr (DIRECT)
-                    into_shared(px[i] + s * kStep, x + wave * 64 + i * kThreads);
-                else
-                    x[t + i * kThreads] = rx[i];
-            }
-#pragma unroll
-            for (int i = 0; i < CW; ++i) {
-                if constexpr (DIRECT)
-                    into_shared(pw[i] + s * kStep, w + wave * 64 + i * kThreads);
-                else
-                    w[t + i * kThreads] = rw[i];
-            }
-        } else if (s < steps) {
-#pragma unroll 1
-            for (int i = 0; i < CX + CW; ++i) {
-                const bool of_x = i < CX;
-                const int place = of_x ? i : i - CX;
-                const int64_t r = (of_x ? m0 : n0) + row + place * kRows, last = (of_x ? k.rows : k.out) - 1;
-                const int8_t* p = (of_x ? k.x : k.w) + (r < last ? r : last) * (of_x ? k.xs : k.ws);
-                (of_x ? x : w)[t + place * kThreads] = load16(p, s * kStep + piece * 16, k.width);
-            }
+        for (int i = 0; i < CX; ++i) {
+            if constexpr (DIRECT)
+                into_shared(px[i] + at, x + wave * 64 + i * kThreads);
+            else
+                x[t + i * kThreads] = rx[i];
         }
+#pragma unroll
+        for (int i = 0; i < CW; ++i) {
+            if constexpr (DIRECT)
+                into_shared(pw[i] + at, w + wave * 64 + i * kThreads);
+            else
+                w[t + i * kThreads] = rw[i];
+        }
+    };
+    const auto put_end = [&](Int4* x, Int4* w) __attribute__((always_inline)) {
+        const int at = (steps - 1) * kStep + piece * 16;
+#pragma unroll
+        for (int i = 0; i < CX; ++i) rx[i] = load16(px[i] - piece * 16, at, k.width);
+#pragma unroll
+        for (int i = 0; i < CW; ++i) rw[i] = load16(pw[i] - piece * 16, at, k.width);
+#pragma unroll
+        for (int i = 0; i < CX; ++i) x[t + i * kThreads] = rx[i];
+#pragma unroll
+        for (int i = 0; i < CW; ++i) w[t + i * kThreads] = rw[i];
     };
     Int16 acc[PN][PM];
 #pragma unroll
@@ -185,14 +200,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     const int lr = lane & 31, half = lane >> 5;
     const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
     Int4 fx[2][PM], fw[2][PN];
-    const auto read = [&](const Int4* x, const Int4* w, int kk) {
+    const auto read = [&](const Int4* x, const Int4* w, int kk) __attribute__((always_inline)) {
         const int p = (kk * 2 + half) ^ (lr & 7);
 #pragma unroll
         for (int j = 0; j < PM; ++j) fx[kk & 1][j] = x[ax + j * 256 + p];
 #pragma unroll
         for (int i = 0; i < PN; ++i) fw[kk & 1][i] = w[aw + i * 256 + p];
     };
-    const auto multiply = [&](int kk) {
+    const auto multiply = [&](int kk) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -203,37 +218,74 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // what this wave has on its way into shared memory (a barrier alone does not wait for it)
-    const auto arrived = [] {
-        if (DIRECT) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    // Waits until this wave's part of step s lies in shared memory; of the later ones
+    // up to `ahead` may be on their way (a barrier alone does not wait for them).
+    const auto arrived = [&](int s, int ahead) __attribute__((always_inline)) {
+        if constexpr (DIRECT) {
+            constexpr int kEach = CX + CW;
+            static_assert((STAGES - 1) * kEach < 64, "");
+            constexpr auto code = [](int n) constexpr { return 0x0f70 | (n & 15) | (n >> 4) << 14; };  // vmcnt(n)
+            if (STAGES == 4 && ahead == 3 && s + 3 < steps) __builtin_amdgcn_s_waitcnt(code(STAGES == 4 ? 3 * kEach : 0));
+            else if (STAGES == 4 && ahead == 2 && s + 2 < steps) __builtin_amdgcn_s_waitcnt(code(STAGES == 4 ? 2 * kEach : 0));
+            else if (STAGES == 2 && ahead == 1 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(code(kEach));
+            else __builtin_amdgcn_s_waitcnt(code(0));
+        }
+    };
+    // with more than two stages later rows stay on their way across the barrier: only
+    // what this wave reads and writes in shared memory is waited for (lgkmcnt(0))
+    const auto meet = [] {
+        if constexpr (STAGES == 2) {
+            __syncthreads();
+        } else {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xc07f);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        }
     };
     // The operands of the next products are read while one step's run.  One barrier a
     // step, before its last products: what is read of this step's rows has been
-    // read, and the step after next takes their place; the next step's lie ready.
-    const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w) {
+    // read, and rows STAGES steps on take their place; the next step's lie ready.
+    const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk + 1 < kStep / 32; ++kk) {
             read(x, w, kk + 1);
             multiply(kk);
         }
-        arrived();
-        __syncthreads();
-        put(x, w, s + 2);
-        fetch(s + 3);
+        arrived(s + 1, STAGES - 2);
+        meet();
+        put(x, w, s + STAGES);
+        fetch(s + STAGES + 1);
         if (s + 1 < steps) read(next_x, next_w, 0);
         multiply(kStep / 32 - 1);
     };
-    fetch(0);
-    put(x0, w0, 0);
+    if (part) {
+        put_end(x0, w0);
+    } else {
+        fetch(0);
+        put(x0, w0, 0);
+    }
     fetch(1);
     put(x1, w1, 1);
     fetch(2);
-    arrived();
-    __syncthreads();
+    if constexpr (STAGES == 4) {
+        put(x2, w2, 2);
+        fetch(3);
+        put(x3, w3, 3);
+        fetch(4);
+    }
+    arrived(0, STAGES - 1);
+    meet();
     read(x0, w0, 0);
-    for (int s = 0; s < steps; s += 2) {
+    for (int s = 0; s < steps; s += STAGES) {
         step(s, x0, w0, x1, w1);
-        if (s + 1 < steps) step(s + 1, x1, w1, x0, w0);
+        if constexpr (STAGES == 2) {
+            if (s + 1 < steps) step(s + 1, x1, w1, x0, w0);
+        } else {
+            if (s + 1 < steps) step(s + 1, x1, w1, x2, w2);
+            if (s + 2 < steps) step(s + 2, x2, w2, x3, w3);
+            if (s + 3 < steps) step(s + 3, x3, w3, x0, w0);
+        }
     }
     __syncthreads();
     // 32 tokens of a wave at a time through its own part of shared memory, so that
@@ -370,11 +422,11 @@ static void few(const Product& k, hipStream_t s)
     k_few<T, B><<<grid, 64 * kFewWaves, 0, s>>>(k, split);
 }
 
-template <typename T, int TM, int TN, int WM, int WN, bool DIRECT>
+template <typename T, int TM, int TN, int WM, int WN, int STAGES, bool DIRECT>
 static int tiles(const Product& k, hipStream_t s)
 {
     const int64_t tm = cdiv(k.rows, TM), tn = cdiv(k.out, TN);
-    k_tile<T, TM, TN, WM, WN, DIRECT><<<row_grid(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
+    k_tile<T, TM, TN, WM, WN, STAGES, DIRECT><<<row_grid(tm * tn), 64 * WM * WN, 0, s>>>(k, (int)tm, (int)tn);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
@@ -393,9 +445,12 @@ static int product(const Product& k, hipStream_t s)
         return SGC_OK;
     }
     const bool direct = aligned16(k.x) && aligned16(k.w) && k.xs % 16 == 0 && k.ws % 16 == 0;
-    if (cdiv(k.rows, 256) * cdiv(k.out, 256) >= 256)
-        return direct ? tiles<T, 256, 256, 4, 2, true>(k, s) : tiles<T, 256, 256, 4, 2, false>(k, s);
-    return direct ? tiles<T, 128, 128, 2, 2, true>(k, s) : tiles<T, 128, 128, 2, 2, false>(k, s);
+    const auto count = [&](int64_t tm, int64_t tn) { return cdiv(k.rows, tm) * cdiv(k.out, tn); };
+    if (count(256, 256) >= 256)
+        return direct ? tiles<T, 256, 256, 4, 2, 2, true>(k, s) : tiles<T, 256, 256, 4, 2, 2, false>(k, s);
+    if (count(128, 128) >= 256)
+        return direct ? tiles<T, 128, 128, 2, 2, 2, true>(k, s) : tiles<T, 128, 128, 2, 2, 2, false>(k, s);
+    return direct ? tiles<T, 64, 64, 2, 2, 4, true>(k, s) : tiles<T, 64, 64, 2, 2, 2, false>(k, s);
 }
 
 }  // namespace sgc
