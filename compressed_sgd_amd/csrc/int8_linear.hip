@@ -346,8 +346,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
     __shared__ Int4 part[kFewWaves][B][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int share = wave % split, per = kFewWaves / split;
-    const int64_t n0 = ((int64_t)blockIdx.x * per + wave / split) * 16;
-    const int64_t m0 = (int64_t)blockIdx.y * 16 * B;
+    const int64_t n0 = (row_of_block() * per + wave / split) * 16;
     const int lr = lane & 15, quarter = lane >> 4;
     Int4 acc[B];
 #pragma unroll
@@ -358,7 +357,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
         const int8_t* px[B];
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            const int64_t r = m0 + j * 16 + lr;
+            const int64_t r = j * 16 + lr;
             px[j] = k.x + (r < k.rows ? r : k.rows - 1) * k.xs;
         }
         const int steps = (k.width + 63) / 64, each = (steps + split - 1) / split;
@@ -404,7 +403,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
     channel4(k, o, ws, bias);
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-        const int64_t r = m0 + j * 16 + lr;
+        const int64_t r = j * 16 + lr;
         if (r >= k.rows) continue;
         const float xscale = k.xscale[r];
 #pragma unroll
@@ -413,13 +412,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
     }
 }
 
+// The sum is split until eight waves a compute unit have work or each has one
+// trip's loads (1 x 4096 x 4096: 8.6 us a pass with its call).
 template <typename T, int B>
-static void few(const Product& k, hipStream_t s)
+static int few(const Product& k, hipStream_t s)
 {
+    const int64_t units = cdiv(k.out, 16);
     int split = 1;
-    while (split < kFewWaves && cdiv(k.out, 16) * split < 256 * 8 && k.width > split * 64 * kFewDeep) split *= 2;
-    const dim3 grid((unsigned)cdiv(cdiv(k.out, 16), kFewWaves / split), (unsigned)cdiv(k.rows, 16 * B));
-    k_few<T, B><<<grid, 64 * kFewWaves, 0, s>>>(k, split);
+    while (split < kFewWaves && units * split < 256 * 8 && k.width > split * 64 * kFewDeep) split *= 2;
+    k_few<T, B><<<row_grid(cdiv(units, kFewWaves / split)), 64 * kFewWaves, 0, s>>>(k, split);
+    SGC_LAUNCH_CHECK();
+    return SGC_OK;
 }
 
 template <typename T, int TM, int TN, int WM, int WN, int STAGES, bool DIRECT>
@@ -431,26 +434,31 @@ static int tiles(const Product& k, hipStream_t s)
     return SGC_OK;
 }
 
+template <typename T, int TM, int TN, int WM, int WN, int STAGES>
+static int tiles_of(const Product& k, hipStream_t s)
+{
+    const bool direct = aligned16(k.x) && aligned16(k.w) && k.xs % 16 == 0 && k.ws % 16 == 0;
+    return direct ? tiles<T, TM, TN, WM, WN, STAGES, true>(k, s) : tiles<T, TM, TN, WM, WN, 2, false>(k, s);
+}
+
+// Few tokens: straight from memory up to 8192 channels (32 x 4096 x 4096 9.0 us, in
+// tiles 11.8; 24 x 4096 x 16384 21.9, in tiles 15.8: every wave reads the
+// tokens' rows, where a tile reads them once), for one or two tokens always.
+// Else tiles of the size whose rounds over the chip take least, by what a round
+// takes there in microseconds, a part and a part a step (and about 2 more a
+// call): 2048 x 1024 x 10000 in tiles of 64, 128, 256: 53, 35, 44; 512 x 4096 x
+// 4096: 16, 23, 54; 1500 x 656 x 10000: 41, 25, 22; 800 x 2048 x 6000: 25, 22, 34.
 template <typename T>
 static int product(const Product& k, hipStream_t s)
 {
-    if (k.rows <= 16) {
-        few<T, 1>(k, s);
-        SGC_LAUNCH_CHECK();
-        return SGC_OK;
-    }
-    if (k.rows <= 32) {
-        few<T, 2>(k, s);
-        SGC_LAUNCH_CHECK();
-        return SGC_OK;
-    }
-    const bool direct = aligned16(k.x) && aligned16(k.w) && k.xs % 16 == 0 && k.ws % 16 == 0;
-    const auto count = [&](int64_t tm, int64_t tn) { return cdiv(k.rows, tm) * cdiv(k.out, tn); };
-    if (count(256, 256) >= 256)
-        return direct ? tiles<T, 256, 256, 4, 2, 2, true>(k, s) : tiles<T, 256, 256, 4, 2, 2, false>(k, s);
-    if (count(128, 128) >= 256)
-        return direct ? tiles<T, 128, 128, 2, 2, 2, true>(k, s) : tiles<T, 128, 128, 2, 2, 2, false>(k, s);
-    return direct ? tiles<T, 64, 64, 2, 2, 4, true>(k, s) : tiles<T, 64, 64, 2, 2, 2, false>(k, s);
+    if (k.rows <= 2 || (k.rows <= 32 && k.out <= 8192)) return k.rows <= 16 ? few<T, 1>(k, s) : few<T, 2>(k, s);
+    const double steps = (double)cdiv(k.width, kStep);
+    const auto cost = [&](int64_t tile, int64_t at_once, double round, double step) {
+        return (double)cdiv(cdiv(k.rows, tile) * cdiv(k.out, tile), at_once) * (round + step * steps);
+    };
+    const double c64 = cost(64, 512, 2.3, 0.35), c128 = cost(128, 512, 4.0, 1.0), c256 = cost(256, 256, 6.0, 1.9);
+    if (c64 <= c128 && c64 <= c256) return tiles_of<T, 64, 64, 2, 2, 4>(k, s);
+    return c128 <= c256 ? tiles_of<T, 128, 128, 2, 2, 2>(k, s) : tiles_of<T, 256, 256, 4, 2, 2>(k, s);
 }
 
 }  // namespace sgc
