@@ -18,8 +18,8 @@ from typing import Optional
 import torch
 
 from . import _check, lib
-from .lm import (_DTYPES, NORM_ADD_GRADS, NormOpts, _affine, _empty, _no_graph, _ptr, _rows, _scratch, _stream, _vec,
-                 _vec1, _written)
+from .lm import (_DTYPES, NORM_ADD_GRADS, NormOpts, _affine, _empty, _no_graph, _ptr, _rows, _scratch, _vec1,
+                 _written)
 
 NORM_LAYER, NORM_RMS = 0, 1
 Q8_GROUPS = (0, 32, 64, 128, 256)
@@ -57,15 +57,21 @@ def _declare(L) -> None:
 
 def _run(name: str, device: torch.device, stream, *args) -> None:
     """Calls the library with the device of the tensors current."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     f = getattr(lib(), name)
-    if torch._C._cuda_getDevice() == device.index:
-        rc = f(*args, _stream(device, stream))
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, _stream(device, stream))
-    _check(rc, name)
+            rc = f(*args, handle)
+    if rc:
+        _check(rc, name)
 
 
 # ------------------------------------------------------------- 8 bits
@@ -83,28 +89,37 @@ def _groups(cols: int, group: int) -> int:
     return -(-cols // group) if group else 1
 
 
-def _q8(t: Quantized, name: str, device=None, rows: Optional[int] = None, cols: Optional[int] = None) -> int:
-    """Checks 8-bit rows; their stride."""
-    q = t.q
+def _q8(t: Quantized, name: str):
+    """Checks 8-bit rows; their number, length and stride."""
+    q, scale, group = t.q, t.scale, t.group
     if not q.is_cuda:
         raise ValueError(f"{name}.q must be a device (HIP) tensor")
     if q.dim() != 2 or q.dtype != torch.int8:
         raise ValueError(f"{name}.q must be 2-D int8")
+    rows, cols = q.shape
     stride = q.stride()
-    if stride[1] != 1 and q.shape[1] > 1:
+    if stride[1] != 1 and cols > 1:
         raise ValueError(f"{name}.q must have contiguous rows")
-    if (device is not None and q.device != device) or (rows is not None and q.shape[0] != rows) or \
-            (cols is not None and q.shape[1] != cols):
+    shape = (rows, _groups(cols, group) if group else 1)
+    if scale.shape != shape or scale.dtype != torch.float32 or scale.device != q.device or not scale.is_contiguous():
+        raise ValueError(f"{name}.scale must be a contiguous float32 tensor of shape {shape} on {q.device}")
+    return rows, cols, stride[0]
+
+
+def _q8_like(t: Quantized, name: str, rows: int, cols: int, device) -> int:
+    """_q8 for rows of a known number, length and device; their stride."""
+    n, c, stride = _q8(t, name)
+    if n != rows or c != cols or t.q.device != device:
         raise ValueError(f"{name}.q must match the call's shape and device")
-    _vec(t.scale, f"{name}.scale", (q.shape[0], _groups(q.shape[1], t.group)), torch.float32, q.device)
-    return stride[0]
+    return stride
 
 
 def _new_q8(stream, rows: int, cols: int, group: int, device) -> Quantized:
     """Rows that begin at multiples of 16 bytes, which the products read fastest."""
-    q = _empty(stream, (rows, -(-cols // 16) * 16), torch.int8, device)
-    return Quantized(q if q.shape[1] == cols else q[:, :cols],
-                     _empty(stream, (rows, _groups(cols, group)), torch.float32, device), group)
+    whole = -(-cols // 16) * 16
+    q = _empty(stream, (rows, whole), torch.int8, device)
+    return Quantized(q if whole == cols else q[:, :cols],
+                     _empty(stream, (rows, _groups(cols, group) if group else 1), torch.float32, device), group)
 
 
 def quantize_q8(x: torch.Tensor, *, group: int = 128, out: Optional[Quantized] = None, stream=None) -> Quantized:
@@ -121,7 +136,7 @@ def quantize_q8(x: torch.Tensor, *, group: int = 128, out: Optional[Quantized] =
         to = out
         if out.group != group:
             raise ValueError("out.group must be the call's group")
-        qs = _q8(out, "out", dev, rows, cols)
+        qs = _q8_like(out, "out", rows, cols, dev)
     o = Q8Opts(rows, cols, _DTYPES[x.dtype], group)
     _run("sgc_quantize_q8", dev, stream, C.byref(o), _ptr(x), xs, _ptr(to.q), qs, _ptr(to.scale))
     if out is not None:
@@ -133,8 +148,7 @@ def dequantize_q8(x: Quantized, dtype: torch.dtype = torch.float32, *, out: Opti
                   stream=None) -> torch.Tensor:
     """The values that 8-bit rows stand for."""
     _no_graph(x.scale, out)
-    qs = _q8(x, "x")
-    rows, cols = x.q.shape
+    rows, cols, qs = _q8(x, "x")
     dev = x.q.device
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32, bfloat16 or float16")
@@ -171,24 +185,44 @@ class RmsGrads:
     dweight: Optional[torch.Tensor]   # float32 [cols]
 
 
-def _rms(x, weight, residual, sum_out, eps, y, ys, q8, qs, stream):
+def _rms(x, weight, residual, sum_out, out, eps, eight, stream):
+    """Either kind of output: y (out a tensor), or with `eight` Quantized; the sum, rstd."""
+    if torch.is_grad_enabled():
+        _no_graph(x, weight, residual, sum_out, None if eight else out)
     xs = _rows(x, "x")
     rows, cols = x.shape
-    dev = x.device
+    dev, dt = x.device, x.dtype
     wdt = _affine(weight, None, x, cols, dev)
-    rs = 0 if residual is None else _rows(residual, "residual", x)
+    rs = ss = ys = qs = 0
+    y = q8 = total = None
+    if residual is not None:
+        rs = _rows(residual, "residual", x)
+    if eight:
+        if out is None:
+            q8 = _new_q8(stream, rows, cols, 0, dev)
+            qs = q8.q.stride(0)
+        else:
+            if out.group:
+                raise ValueError("out must have one scale a row (group 0)")
+            q8, qs = out, _q8_like(out, "out", rows, cols, dev)
+    elif out is None:
+        y, ys = _empty(stream, (rows, cols), dt, dev), cols
+    else:
+        y, ys = out, _rows(out, "out", x)
     if sum_out is not None:
         total, ss = sum_out, _rows(sum_out, "sum_out", x)
     elif residual is not None:
-        total, ss = _empty(stream, (rows, cols), x.dtype, dev), cols
-    else:
-        total, ss = None, 0
+        total, ss = _empty(stream, (rows, cols), dt, dev), cols
     rstd = _empty(stream, (rows,), torch.float32, dev)
-    o = NormOpts(rows, cols, _DTYPES[x.dtype], wdt, eps, 0)
-    _run("sgc_rms_norm", dev, stream, C.byref(o), _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(total), ss,
-         _ptr(y), ys, None if q8 is None else _ptr(q8.q), qs, None if q8 is None else _ptr(q8.scale), _ptr(rstd))
-    _written(sum_out)
-    return x if total is None else total, rstd
+    o = NormOpts(rows, cols, _DTYPES[dt], wdt, eps, 0)
+    _run("sgc_rms_norm", dev, stream, C.byref(o), x.data_ptr(), xs, _ptr(residual), rs, _ptr(weight), _ptr(total), ss,
+         _ptr(y), ys, q8.q.data_ptr() if eight else None, qs, q8.scale.data_ptr() if eight else None,
+         rstd.data_ptr())
+    if sum_out is not None:
+        _written(sum_out)
+    if out is not None:
+        _written(*((out.q, out.scale) if eight else (out,)))
+    return q8 if eight else y, x if total is None else total, rstd
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
@@ -197,35 +231,14 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual
     """RMS norm of every row of x + residual [rows, cols]; the sum, rounded to
     x's type, is given too.  out and sum_out may be x or residual, not the
     same one."""
-    _no_graph(x, weight, residual, out, sum_out)
-    _rows(x, "x")
-    if out is None:
-        y, ys = _empty(stream, x.shape, x.dtype, x.device), x.shape[1]
-    else:
-        y, ys = out, _rows(out, "out", x)
-    total, rstd = _rms(x, weight, residual, sum_out, eps, y, ys, None, 0, stream)
-    _written(out)
-    return RmsNormalized(y, total, rstd)
+    return RmsNormalized(*_rms(x, weight, residual, sum_out, out, eps, False, stream))
 
 
 def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
                 eps: float = 1e-6, out: Optional[Quantized] = None, sum_out: Optional[torch.Tensor] = None,
                 stream=None) -> RmsQuantized:
     """rms_norm with its output in 8 bits, a scale a row: what int8_linear takes."""
-    _no_graph(x, weight, residual, sum_out)
-    _rows(x, "x")
-    rows, cols = x.shape
-    if out is None:
-        q8 = _new_q8(stream, rows, cols, 0, x.device)
-        qs = q8.q.stride(0)
-    else:
-        if out.group:
-            raise ValueError("out must have one scale a row (group 0)")
-        q8, qs = out, _q8(out, "out", x.device, rows, cols)
-    total, rstd = _rms(x, weight, residual, sum_out, eps, None, 0, q8, qs, stream)
-    if out is not None:
-        _written(out.q, out.scale)
-    return RmsQuantized(q8, total, rstd)
+    return RmsQuantized(*_rms(x, weight, residual, sum_out, out, eps, True, stream))
 
 
 def rms_norm_backward_workspace_bytes(rows: int, cols: int, dtype: torch.dtype = torch.float32) -> int:
@@ -290,7 +303,7 @@ def _backward_q8(kind, dy, x, weight, bias, mean, rstd, dsum, dx, dweight, dbias
     dys = _rows(dy, "dy")
     rows, cols = dy.shape
     dev = dy.device
-    qs = _q8(x, "x", dev, rows, cols)
+    qs = _q8_like(x, "x", rows, cols, dev)
     wdt = _affine(weight, bias, dy, cols, dev)
     for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (dweight, "dweight", cols),
                        (dbias, "dbias", cols)):
@@ -353,15 +366,17 @@ def int8_linear(x: Quantized, w: Quantized, bias: Optional[torch.Tensor] = None,
     width], each with one scale a row, plus bias [out] float32.  For scoring and
     serving: it has no gradient.  Rows that begin at multiples of 16 bytes, as
     quantize_q8 and rms_norm_q8 lay them out, are read fastest."""
-    _no_graph(x.scale, w.scale, bias, out)
+    if torch.is_grad_enabled():
+        _no_graph(x.scale, w.scale, bias, out)
     if x.group or w.group:
         raise ValueError("a product takes one scale a row (group 0)")
-    xs = _q8(x, "x")
-    rows, width = x.q.shape
+    rows, width, xs = _q8(x, "x")
+    n, length, wst = _q8(w, "w")
     dev = x.q.device
-    wst = _q8(w, "w", dev, None, width)
-    n = w.q.shape[0]
-    _vec1(bias, "bias", n, torch.float32, dev)
+    if length != width or w.q.device != dev:
+        raise ValueError("w must have x's width and device")
+    if bias is not None:
+        _vec1(bias, "bias", n, torch.float32, dev)
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32, bfloat16 or float16")
     if out is None:
@@ -371,7 +386,8 @@ def int8_linear(x: Quantized, w: Quantized, bias: Optional[torch.Tensor] = None,
         if out.shape != (rows, n) or out.dtype != dtype or out.device != dev:
             raise ValueError("out must match the product's shape and device and the type asked for")
     o = Int8Opts(rows, width, n, _DTYPES[dtype], 0)
-    _run("sgc_int8_linear", dev, stream, C.byref(o), _ptr(x.q), xs, _ptr(x.scale), _ptr(w.q), wst, _ptr(w.scale),
-         _ptr(bias), _ptr(y), ys)
-    _written(out)
+    _run("sgc_int8_linear", dev, stream, C.byref(o), x.q.data_ptr(), xs, x.scale.data_ptr(), w.q.data_ptr(), wst,
+         w.scale.data_ptr(), _ptr(bias), y.data_ptr(), ys)
+    if out is not None:
+        _written(out)
     return y
