@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
                 *(Pack<T, 4>*)(mine + lr * kPitch + c0 * (int)sizeof(T)) = p;
                 __builtin_amdgcn_sched_barrier(0);
             }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         constexpr int kPieces = PN * 32 / kPiece, kAtOnce = 64 / kPieces;
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
                     if (on + c0 + c < k.out) y[c] = v[c];
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
 }

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int wave
                 for (int e = 0; e < VL; e += 4) b.w[e / 4] = four_bytes(q[e], q[e + 1], q[e + 2], q[e + 3]) & u.keep;
                 store_bytes<VL, RAG>(k.q + r * k.qs, n * across + t, cols, b);
             }
-            if (t == 0) k.qscale[r] = u.scale * rs;
+            if (t == 0) k.qscale[r] = u.scale == 0.f ? 0.f : u.scale * rs;  // rs is infinite for zeros and eps 0
         } else {
 #pragma unroll
             for (int i = 0; i < EPT; ++i) f[i] = f[i] * rs * wf[i];
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(Rms k)
     Quant u = {};
     if (k.q) {
         u = quant_of(block_umax<kLongWaves>(top, utmp));
-        if (threadIdx.x == 0) k.qscale[r] = u.scale * rs;
+        if (threadIdx.x == 0) k.qscale[r] = u.scale == 0.f ? 0.f : u.scale * rs;  // rs is infinite for zeros and eps 0
     }
     if (threadIdx.x == 0 && k.rstd) k.rstd[r] = rs;
     for (int c = threadIdx.x; c < k.cols; c += kLongThreads) {

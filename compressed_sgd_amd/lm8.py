@@ -74,6 +74,16 @@ def _run(name: str, device: torch.device, stream, *args) -> None:
         _check(rc, name)
 
 
+def _like(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """Checks rows of a known shape, type and device; their stride."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must match the input's shape, type and device")
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return stride[0]
+
+
 # ------------------------------------------------------------- 8 bits
 @dataclass
 class Quantized:
@@ -196,7 +206,7 @@ def _rms(x, weight, residual, sum_out, out, eps, eight, stream):
     rs = ss = ys = qs = 0
     y = q8 = total = None
     if residual is not None:
-        rs = _rows(residual, "residual", x)
+        rs = _like(residual, "residual", x.shape, dt, dev)
     if eight:
         if out is None:
             q8 = _new_q8(stream, rows, cols, 0, dev)
@@ -208,9 +218,9 @@ def _rms(x, weight, residual, sum_out, out, eps, eight, stream):
     elif out is None:
         y, ys = _empty(stream, (rows, cols), dt, dev), cols
     else:
-        y, ys = out, _rows(out, "out", x)
+        y, ys = out, _like(out, "out", x.shape, dt, dev)
     if sum_out is not None:
-        total, ss = sum_out, _rows(sum_out, "sum_out", x)
+        total, ss = sum_out, _like(sum_out, "sum_out", x.shape, dt, dev)
     elif residual is not None:
         total, ss = _empty(stream, (rows, cols), dt, dev), cols
     rstd = _empty(stream, (rows,), torch.float32, dev)
@@ -241,6 +251,10 @@ def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, resid
     return RmsQuantized(*_rms(x, weight, residual, sum_out, out, eps, True, stream))
 
 
+def _bytes(ws: Optional[torch.Tensor]) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
 def rms_norm_backward_workspace_bytes(rows: int, cols: int, dtype: torch.dtype = torch.float32) -> int:
     return int(lib().sgc_rms_norm_backward_workspace(
         C.byref(NormOpts(rows, cols, _DTYPES[dtype], _DTYPES[torch.float32], 0.0, 0))))
@@ -254,28 +268,31 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: Optional[torch.
     the gradient that reaches the stream past the norm.  dweight (float32, e.g.
     a slice of a flat gradient) is written, or with accumulate added to.  dx
     may be dy, s or dsum."""
-    _no_graph(dy, s, weight, rstd, dsum, dx, dweight)
+    if torch.is_grad_enabled():
+        _no_graph(dy, s, weight, rstd, dsum, dx, dweight)
     ss = _rows(s, "s")
-    dys = _rows(dy, "dy", s)
-    rows, cols = s.shape
-    dev = s.device
+    shape, dt, dev = s.shape, s.dtype, s.device
+    rows, cols = shape
+    dys = _like(dy, "dy", shape, dt, dev)
     wdt = _affine(weight, None, s, cols, dev)
     _vec1(rstd, "rstd", rows, torch.float32, dev)
-    _vec1(dweight, "dweight", cols, torch.float32, dev)
-    dss = 0 if dsum is None else _rows(dsum, "dsum", s)
+    dss = 0 if dsum is None else _like(dsum, "dsum", shape, dt, dev)
     if accumulate and dweight is None:
         raise ValueError("accumulate needs dweight")
-    given = (dx, dweight)
-    if dx is None and want_dx:
-        dx = _empty(stream, (rows, cols), s.dtype, dev)
-    dxs = 0 if dx is None else _rows(dx, "dx", s)
+    given, dxs = (dx, dweight), cols
+    if dx is not None:
+        dxs = _like(dx, "dx", shape, dt, dev)
+    elif want_dx:
+        dx = _empty(stream, (rows, cols), dt, dev)
     if dweight is None:
         dweight = _empty(stream, (cols,), torch.float32, dev)
-    o = NormOpts(rows, cols, _DTYPES[s.dtype], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
+    else:
+        _vec1(dweight, "dweight", cols, torch.float32, dev)
+    o = NormOpts(rows, cols, _DTYPES[dt], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
     need = lib().sgc_rms_norm_backward_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "rms_norm", stream, "sgc_rms_norm_backward_workspace")
-    _run("sgc_rms_norm_backward", dev, stream, C.byref(o), _ptr(dy), dys, _ptr(s), ss, _ptr(weight), _ptr(rstd),
-         _ptr(dsum), dss, _ptr(dx), dxs, _ptr(dweight), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    _run("sgc_rms_norm_backward", dev, stream, C.byref(o), dy.data_ptr(), dys, s.data_ptr(), ss, _ptr(weight),
+         rstd.data_ptr(), _ptr(dsum), dss, _ptr(dx), dxs, dweight.data_ptr(), _ptr(ws), _bytes(ws))
     _written(*given)
     return RmsGrads(dx, dweight)
 
@@ -298,36 +315,42 @@ def norm_backward_q8_workspace_bytes(rows: int, cols: int, *, kind: int = NORM_R
 
 def _backward_q8(kind, dy, x, weight, bias, mean, rstd, dsum, dx, dweight, dbias, accumulate, want_dx, want_y, y, ws,
                  stream) -> NormQ8Grads:
-    _no_graph(dy, x.scale, weight, bias, mean, rstd, dsum, dx, dweight, dbias, y)
+    if torch.is_grad_enabled():
+        _no_graph(dy, x.scale, weight, bias, mean, rstd, dsum, dx, dweight, dbias, y)
     layer = kind == NORM_LAYER
     dys = _rows(dy, "dy")
-    rows, cols = dy.shape
-    dev = dy.device
+    shape, dt, dev = dy.shape, dy.dtype, dy.device
+    rows, cols = shape
     qs = _q8_like(x, "x", rows, cols, dev)
     wdt = _affine(weight, bias, dy, cols, dev)
-    for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (dweight, "dweight", cols),
-                       (dbias, "dbias", cols)):
-        _vec1(t, name, n, torch.float32, dev)
-    dss = 0 if dsum is None else _rows(dsum, "dsum", dy)
+    _vec1(mean, "mean", rows, torch.float32, dev)
+    _vec1(rstd, "rstd", rows, torch.float32, dev)
+    dss = 0 if dsum is None else _like(dsum, "dsum", shape, dt, dev)
     if accumulate and (dweight is None or (layer and dbias is None)):
         raise ValueError("accumulate needs dweight" + (" and dbias" if layer else ""))
-    given = (dx, dweight, dbias, y)
-    if dx is None and want_dx:
-        dx = _empty(stream, (rows, cols), dy.dtype, dev)
-    dxs = 0 if dx is None else _rows(dx, "dx", dy)
-    if y is None and want_y:
-        y = _empty(stream, (rows, cols), dy.dtype, dev)
-    ys = 0 if y is None else _rows(y, "y", dy)
+    given, dxs, ys = (dx, dweight, dbias, y), cols, cols
+    if dx is not None:
+        dxs = _like(dx, "dx", shape, dt, dev)
+    elif want_dx:
+        dx = _empty(stream, (rows, cols), dt, dev)
+    if y is not None:
+        ys = _like(y, "y", shape, dt, dev)
+    elif want_y:
+        y = _empty(stream, (rows, cols), dt, dev)
     if dweight is None:
         dweight = _empty(stream, (cols,), torch.float32, dev)
-    if dbias is None and layer:
+    else:
+        _vec1(dweight, "dweight", cols, torch.float32, dev)
+    if dbias is not None:
+        _vec1(dbias, "dbias", cols, torch.float32, dev)
+    elif layer:
         dbias = _empty(stream, (cols,), torch.float32, dev)
-    o = NormQ8Opts(rows, cols, _DTYPES[dy.dtype], wdt, x.group, kind, NORM_ADD_GRADS if accumulate else 0, 0)
+    o = NormQ8Opts(rows, cols, _DTYPES[dt], wdt, x.group, kind, NORM_ADD_GRADS if accumulate else 0, 0)
     need = lib().sgc_norm_backward_q8_workspace(C.byref(o))
     ws = _scratch(need, ws, dev, "norm_q8", stream, "sgc_norm_backward_q8_workspace")
-    _run("sgc_norm_backward_q8", dev, stream, C.byref(o), _ptr(dy), dys, _ptr(x.q), qs, _ptr(x.scale), _ptr(weight),
-         _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dsum), dss, _ptr(dx), dxs, _ptr(y), ys, _ptr(dweight), _ptr(dbias),
-         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    _run("sgc_norm_backward_q8", dev, stream, C.byref(o), dy.data_ptr(), dys, x.q.data_ptr(), qs, x.scale.data_ptr(),
+         _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dsum), dss, _ptr(dx), dxs, _ptr(y), ys,
+         dweight.data_ptr(), _ptr(dbias), _ptr(ws), _bytes(ws))
     _written(*given)
     return NormQ8Grads(dx, dweight, dbias, y)
 

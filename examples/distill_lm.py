@@ -14,7 +14,14 @@ worker:
 
 and the receiver adds the workers' messages into one dense update.
 
-    python examples/distill_lm.py [--vocab 98] [--width 512] [--steps 60]
+With --bits 8 the model is an RMS norm's, and what lies between the norm and
+the loss is in 8 bits: the teacher is a network of its own, whose normed rows
+and head are 8-bit integers (rms_norm_q8, int8_linear), and the student keeps
+its norm's input in 8 bits for the backward pass (quantize_q8,
+rms_norm_backward_q8), which gives the normed rows again for the head's
+gradient.
+
+    python examples/distill_lm.py [--vocab 98] [--width 512] [--steps 60] [--bits 8]
 """
 from __future__ import annotations
 
@@ -67,13 +74,55 @@ class Student:
         self.part(out, 0).zero_().index_add_(0, tokens, g.dx)
 
 
+@dataclass
+class Student8(Student):
+    """The student with an RMS norm, whose input is all that is kept of it: in 8 bits."""
+
+    def logits(self, tokens: torch.Tensor):
+        x = self.part(self.flat, 0)[tokens].bfloat16()
+        n = sgc.rms_norm(x, self.part(self.flat, 1))
+        return n.y @ self.part(self.flat, 3).bfloat16().t(), (sgc.quantize_q8(x, group=64), n.rstd)
+
+    def gradient(self, tokens: torch.Tensor, saved, dlogits: torch.Tensor, out: torch.Tensor) -> None:
+        kept, rstd = saved
+        dy = dlogits @ self.part(self.flat, 3).bfloat16()
+        g = sgc.rms_norm_backward_q8(dy, kept, self.part(self.flat, 1), rstd, dx=dy, dweight=self.part(out, 1),
+                                     want_y=True)
+        self.part(out, 2).zero_()  # an RMS norm has no bias
+        self.part(out, 3).copy_(dlogits.t() @ g.y)
+        self.part(out, 0).zero_().index_add_(0, tokens, g.dx.float())
+
+
+@dataclass
+class Teacher8:
+    """Embedding, RMS norm and head of a fixed network; it scores in 8-bit integers."""
+    embedding: torch.Tensor
+    weight: torch.Tensor
+    head: sgc.Quantized
+
+    @classmethod
+    def make(cls, vocab: int, width: int, gen: torch.Generator) -> "Teacher8":
+        normal = lambda *s: torch.empty(*s, device="cuda").normal_(0.0, 1.0, generator=gen)  # noqa: E731
+        return cls(normal(vocab, width).bfloat16(), 1.0 + 0.1 * normal(width),
+                   sgc.quantize_q8(normal(vocab, width) * (2.0 * width ** -0.5), group=0))
+
+    def logits(self, tokens: torch.Tensor) -> torch.Tensor:
+        return sgc.int8_linear(sgc.rms_norm_q8(self.embedding[tokens], self.weight).q8, self.head)
+
+
 def train(vocab: int = 98, width: int = 512, rows: int = 1024, steps: int = 60, workers: int = 4, top: int = 16,
-          keep_ppm: int = 50000, scale: float = 1.0, lr: float = 4.0, seed: int = 0, log=print):
+          keep_ppm: int = 50000, scale: float = 1.0, lr: float = 4.0, seed: int = 0, bits: int = 16,
+          log=print):
     """Teaches a student; its mean divergence before and after, and the bits sent per parameter and step."""
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
-    teacher = torch.empty(vocab, vocab, device="cuda").normal_(0.0, 2.0, generator=gen)  # next-token logits
-    student = Student.make(vocab, width, gen)
+    if bits == 8:
+        score = Teacher8.make(vocab, width, gen).logits
+        student = Student8.make(vocab, width, gen)
+    else:
+        teacher = torch.empty(vocab, vocab, device="cuda").normal_(0.0, 2.0, generator=gen)  # next-token logits
+        score = teacher.__getitem__
+        student = Student.make(vocab, width, gen)
     layout = student.layout
     residual = [torch.zeros(layout.n, device="cuda") for _ in range(workers)]
     grad = torch.empty(layout.n, device="cuda")
@@ -86,7 +135,7 @@ def train(vocab: int = 98, width: int = 512, rows: int = 1024, steps: int = 60, 
 
     def divergence() -> float:
         tokens = torch.arange(vocab, device="cuda")
-        t = sgc.token_logprobs(teacher, scale=scale, top=top)
+        t = sgc.token_logprobs(score(tokens), scale=scale, top=top)
         z, _ = student.logits(tokens)
         return float(sgc.distill(z, t.top_idx, t.top_logp, mode=sgc.DISTILL_TAIL, scale=scale).loss.mean())
 
@@ -95,7 +144,7 @@ def train(vocab: int = 98, width: int = 512, rows: int = 1024, steps: int = 60, 
         messages = []
         for w in range(workers):
             tokens = draw()
-            t = sgc.token_logprobs(teacher[tokens], scale=scale, top=top)
+            t = sgc.token_logprobs(score(tokens), scale=scale, top=top)
             z, saved = student.logits(tokens)
             d = sgc.distill(z, t.top_idx, t.top_logp, mode=sgc.DISTILL_TAIL, scale=scale, dloss=weight, dlogits=z)
             student.gradient(tokens, saved, d.dlogits, grad)
@@ -120,8 +169,10 @@ def main() -> None:
     p.add_argument("--workers", type=int, default=4)
     p.add_argument("--top", type=int, default=16)
     p.add_argument("--keep-ppm", type=int, default=50000)
+    p.add_argument("--bits", type=int, choices=(8, 16), default=16)
     a = p.parse_args()
-    first, last, bits = train(a.vocab, a.width, a.rows, a.steps, a.workers, a.top, a.keep_ppm)
+    first, last, bits = train(a.vocab, a.width, a.rows, a.steps, a.workers, a.top, a.keep_ppm,
+                              bits=a.bits)
     print(f"divergence from the teacher {first:.4f} -> {last:.4f}, {bits:.2f} bits sent per parameter and step")
 
 

@@ -199,6 +199,8 @@ def test_rms_edges():
         assert torch.isnan(q.q8.scale[2:5]).all() and q.q8.scale[6] == 0 and q.q8.scale[1] == 0
         zero = sgc.rms_norm(torch.zeros(2, cols, device="cuda"), eps=0.0)  # 0 * inf, as the formula
         assert torch.isnan(zero.y).all()
+        zero = sgc.rms_norm_q8(torch.zeros(2, cols, device="cuda"), eps=0.0)
+        assert not zero.q8.q.any() and not zero.q8.scale.any()
     row = torch.randn(1, 300, generator=gen(1))
     r = sgc.rms_norm(row.cuda().expand(50, 300), residual=row.cuda().expand(50, 300))
     equal_bits(r.sum, (row + row).expand(50, 300), "one row for all")
