@@ -24,7 +24,6 @@ struct Product {
 };
 
 typedef int Int4 __attribute__((ext_vector_type(4)));
-typedef int Int16 __attribute__((ext_vector_type(16)));
 // 16 bytes of a row, at any address.
 typedef int Bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
@@ -109,12 +108,12 @@ __device__ inline void into_shared(const int8_t* p, Int4* to)
 template <typename T, int TM, int TN, int WM, int WN, int STAGES, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m, int tiles_n)
 {
-    constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 32, PN = TN / WN / 32;
+    constexpr int kThreads = 64 * WM * WN, PM = TM / WM / 16, PN = TN / WN / 16;
     constexpr int CX = TM * 8 / kThreads, CW = TN * 8 / kThreads, kRows = kThreads / 8;
     // Each step's rows in an array of its own: the compiler then knows that rows on
     // their way into one are not what is read from another.  Later 32 tokens of
     // each wave's results, a row's pitch 16 bytes past its length.
-    constexpr int kPitch = PN * 32 * (int)sizeof(T) + 16, kOut = WM * WN / 4 * 2 * kPitch;
+    constexpr int kPitch = PN * 16 * (int)sizeof(T) + 16, kOut = WM * WN / 4 * 2 * kPitch;
     constexpr int kX = TM * 8 > kOut ? TM * 8 : kOut, kW = TN * 8 > kOut ? TN * 8 : kOut;
     __shared__ Int4 x0[kX], x1[kX], w0[kW], w1[kW];
     __shared__ Int4 x2[STAGES > 2 ? TM * 8 : 1], x3[STAGES > 2 ? TM * 8 : 1];
@@ -190,32 +189,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
 #pragma unroll
         for (int i = 0; i < CW; ++i) w[t + i * kThreads] = rw[i];
     };
-    Int16 acc[PN][PM];
+    // 16 x 16 results an instruction (32 x 32: 4096 x 4096 x 50000 834 us, with 16 754)
+    Int4 acc[PN][PM];
 #pragma unroll
     for (int i = 0; i < PN; ++i)
 #pragma unroll
-        for (int j = 0; j < PM; ++j)
+        for (int j = 0; j < PM; ++j) acc[i][j] = Int4{0, 0, 0, 0};
+    const int lr = lane & 15, quarter = lane >> 4;
+    const int ax = (wm * PM * 16 + lr) * 8, aw = (wn * PN * 16 + lr) * 8;
+    // A step is four phases: 64 bytes of the sum with one half of the channels, with
+    // the other, and the same for the other 64 bytes.
+    constexpr int kPhases = 4, kHalf = PN / 2;
+    Int4 fx[2][PM], fw[2][kHalf];
+    const auto read = [&](const Int4* x, const Int4* w, int ph) __attribute__((always_inline)) {
+        const int p = ((ph >> 1) * 4 + quarter) ^ (lr & 7);
+        if ((ph & 1) == 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-    const int lr = lane & 31, half = lane >> 5;
-    const int ax = (wm * PM * 32 + lr) * 8, aw = (wn * PN * 32 + lr) * 8;
-    Int4 fx[2][PM], fw[2][PN];
-    const auto read = [&](const Int4* x, const Int4* w, int kk) __attribute__((always_inline)) {
-        const int p = (kk * 2 + half) ^ (lr & 7);
+            for (int j = 0; j < PM; ++j) fx[ph >> 1][j] = x[ax + j * 128 + p];
+        }
 #pragma unroll
-        for (int j = 0; j < PM; ++j) fx[kk & 1][j] = x[ax + j * 256 + p];
-#pragma unroll
-        for (int i = 0; i < PN; ++i) fw[kk & 1][i] = w[aw + i * 256 + p];
+        for (int i = 0; i < kHalf; ++i) fw[ph & 1][i] = w[aw + ((ph & 1) * kHalf + i) * 128 + p];
     };
-    const auto multiply = [&](int kk) __attribute__((always_inline)) {
+    const auto multiply = [&](int ph) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < PN; ++i)
+        for (int i = 0; i < kHalf; ++i)
 #pragma unroll
-            for (int j = 0; j < PM; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][i], fx[kk & 1][j], acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_s_setprio(0);
+            for (int j = 0; j < PM; ++j) {
+                Int4& a = acc[(ph & 1) * kHalf + i][j];
+                a = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ph & 1][i], fx[ph >> 1][j], a, 0, 0, 0);
+            }
         __builtin_amdgcn_sched_barrier(0);
     };
     // Waits until this wave's part of step s lies in shared memory; of the later ones
@@ -248,16 +251,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     // read, and rows STAGES steps on take their place; the next step's lie ready.
     const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w) __attribute__((always_inline)) {
 #pragma unroll
-        for (int kk = 0; kk + 1 < kStep / 32; ++kk) {
-            read(x, w, kk + 1);
-            multiply(kk);
+        for (int ph = 0; ph + 1 < kPhases; ++ph) {
+            read(x, w, ph + 1);
+            multiply(ph);
         }
         arrived(s + 1, STAGES - 2);
         meet();
         put(x, w, s + STAGES);
         fetch(s + STAGES + 1);
         if (s + 1 < steps) read(next_x, next_w, 0);
-        multiply(kStep / 32 - 1);
+        multiply(kPhases - 1);
     };
     if (part) {
         put_end(x0, w0);
@@ -292,29 +295,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     // rows are written in long pieces
     constexpr int kPiece = 16 / (int)sizeof(T);
     char* mine = (char*)((wave & 2) ? (wave & 1) ? w1 : w0 : (wave & 1) ? x1 : x0) + (wave >> 2) * 32 * kPitch;
-    const int64_t on = n0 + wn * PN * 32;
+    const int64_t on = n0 + wn * PN * 16;
 #pragma unroll
-    for (int j = 0; j < PM; ++j) {
-        const int64_t rm = m0 + (wm * PM + j) * 32, r = rm + lr;
-        const float xscale = k.xscale[r < k.rows ? r : k.rows - 1];
+    for (int j = 0; j < PM / 2; ++j) {
+        const int64_t rm = m0 + (wm * PM + j * 2) * 16;
 #pragma unroll
-        for (int i = 0; i < PN; ++i)
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = rm + h * 16 + lr;
+            const float xscale = k.xscale[r < k.rows ? r : k.rows - 1];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const int c0 = i * 32 + e * 2 + half * 4;
-                const float4 ws = *(const float4*)&channels[0][wn * PN * 32 + c0];
-                const float4 bias = *(const float4*)&channels[1][wn * PN * 32 + c0];
+            for (int i = 0; i < PN; ++i) {
+                const int c0 = i * 16 + quarter * 4;
+                const float4 ws = *(const float4*)&channels[0][wn * PN * 16 + c0];
+                const float4 bias = *(const float4*)&channels[1][wn * PN * 16 + c0];
+                const Int4 a = acc[i][j * 2 + h];
                 Pack<T, 4> p;
-                p.v[0] = from_f<T>(product_out(acc[i][j][e], xscale, ws.x, bias.x));
-                p.v[1] = from_f<T>(product_out(acc[i][j][e + 1], xscale, ws.y, bias.y));
-                p.v[2] = from_f<T>(product_out(acc[i][j][e + 2], xscale, ws.z, bias.z));
-                p.v[3] = from_f<T>(product_out(acc[i][j][e + 3], xscale, ws.w, bias.w));
-                *(Pack<T, 4>*)(mine + lr * kPitch + c0 * (int)sizeof(T)) = p;
+                p.v[0] = from_f<T>(product_out(a.x, xscale, ws.x, bias.x));
+                p.v[1] = from_f<T>(product_out(a.y, xscale, ws.y, bias.y));
+                p.v[2] = from_f<T>(product_out(a.z, xscale, ws.z, bias.z));
+                p.v[3] = from_f<T>(product_out(a.w, xscale, ws.w, bias.w));
+                *(Pack<T, 4>*)(mine + (h * 16 + lr) * kPitch + c0 * (int)sizeof(T)) = p;
                 __builtin_amdgcn_sched_barrier(0);
             }
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        constexpr int kPieces = PN * 32 / kPiece, kAtOnce = 64 / kPieces;
+        constexpr int kPieces = PN * 16 / kPiece, kAtOnce = 64 / kPieces;
 #pragma unroll
         for (int a = 0; a < 32; a += kAtOnce) {
             const int rr = a + lane / kPieces, c0 = lane % kPieces * kPiece;
@@ -456,7 +462,7 @@ static int product(const Product& k, hipStream_t s)
     const auto cost = [&](int64_t tile, int64_t at_once, double round, double step) {
         return (double)cdiv(cdiv(k.rows, tile) * cdiv(k.out, tile), at_once) * (round + step * steps);
     };
-    const double c64 = cost(64, 512, 2.3, 0.35), c128 = cost(128, 512, 4.0, 1.0), c256 = cost(256, 256, 6.0, 1.9);
+    const double c64 = cost(64, 512, 2.3, 0.35), c128 = cost(128, 512, 4.0, 1.0), c256 = cost(256, 256, 6.0, 1.65);
     if (c64 <= c128 && c64 <= c256) return tiles_of<T, 64, 64, 2, 2, 4>(k, s);
     return c128 <= c256 ? tiles_of<T, 128, 128, 2, 2, 2>(k, s) : tiles_of<T, 256, 256, 4, 2, 2>(k, s);
 }

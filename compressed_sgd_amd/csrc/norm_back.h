@@ -132,13 +132,15 @@ __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int si
     float nm = 0.f, nr = 0.f;
     int64_t r = (int64_t)blockIdx.x * side + sub;
     const int64_t step = (int64_t)gridDim.x * side;
+    // at 16 elements a thread there are no registers for the next row's
+    constexpr bool kAhead = EPT < 16;
     const auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             nx[n] = x.template load<RAG>(at, n * across + t, cols, once);
             ny[n] = load_vec<T, RAG>((const T*)k.dy + at * k.dys, n * across + t, cols, once);
         }
-        if (k.dsum) {
+        if (kAhead && k.dsum) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
                 ns[n] = load_vec<T, RAG>((const T*)k.dsum + at * k.dss, n * across + t, cols, once);
@@ -146,21 +148,20 @@ __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int si
         if (LAYER) nm = k.mean[at];
         nr = k.rstd[at];
     };
-    constexpr bool kAhead = EPT < 16;
     if (kAhead && r < k.rows) fetch(r);
     int turn = 0;
     for (; r - sub < k.rows; r += step, turn ^= 1) {
         const bool live = r < k.rows;
         if (!kAhead && live) fetch(r);
         float h[EPT], g[EPT];
-        Raw ds[NV];
+        Raw ds[NV] = {};
         const float m = live && LAYER ? nm : 0.f, rs = live ? nr : 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             X::template values<RAG>(nx[n], n * across + t, cols, h + n * VL);
             settle<T, RAG>(ny[n], n * across + t, cols);
             unpack<T>(ny[n], g + n * VL);
-            ds[n] = ns[n];
+            if (kAhead) ds[n] = ns[n];
         }
         if (!live) {
 #pragma unroll
@@ -168,27 +169,31 @@ __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int si
         }
         if (kAhead && r + step < k.rows) fetch(r + step);
         float s1 = 0.f, s2 = 0.f;
-        float y[EPT];
 #pragma unroll
-        for (int i = 0; i < EPT; i += 4) {  // past cols dy is 0
-            const Four w = weights(i);
-            Four b = {0.f, 0.f, 0.f, 0.f};
-            if (LAYER && k.y) b = biases(i);
+        for (int n = 0; n < NV; ++n) {  // past cols dy is 0
+            float y[VL];
 #pragma unroll
-            for (int e = i; e < i + 4; ++e) {
-                h[e] = (LAYER ? h[e] - m : h[e]) * rs;
-                y[e] = LAYER ? fmaf(h[e], w[e - i], b[e - i]) : h[e] * w[e - i];
-                aw[e] = fmaf(g[e], h[e], aw[e]);
-                if (LAYER) ab[e] += g[e];
-                g[e] *= w[e - i];
-                if (LAYER) s1 += g[e];
-                s2 = fmaf(g[e], h[e], s2);
+            for (int i = n * VL; i < (n + 1) * VL; i += 4) {
+                const Four w = weights(i);
+                Four b = {0.f, 0.f, 0.f, 0.f};
+                if (LAYER && k.y) b = biases(i);
+#pragma unroll
+                for (int e = i; e < i + 4; ++e) {
+                    h[e] = (LAYER ? h[e] - m : h[e]) * rs;
+                    y[e - n * VL] = LAYER ? fmaf(h[e], w[e - i], b[e - i]) : h[e] * w[e - i];
+                    aw[e] = fmaf(g[e], h[e], aw[e]);
+                    if (LAYER) ab[e] += g[e];
+                    g[e] *= w[e - i];
+                    if (LAYER) s1 += g[e];
+                    s2 = fmaf(g[e], h[e], s2);
+                }
             }
+            if (k.y && live) store_vec<T, RAG>((T*)k.y + r * k.ys, n * across + t, cols, y, once);
         }
-        if (k.y && live) {
+        if (!kAhead && live && k.dsum) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                store_vec<T, RAG>((T*)k.y + r * k.ys, n * across + t, cols, y + n * VL, once);
+                ds[n] = load_vec<T, RAG>((const T*)k.dsum + r * k.dss, n * across + t, cols, once);
         }
         if (k.dx) {
             row_join<false, LANES>(s1, s2, tmp, turn, waves, sub);
