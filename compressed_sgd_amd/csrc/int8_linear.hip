@@ -351,8 +351,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
 {
     __shared__ Int4 part[kFewWaves][B][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int share = wave % split, per = kFewWaves / split;
-    const int64_t n0 = (row_of_block() * per + wave / split) * 16;
+    const int share = wave;
+    const int64_t n0 = row_of_block() * 16;
     const int lr = lane & 15, quarter = lane >> 4;
     Int4 acc[B];
 #pragma unroll
@@ -426,7 +426,7 @@ static int few(const Product& k, hipStream_t s)
     const int64_t units = cdiv(k.out, 16);
     int split = 1;
     while (split < kFewWaves && units * split < 256 * 8 && k.width > split * 64 * kFewDeep) split *= 2;
-    k_few<T, B><<<row_grid(cdiv(units, kFewWaves / split)), 64 * kFewWaves, 0, s>>>(k, split);
+    k_few<T, B><<<row_grid(units), 64 * split, 0, s>>>(k, split);
     SGC_LAUNCH_CHECK();
     return SGC_OK;
 }
