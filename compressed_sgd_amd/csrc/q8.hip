@@ -226,7 +226,9 @@ static int quantize(const sgc_q8_opts* o, const void* xv, int64_t xs, int8_t* q,
     constexpr int VL = VecLen<T>::value;
     const T* x = (const T*)xv;
     const int cols = (int)o->cols;
-    const bool once = o->rows * cols * (int64_t)(sizeof(T) + 1) >= kCacheBytes;
+    // what is kept in 8 bits is not read again: past the caches from half of them on
+    // (16384 x 4096 bf16, quantised and read back from cold inputs: 72.9 -> 67.8 us)
+    const bool once = o->rows * cols * (int64_t)(sizeof(T) + 1) >= kCacheBytes / 2;
     if (o->group) {
         const Line l = line_of(o, VL, o->group);
         const unsigned g = line_groups(l);
