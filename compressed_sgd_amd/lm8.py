@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -251,11 +252,9 @@ def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, resid
     return RmsQuantized(*_rms(x, weight, residual, sum_out, out, eps, True, stream))
 
 
-def _bytes(ws: Optional[torch.Tensor]) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
-
-
+@lru_cache(maxsize=1024)
 def rms_norm_backward_workspace_bytes(rows: int, cols: int, dtype: torch.dtype = torch.float32) -> int:
+    """Workspace bytes of one rms_norm_backward call; 0 for sizes that it refuses."""
     return int(lib().sgc_rms_norm_backward_workspace(
         C.byref(NormOpts(rows, cols, _DTYPES[dtype], _DTYPES[torch.float32], 0.0, 0))))
 
@@ -289,10 +288,12 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: Optional[torch.
     else:
         _vec1(dweight, "dweight", cols, torch.float32, dev)
     o = NormOpts(rows, cols, _DTYPES[dt], wdt, 0.0, NORM_ADD_GRADS if accumulate else 0)
-    need = lib().sgc_rms_norm_backward_workspace(C.byref(o))
+    need = rms_norm_backward_workspace_bytes(rows, cols, dt)
+    if ws is not None:
+        need = ws.numel() * ws.element_size()
     ws = _scratch(need, ws, dev, "rms_norm", stream, "sgc_rms_norm_backward_workspace")
     _run("sgc_rms_norm_backward", dev, stream, C.byref(o), dy.data_ptr(), dys, s.data_ptr(), ss, _ptr(weight),
-         rstd.data_ptr(), _ptr(dsum), dss, _ptr(dx), dxs, dweight.data_ptr(), _ptr(ws), _bytes(ws))
+         rstd.data_ptr(), _ptr(dsum), dss, _ptr(dx), dxs, dweight.data_ptr(), ws.data_ptr(), need)
     _written(*given)
     return RmsGrads(dx, dweight)
 
@@ -306,6 +307,7 @@ class NormQ8Grads:
     y: Optional[torch.Tensor]         # the norm's output from the 8 bits, where wanted
 
 
+@lru_cache(maxsize=1024)
 def norm_backward_q8_workspace_bytes(rows: int, cols: int, *, kind: int = NORM_RMS, group: int = 128,
                                      dtype: torch.dtype = torch.float32) -> int:
     """Workspace bytes of one rms_norm_backward_q8 (NORM_RMS) or layer_norm_backward_q8 (NORM_LAYER) call."""
@@ -346,11 +348,13 @@ def _backward_q8(kind, dy, x, weight, bias, mean, rstd, dsum, dx, dweight, dbias
     elif layer:
         dbias = _empty(stream, (cols,), torch.float32, dev)
     o = NormQ8Opts(rows, cols, _DTYPES[dt], wdt, x.group, kind, NORM_ADD_GRADS if accumulate else 0, 0)
-    need = lib().sgc_norm_backward_q8_workspace(C.byref(o))
+    need = norm_backward_q8_workspace_bytes(rows, cols, kind=kind, group=x.group, dtype=dt)
+    if ws is not None:
+        need = ws.numel() * ws.element_size()
     ws = _scratch(need, ws, dev, "norm_q8", stream, "sgc_norm_backward_q8_workspace")
     _run("sgc_norm_backward_q8", dev, stream, C.byref(o), dy.data_ptr(), dys, x.q.data_ptr(), qs, x.scale.data_ptr(),
          _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dsum), dss, _ptr(dx), dxs, _ptr(y), ys,
-         dweight.data_ptr(), _ptr(dbias), _ptr(ws), _bytes(ws))
+         dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), need)
     _written(*given)
     return NormQ8Grads(dx, dweight, dbias, y)
 

@@ -732,6 +732,91 @@ def test_large_norms(cols, dtype):
     close(k.dweight, dw8.cpu(), tol * mag8.cpu(), "dweight from 8 bits")
 
 
+def test_rows_past_32_bits():
+    """Rows more than 2^31 elements, and 2^32 bytes, apart."""
+    announce("rows past 32 bits")
+    rows, cols, step = 3, 1003, (1 << 31) + 72
+    g = gen(9)
+    x, dy = [torch.randn(rows, cols, generator=g).to(BF16) for _ in range(2)]
+    w = torch.randn(cols, generator=g)
+    far = [torch.empty((rows - 1) * step + cols, dtype=BF16, device="cuda").as_strided((rows, cols), (step, 1))
+           for _ in range(3)]
+    q = torch.empty((rows - 1) * 2 * step + cols, dtype=torch.int8, device="cuda").as_strided((rows, cols),
+                                                                                           (2 * step, 1))
+    xd, yd, dxd = far
+    xd.copy_(x)
+    r = sgc.rms_norm(xd, w.cuda(), out=yd)
+    (y, rstd), (ty, tr) = lm8_ref.rms(x, w, 1e-6)
+    close(r.y, y, ty, "y", BF16)
+    for group in (0, 64):
+        want, scale = lm8_ref.quantize(x, group)
+        c = sgc.quantize_q8(xd, group=group,
+                            out=sgc.Quantized(q, torch.empty(scale.shape, device="cuda"), group))
+        equal_bits(c.q, want, "q")
+        equal_bits(c.scale, scale, "scale")
+        equal_bits(sgc.dequantize_q8(c, BF16, out=yd), lm8_ref.values(want, scale, group).to(BF16), "values")
+        b = sgc.rms_norm_backward_q8(dy.cuda(), c, w.cuda(), r.rstd, dx=dxd, y=yd)
+        v = lm8_ref.values(want, scale, group)
+        (dx, dw, _), (tdx, tdw, _) = lm8_ref.backward(dy, v, w, None, r.rstd, None)
+        close(b.dx, dx, tdx, "dx from 8 bits", BF16)
+        close(b.dweight, dw, tdw, "dweight from 8 bits")
+    b = sgc.rms_norm_backward(dy.cuda(), xd, w.cuda(), r.rstd, dx=dxd)
+    (dx, dw, _), (tdx, tdw, _) = lm8_ref.backward(dy, x, w, None, r.rstd, None)
+    close(b.dx, dx, tdx, "dx", BF16)
+    close(b.dweight, dw, tdw, "dweight")
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams that run side by side, each with its own cached workspaces."""
+    announce("two streams at once")
+    t, u = step_tensors(300, 640, 1000), step_tensors(301, 640, 1000)
+    want = [all_calls(t), all_calls(u)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for k, (s, v) in enumerate(((a, t), (b, u))):
+            got.append((k, all_calls(v, stream=s)))
+    torch.cuda.synchronize()
+    for k, r in got:
+        same_bits(r, want[k], f"stream {k}")
+
+
+def test_binding_refuses_mismatches():
+    announce("mismatched calls are refused")
+    x = torch.zeros(4, 64, device="cuda", dtype=BF16)
+    w, v = torch.zeros(64, device="cuda"), torch.zeros(4, device="cuda")
+    c, k = sgc.quantize_q8(x, group=32), sgc.quantize_q8(x, group=0)
+    short = sgc.Quantized(k.q[:, :32], k.scale)
+    for f in (lambda: sgc.rms_norm(x, residual=x[:, :32]), lambda: sgc.rms_norm(x, residual=x.float()),
+              lambda: sgc.rms_norm(x, w[:32]), lambda: sgc.rms_norm(x, w.half()), lambda: sgc.rms_norm(x, out=x[:2]),
+              lambda: sgc.rms_norm(x.t()), lambda: sgc.rms_norm(x, sum_out=x.float()),
+              lambda: sgc.rms_norm_q8(x, out=c), lambda: sgc.rms_norm_q8(x, out=short),
+              lambda: sgc.rms_norm_backward(x, x[:, :32], None, v), lambda: sgc.rms_norm_backward(x, x, None, v[:3]),
+              lambda: sgc.rms_norm_backward(x, x, None, v, dsum=x.float()),
+              lambda: sgc.rms_norm_backward(x, x, None, v, accumulate=True),
+              lambda: sgc.rms_norm_backward(x, x, None, v, dweight=w[:32]),
+              lambda: sgc.quantize_q8(x, group=48), lambda: sgc.quantize_q8(x, group=64, out=c),
+              lambda: sgc.quantize_q8(x, group=0, out=short), lambda: sgc.dequantize_q8(c, torch.float64),
+              lambda: sgc.dequantize_q8(c, BF16, out=x[:2]),
+              lambda: sgc.dequantize_q8(sgc.Quantized(c.q, c.scale[:, :1], 32)),
+              lambda: sgc.dequantize_q8(sgc.Quantized(c.q, c.scale.double(), 32)),
+              lambda: sgc.rms_norm_backward_q8(x, short, None, v),
+              lambda: sgc.rms_norm_backward_q8(x, c, None, v, y=x[:2]),
+              lambda: sgc.layer_norm_backward_q8(x, c, w, w, v[:2], v),
+              lambda: sgc.layer_norm_backward_q8(x, c, w, w, v, v, dweight=w, accumulate=True),
+              lambda: sgc.int8_linear(k, short), lambda: sgc.int8_linear(k, k, w),
+              lambda: sgc.int8_linear(k, k, dtype=torch.int32), lambda: sgc.int8_linear(k, k, out=x),
+              lambda: sgc.int8_linear(sgc.Quantized(k.q.t(), k.scale), k),
+              lambda: sgc.int8_linear(sgc.Quantized(k.q, k.scale[:, 0]), k)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(sgc.SGCError):
+        sgc.rms_norm(x, out=x, sum_out=x)  # the same buffer for both
+    with pytest.raises(sgc.SGCError):
+        sgc.rms_norm_backward_q8(x, c, None, v, dx=(t := x.clone()), y=t)
+
+
 def test_more_rows_than_a_grid_line():
     rows, cols = (1 << 20) + 5, 9
     announce(f"{rows} rows of {cols}")
