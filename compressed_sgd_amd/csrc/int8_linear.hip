@@ -123,8 +123,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     constexpr int kPitch = PN * 16 * (int)sizeof(T) + 16, kOut = WM * WN / 4 * 2 * kPitch;
     constexpr int kX = TM * 8 > kOut ? TM * 8 : kOut, kW = TN * 8 > kOut ? TN * 8 : kOut;
     __shared__ Int4 x0[kX], x1[kX], w0[kW], w1[kW];
-    __shared__ Int4 x2[STAGES > 2 ? TM * 8 : 1], x3[STAGES > 2 ? TM * 8 : 1];
-    __shared__ Int4 w2[STAGES > 2 ? TN * 8 : 1], w3[STAGES > 2 ? TN * 8 : 1];
+    constexpr int kX4 = STAGES > 2 ? TM * 8 : 1, kW4 = STAGES > 2 ? TN * 8 : 1;
+    constexpr int kX8 = STAGES > 4 ? TM * 8 : 1, kW8 = STAGES > 4 ? TN * 8 : 1;
+    __shared__ Int4 x2[kX4], x3[kX4], w2[kW4], w3[kW4];
+    __shared__ Int4 x4[kX8], x5[kX8], x6[kX8], x7[kX8], w4[kW8], w5[kW8], w6[kW8], w7[kW8];
     __shared__ alignas(16) float channels[2][TN];  // their scales and biases
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
@@ -235,9 +237,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
             constexpr int kEach = CX + CW;
             static_assert((STAGES - 1) * kEach < 64, "");
             constexpr auto code = [](int n) constexpr { return 0x0f70 | (n & 15) | (n >> 4) << 14; };  // vmcnt(n)
-            if (STAGES == 4 && ahead == 3 && s + 3 < steps) __builtin_amdgcn_s_waitcnt(code(STAGES == 4 ? 3 * kEach : 0));
-            else if (STAGES == 4 && ahead == 2 && s + 2 < steps) __builtin_amdgcn_s_waitcnt(code(STAGES == 4 ? 2 * kEach : 0));
-            else if (STAGES == 2 && ahead == 1 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(code(kEach));
+            if (ahead == STAGES - 1 && s + ahead < steps) __builtin_amdgcn_s_waitcnt(code((STAGES - 1) * kEach));
+            else if (ahead == STAGES - 2 && s + ahead < steps) __builtin_amdgcn_s_waitcnt(code((STAGES - 2) * kEach));
             else __builtin_amdgcn_s_waitcnt(code(0));
         }
     };
@@ -253,21 +254,61 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
             asm volatile("" ::: "memory");
         }
     };
-    // The operands of the next products are read while one step's run.  One barrier a
-    // step, before its last products: what is read of this step's rows has been
-    // read, and rows STAGES steps on take their place; the next step's lie ready.
-    const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w) __attribute__((always_inline)) {
+    // Small tiles: a wave's few products do not cover its reads' way, so the whole next
+    // step's operands are read while one step's products run.
+    constexpr bool kWhole = PM * PN <= 4;
+    struct Operands {
+        Int4 x[kWhole ? 2 : 1][PM], w[kWhole ? 2 : 1][PN];
+    } even, odd;
+    const auto read_whole = [&](const Int4* x, const Int4* w, Operands& f) __attribute__((always_inline)) {
+        if constexpr (kWhole) {
 #pragma unroll
-        for (int ph = 0; ph + 1 < kPhases; ++ph) {
-            read(x, w, ph + 1);
-            multiply(ph);
+            for (int kk = 0; kk < 2; ++kk) {
+                const int p = (kk * 4 + quarter) ^ (lr & 7);
+#pragma unroll
+                for (int j = 0; j < PM; ++j) f.x[kk][j] = x[ax + j * 128 + p];
+#pragma unroll
+                for (int i = 0; i < PN; ++i) f.w[kk][i] = w[aw + i * 128 + p];
+            }
+        }
+    };
+    // The operands of the next products are read while one step's run.  One barrier a
+    // step, before its last products (or, whole steps at a time, all of them): what
+    // is read of this step's rows has been read, and rows STAGES steps on take their
+    // place; the next step's lie ready.
+    const auto step = [&](int s, Int4* x, Int4* w, const Int4* next_x, const Int4* next_w, Operands& now,
+                          Operands& next) __attribute__((always_inline)) {
+        if constexpr (!kWhole) {
+#pragma unroll
+            for (int ph = 0; ph + 1 < kPhases; ++ph) {
+                read(x, w, ph + 1);
+                multiply(ph);
+            }
         }
         arrived(s + 1, STAGES - 2);
         meet();
         put(x, w, s + STAGES);
         fetch(s + STAGES + 1);
-        if (s + 1 < steps) read(next_x, next_w, 0);
-        multiply(kPhases - 1);
+        if constexpr (kWhole) {
+            read_whole(next_x, next_w, next);  // past the last step what lies there, unused
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < PN; ++i)
+#pragma unroll
+                    for (int j = 0; j < PM; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(now.w[kk][i], now.x[kk][j], acc[i][j], 0, 0, 0);
+            // a read beside each product
+#pragma unroll
+            for (int i = 0; i < 2 * (PM + PN); ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            if (s + 1 < steps) read(next_x, next_w, 0);
+            multiply(kPhases - 1);
+        }
     };
     if (part) {
         put_end(x0, w0);
@@ -278,23 +319,37 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
     fetch(1);
     put(x1, w1, 1);
     fetch(2);
-    if constexpr (STAGES == 4) {
+    static_assert(STAGES == 2 || DIRECT, "");  // rows through registers are fetched one step ahead
+    if constexpr (STAGES > 2) {
         put(x2, w2, 2);
-        fetch(3);
         put(x3, w3, 3);
-        fetch(4);
+    }
+    if constexpr (STAGES > 4) {
+        put(x4, w4, 4);
+        put(x5, w5, 5);
+        put(x6, w6, 6);
+        put(x7, w7, 7);
     }
     arrived(0, STAGES - 1);
     meet();
-    read(x0, w0, 0);
+    if constexpr (kWhole) read_whole(x0, w0, even);
+    else read(x0, w0, 0);
     for (int s = 0; s < steps; s += STAGES) {
-        step(s, x0, w0, x1, w1);
+        step(s, x0, w0, x1, w1, even, odd);
         if constexpr (STAGES == 2) {
-            if (s + 1 < steps) step(s + 1, x1, w1, x0, w0);
+            if (s + 1 < steps) step(s + 1, x1, w1, x0, w0, odd, even);
         } else {
-            if (s + 1 < steps) step(s + 1, x1, w1, x2, w2);
-            if (s + 2 < steps) step(s + 2, x2, w2, x3, w3);
-            if (s + 3 < steps) step(s + 3, x3, w3, x0, w0);
+            if (s + 1 < steps) step(s + 1, x1, w1, x2, w2, odd, even);
+            if (s + 2 < steps) step(s + 2, x2, w2, x3, w3, even, odd);
+            if constexpr (STAGES == 4) {
+                if (s + 3 < steps) step(s + 3, x3, w3, x0, w0, odd, even);
+            } else {
+                if (s + 3 < steps) step(s + 3, x3, w3, x4, w4, odd, even);
+                if (s + 4 < steps) step(s + 4, x4, w4, x5, w5, even, odd);
+                if (s + 5 < steps) step(s + 5, x5, w5, x6, w6, odd, even);
+                if (s + 6 < steps) step(s + 6, x6, w6, x7, w7, even, odd);
+                if (s + 7 < steps) step(s + 7, x7, w7, x0, w0, odd, even);
+            }
         }
     }
     __syncthreads();
@@ -460,19 +515,26 @@ static int tiles_of(const Product& k, hipStream_t s)
 // tiles 11.8; 24 x 4096 x 16384 21.9, in tiles 15.8: every wave reads the
 // tokens' rows, where a tile reads them once), for one or two tokens always.
 // Else tiles of the size whose rounds over the chip take least, by what a round
-// takes there in microseconds, a part and a part a step (and about 2 more a
-// call): 2048 x 1024 x 10000 in tiles of 64, 128, 256: 53, 35, 44; 512 x 4096 x
-// 4096: 16, 23, 54; 1500 x 656 x 10000: 41, 25, 22; 800 x 2048 x 6000: 25, 22, 34.
+// takes there in microseconds, a part and a part a step, the latter less where
+// a compute unit has one tile (and about 2 more a call): 2048 x 1024 x 10000 in
+// tiles of 64, 128, 256: 53, 35, 44; 512 x 4096 x 4096: 15, 23, 54; 1500 x 656 x
+// 10000: 41, 25, 22; 800 x 2048 x 6000: 25, 21, 34; 1024 x 4096 x 4096: 31, 26, 54.
+// Tiles of 64 that have a compute unit each keep eight steps in shared memory, not
+// four (40 x 16384 x 4096: 37.7 -> 33.1 us, 28.6 with reads beside products).
 template <typename T>
 static int product(const Product& k, hipStream_t s)
 {
     if (k.rows <= 2 || (k.rows <= 32 && k.out <= 8192)) return k.rows <= 16 ? few<T, 1>(k, s) : few<T, 2>(k, s);
     const double steps = (double)cdiv(k.width, kStep);
-    const auto cost = [&](int64_t tile, int64_t at_once, double round, double step) {
-        return (double)cdiv(cdiv(k.rows, tile) * cdiv(k.out, tile), at_once) * (round + step * steps);
+    const auto count = [&](int64_t tile) { return cdiv(k.rows, tile) * cdiv(k.out, tile); };
+    const auto cost = [&](int64_t tile, int64_t at_once, double round, double alone, double step) {
+        const int64_t n = count(tile);
+        return n <= 256 ? round + alone * steps : (double)cdiv(n, at_once) * (round + step * steps);
     };
-    const double c64 = cost(64, 512, 2.3, 0.35), c128 = cost(128, 512, 4.0, 1.0), c256 = cost(256, 256, 6.0, 1.65);
-    if (c64 <= c128 && c64 <= c256) return tiles_of<T, 64, 64, 2, 2, 4>(k, s);
+    const double c64 = cost(64, 512, 2.3, 0.2, 0.33), c128 = cost(128, 512, 4.0, 0.65, 1.0),
+                 c256 = cost(256, 256, 6.0, 1.5, 1.65);
+    if (c64 <= c128 && c64 <= c256)
+        return count(64) <= 256 ? tiles_of<T, 64, 64, 2, 2, 8>(k, s) : tiles_of<T, 64, 64, 2, 2, 4>(k, s);
     return c128 <= c256 ? tiles_of<T, 128, 128, 2, 2, 2>(k, s) : tiles_of<T, 256, 256, 4, 2, 2>(k, s);
 }
 

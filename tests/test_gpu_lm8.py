@@ -475,6 +475,22 @@ def test_product_strides(rows, width, xo, xp, wo, wp):
     untouched(y, buf)
 
 
+@pytest.mark.parametrize("rows,width,out", [(3700, 130, 4001), (3600, 128, 4090), (3599, 17, 3841), (700, 1100, 6001),
+                                            (690, 1152, 6000), (1000, 650, 2001), (1001, 1024, 2048),
+                                            (130, 1500, 1031), (257, 4000, 129)], ids=str)
+@pytest.mark.parametrize("aligned", [True, False], ids=["aligned", "odd"])
+@DTYPES
+def test_product_of_every_tile(rows, width, out, aligned, dtype):
+    """Sizes that take the tiles of 256, 128 and 64 (in four and in eight steps), each with ragged edges."""
+    announce(f"product {rows}x{width}x{out} aligned {aligned} {dtype}")
+    xq, wq = whole(rows, width, 1), whole(out, width, 2)
+    up = -(-width // 16) * 16 + (0 if aligned else 3)
+    xd, wd = rows_like(xq, up, 0, 101)[0], rows_like(wq, up, 0 if aligned else 5, 103)[0]
+    y, buf = rows_like(torch.zeros(rows, out, dtype=dtype), out + 1, 1)
+    check_product(xq, wq, True, dtype, xd, wd, y)
+    untouched(y, buf)
+
+
 @pytest.mark.parametrize("rows,out", [(1, 40), (20, 40), (130, 200), (300, 300)], ids=str)
 def test_product_at_the_largest_sums(rows, out):
     """-128 times -128, 131071 times: 2^31 less 2^14."""
