@@ -80,6 +80,10 @@ struct Back {
     float* part;
     int64_t rows;
     int cols;
+    // where the sums over the rows go: by way of part and k_norm_join, or from one
+    // workgroup straight
+    float *dw, *db;
+    bool add;
 };
 
 template <typename T>
@@ -261,6 +265,16 @@ __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int si
             if (LAYER) ab[i] += sw[kSums - 1][i * across + t];
         }
     }
+    if (gridDim.x == 1) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int c = (i / VL * across + t) * VL + i % VL;
+            if (c >= cols) continue;
+            if (k.dw) k.dw[c] = k.add ? k.dw[c] + aw[i] : aw[i];
+            if (LAYER && k.db) k.db[c] = k.add ? k.db[c] + ab[i] : ab[i];
+        }
+        return;
+    }
     float* p = k.part + kSums * (int64_t)blockIdx.x * cols;
 #pragma unroll
     for (int n = 0; n < NV; ++n)
@@ -339,16 +353,17 @@ static void back_held(const X& x, const Back& k, const RowShape& sh, unsigned g,
             return;
         }
     }
-    if constexpr (LANES == 64) {
+    if constexpr (LANES == 64 && EPT >= 8) {
         if (rag) k_back<T, X, LAYER, LANES, EPT, true, 1024><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
         else k_back<T, X, LAYER, LANES, EPT, false, 1024><<<g, sh.threads(), 0, s>>>(x, k, sh.waves, sh.rows, once);
     }
 }
 
 template <typename T, typename X, bool LAYER>
-static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float* db, bool add, hipStream_t s)
+static int norm_back(const X& x, const Back& k, int32_t dtype, hipStream_t s)
 {
     const int64_t parts = back_parts(k.rows, k.cols, dtype);
+    const bool straight = k.cols <= kNormHeld && parts == 1;
     if (k.rows && k.cols > kNormHeld) {
         if (k.part) {  // before dx, which may take dy's or the input's place
             k_back_long_dw<T, X, LAYER><<<dim3((unsigned)cdiv(k.cols, 256), (unsigned)parts), 256, 0, s>>>(x, k);
@@ -372,10 +387,10 @@ static int norm_back(const X& x, const Back& k, int32_t dtype, float* dw, float*
         else back_held<T, X, LAYER, 64, 16>(x, k, sh, g, once, s);
         SGC_LAUNCH_CHECK();
     }
-    if (k.part) {
+    if (k.part && !straight) {
         const int64_t width = (LAYER ? 2 : 1) * (int64_t)k.cols;
         k_norm_join<<<(unsigned)cdiv(width, kJoinCols), kJoinCols * kJoinDeep, 0, s>>>(k.part, parts, width, k.cols,
-                                                                                        dw, db, add);
+                                                                                        k.dw, k.db, k.add);
         SGC_LAUNCH_CHECK();
     }
     return SGC_OK;

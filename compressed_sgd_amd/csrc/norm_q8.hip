@@ -14,12 +14,11 @@ static bool norm_q8_ok(const sgc_norm_q8_opts* o)
 
 template <typename T>
 static int norm_back_8(const sgc_norm_q8_opts* o, const int8_t* q, int64_t qs, const float* scale, const Back& k,
-                       float* dw, float* db, hipStream_t s)
+                       hipStream_t s)
 {
     const As8Bits<T> x = {q, qs, scale, q8_groups(o->cols, o->group), q8_shift(o->group)};
-    const bool add = o->flags & SGC_NORM_ADD_GRADS;
-    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits<T>, true>(x, k, o->dtype, dw, db, add, s)
-                                     : norm_back<T, As8Bits<T>, false>(x, k, o->dtype, dw, db, add, s);
+    return o->kind == SGC_NORM_LAYER ? norm_back<T, As8Bits<T>, true>(x, k, o->dtype, s)
+                                     : norm_back<T, As8Bits<T>, false>(x, k, o->dtype, s);
 }
 
 }  // namespace sgc
@@ -64,9 +63,10 @@ extern "C" int sgc_norm_backward_q8(const sgc_norm_q8_opts* o, const void* dy, i
         part = Carver(ws).take<float>(1);
     }
     const Back k = {dy, dy_stride, weight, bias,     o->wdtype == SGC_F32, mean,    rstd, dsum, dsum_stride,
-                    dx, dx_stride, y,      y_stride, part,                 o->rows, (int)o->cols};
+                    dx, dx_stride, y,      y_stride, part,                 o->rows, (int)o->cols,
+                    dweight, dbias, (o->flags & SGC_NORM_ADD_GRADS) != 0};
     const hipStream_t s = (hipStream_t)stream;
-    return o->dtype == SGC_F32    ? norm_back_8<float>(o, q, q_stride, scale, k, dweight, dbias, s)
-           : o->dtype == SGC_BF16 ? norm_back_8<bf16_t>(o, q, q_stride, scale, k, dweight, dbias, s)
-                                  : norm_back_8<f16_t>(o, q, q_stride, scale, k, dweight, dbias, s);
+    return o->dtype == SGC_F32    ? norm_back_8<float>(o, q, q_stride, scale, k, s)
+           : o->dtype == SGC_BF16 ? norm_back_8<bf16_t>(o, q, q_stride, scale, k, s)
+                                  : norm_back_8<f16_t>(o, q, q_stride, scale, k, s);
 }

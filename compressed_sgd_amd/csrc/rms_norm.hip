@@ -248,16 +248,15 @@ extern "C" int sgc_rms_norm_backward(const sgc_norm_opts* o, const void* dy, int
         part = Carver(ws).take<float>(1);
     }
     const Back k = {dy, dy_stride, weight,  nullptr, o->wdtype == SGC_F32, nullptr, rstd, dsum, dsum_stride,
-                    dx, dx_stride, nullptr, 0,       part,                 o->rows, (int)o->cols};
+                    dx, dx_stride, nullptr, 0,       part,                 o->rows, (int)o->cols,
+                    dweight, nullptr, (o->flags & SGC_NORM_ADD_GRADS) != 0};
     const hipStream_t s = (hipStream_t)stream;
-    const bool add = o->flags & SGC_NORM_ADD_GRADS;
     switch (o->dtype) {
     case SGC_F32:
-        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+        return norm_back<float, AsIs<float>, false>({(const float*)x, s_stride}, k, o->dtype, s);
     case SGC_BF16:
-        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add,
-                                                      s);
+        return norm_back<bf16_t, AsIs<bf16_t>, false>({(const bf16_t*)x, s_stride}, k, o->dtype, s);
     default:
-        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, o->dtype, dweight, nullptr, add, s);
+        return norm_back<f16_t, AsIs<f16_t>, false>({(const f16_t*)x, s_stride}, k, o->dtype, s);
     }
 }
