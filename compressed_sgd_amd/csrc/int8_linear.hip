@@ -89,10 +89,10 @@ __device__ inline void channel4(const Product& k, int64_t o, float* scale, float
 // both lie in all banks once.  Rows that begin at multiples of 16 bytes come
 // straight from memory (DIRECT), others through registers.
 //
-// 4096 x 4096 x 50000: 758 us, 2.21 PFLOP/s; 8192 cubed 423 us, 2.60 (2.8 with
-// operands of zeros: the clock follows the power that the values take).  What
-// that needs: 32 matrix instructions a wave for 24 reads of shared memory, all
-// of which are on their way while the products before them run.  256 x 256 by
+// 4096 x 4096 x 50000: 757 to 776 us, 2.16 to 2.21 PFLOP/s; 8192 cubed 423 us, 2.60;
+// the matrix units are 53% busy, and the clock follows the power that the values
+// take.  A step is 64 matrix instructions a wave for 24 reads of shared memory,
+// all of which are on their way while the products before them run.  256 x 256 by
 // eight waves of 64 x 128: four waves of 128 x 128 would read a third less, but
 // spill.  A round's beginning and end, 6 us of 60 here, are not overlapped.
 constexpr int kStep = 128;
