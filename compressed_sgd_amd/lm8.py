@@ -179,7 +179,7 @@ def dequantize_q8(x: Quantized, dtype: torch.dtype = torch.float32, *, out: Opti
 @dataclass
 class RmsNormalized:
     y: torch.Tensor
-    sum: torch.Tensor    # the residual stream after the addition; x where there is none
+    sum: torch.Tensor    # the residual stream after the addition; x where there is none (a copy where y is in x)
     rstd: torch.Tensor   # float32 [rows]
 
 
@@ -222,7 +222,8 @@ def _rms(x, weight, residual, sum_out, out, eps, eight, stream):
         y, ys = out, _like(out, "out", x.shape, dt, dev)
     if sum_out is not None:
         total, ss = sum_out, _like(sum_out, "sum_out", x.shape, dt, dev)
-    elif residual is not None:
+    elif residual is not None or (y is not None and y.data_ptr() == x.data_ptr()):
+        # without a residual the stream is x, unless y takes its place
         total, ss = _empty(stream, (rows, cols), dt, dev), cols
     rstd = _empty(stream, (rows,), torch.float32, dev)
     o = NormOpts(rows, cols, _DTYPES[dt], wdt, eps, 0)
@@ -241,7 +242,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual
              stream=None) -> RmsNormalized:
     """RMS norm of every row of x + residual [rows, cols]; the sum, rounded to
     x's type, is given too.  out and sum_out may be x or residual, not the
-    same one."""
+    same one.  Where out is x and there is no residual, x as it was is copied
+    into sum."""
     return RmsNormalized(*_rms(x, weight, residual, sum_out, out, eps, False, stream))
 
 

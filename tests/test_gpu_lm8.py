@@ -167,6 +167,61 @@ def test_rms_in_place_and_added(cols):
     assert got.dx is None and torch.equal(flat, was + one.dweight)
 
 
+@DTYPES
+@pytest.mark.parametrize("cols", [96, 130, 1000, 1031, 4096, 16384, 20000])
+def test_the_stream_of_a_norm_in_place(cols, dtype):
+    """y in x's place without a residual: the result's sum is what x was, as the backward pass needs it."""
+    rows = 21
+    g = gen(cols + 1)
+    x, dy = [torch.randn(rows, cols, generator=g).to(dtype) for _ in range(2)]
+    w = torch.randn(cols, generator=g).cuda()
+    announce(f"the stream of a norm in place, {rows}x{cols} {dtype}")
+    apart = sgc.rms_norm(x.cuda(), w)
+    for pad, offset in ((0, 0), (3, 1)):
+        t, buf = rows_like(x, cols + pad, offset)
+        got = sgc.rms_norm(t, w, out=t)
+        assert got.y is t
+        same_bits([got.y, got.rstd], [apart.y, apart.rstd], "y and rstd")
+        equal_bits(got.sum, x, "sum")
+        untouched(t, buf)
+        b = sgc.rms_norm_backward(dy.cuda(), got.sum, w, got.rstd)
+        (dx, dw, _), (tdx, tdw, _) = lm8_ref.backward(dy, x, w, None, got.rstd, None)
+        close(b.dx, dx, tdx, "dx", dtype)
+        close(b.dweight, dw, tdw, "dweight")
+    # a place for it given: there, x's own among them, which y may not take then
+    t, s = x.cuda(), torch.empty(rows, cols, dtype=dtype, device="cuda")
+    got = sgc.rms_norm(t, w, out=t, sum_out=s)
+    assert got.sum is s
+    equal_bits(s, x, "sum_out")
+    t = x.cuda()
+    got = sgc.rms_norm(t, w, sum_out=t)
+    assert got.sum is t
+    equal_bits(t, x, "the sum in x")
+    same_bits([got.y], [apart.y], "y beside it")
+    # apart, nothing is copied
+    t = x.cuda()
+    assert sgc.rms_norm(t, w).sum is t and sgc.rms_norm(t, w, out=s).sum is t and sgc.rms_norm_q8(t, w).sum is t
+
+
+def test_the_stream_of_a_norm_in_place_captured():
+    announce("the stream of a norm in place, captured")
+    x = torch.randn(9, 1000, generator=gen(4)).to(BF16)
+    u = x.cuda()
+    sgc.rms_norm(u, out=u)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = sgc.rms_norm(u, out=u)
+    for it in range(3):
+        now = x * (1 + it)
+        u.copy_(now)
+        want = sgc.rms_norm(now.cuda())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        same_bits([r.y, r.sum, r.rstd], [want.y, now.cuda(), want.rstd], f"replay {it}")
+
+
 def test_rms_edges():
     announce("rms edges")
     e = torch.empty(0, 10, device="cuda")
