@@ -136,7 +136,7 @@ def _new_q8(stream, rows: int, cols: int, group: int, device) -> Quantized:
 def quantize_q8(x: torch.Tensor, *, group: int = 128, out: Optional[Quantized] = None, stream=None) -> Quantized:
     """Rows of x in 8 bits, a scale every `group` elements (32, 64, 128, 256), or one a row (0): activations kept
     for the backward pass; weights, which int8_linear reads (group 0)."""
-    _no_graph(x)
+    _no_graph(x, None if out is None else out.scale)
     xs = _rows(x, "x")
     rows, cols = x.shape
     dev = x.device
@@ -199,7 +199,7 @@ class RmsGrads:
 def _rms(x, weight, residual, sum_out, out, eps, eight, stream):
     """Either kind of output: y (out a tensor), or with `eight` Quantized; the sum, rstd."""
     if torch.is_grad_enabled():
-        _no_graph(x, weight, residual, sum_out, None if eight else out)
+        _no_graph(x, weight, residual, sum_out, out.scale if eight and out is not None else out)
     xs = _rows(x, "x")
     rows, cols = x.shape
     dev, dt = x.device, x.dtype

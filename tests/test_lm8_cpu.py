@@ -232,3 +232,16 @@ def test_a_tensor_that_requires_grad_is_refused(name):
         grad_calls()[name]()
     with torch.no_grad(), pytest.raises(ValueError, match="device"):
         grad_calls()[name]()
+
+
+@pytest.mark.parametrize("name", ["quantize_q8", "quantize_q8 in groups", "rms_norm_q8"])
+def test_a_scale_to_be_written_that_requires_grad_is_refused(name):
+    x, q = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.int8)
+    row, groups = torch.zeros(4, 1, requires_grad=True), torch.zeros(4, 2, requires_grad=True)
+    f = {"quantize_q8": lambda: sgc.quantize_q8(x, group=0, out=sgc.Quantized(q, row)),
+         "quantize_q8 in groups": lambda: sgc.quantize_q8(x, group=32, out=sgc.Quantized(q, groups, 32)),
+         "rms_norm_q8": lambda: sgc.rms_norm_q8(x, out=sgc.Quantized(q, row))}[name]
+    with pytest.raises(ValueError, match="no graph"):
+        f()
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):
+        f()
