@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(Rms k)
         const T t = sum ? sum[c] : res ? from_f<T>(to_f(x[c]) + to_f(res[c])) : x[c];
         const float w = weight_at<T>(k.w, k.w32, c, 1.f), f = to_f(t);
         if (k.q) k.q[r * k.qs + c] = (int8_t)(quantized(f * w, u) & u.keep);
-        if (k.y) ((T*)k.y)[r * k.ys + c] = from_f<T>(f * rs * w);
+        else ((T*)k.y)[r * k.ys + c] = from_f<T>(f * rs * w);
     }
 }
 

@@ -501,12 +501,13 @@ int sgc_distill_backward(const sgc_distill_opts* opt, const void* logits, int64_
  *   rstd = (sum(s^2) / cols + eps)^(-1/2);  y = s * rstd * weight
  * sum receives s, y the normed rows, q and qscale [rows] the normed rows in 8
  * bits, with p = s * weight and a = max |p| over the row, each fp32:
- *   q = rint(p * r), r = 127 / a;  qscale = (a / 127) * rstd;
- * q * qscale stands for y.  rstd is left out of q: it cancels, so q does not
- * depend on how the squares were summed.  A row with a = 0 has q = 0 and
- * qscale 0, one with a p that is not finite q = 0 and qscale NaN.  Squares whose
- * sum passes fp32's range leave rstd 0, as the formula does.  Either of y and
- * q may be NULL, not both; sum, qscale (only without q), rstd [rows fp32] and
+ *   q = rint(p * r), r = 127 / a;  qscale = (a / 127) * rstd
+ * (a < 2^-100: as in sgc_quantize_q8); q * qscale stands for y.  rstd is left
+ * out of q: it cancels, so q does not depend on how the squares were summed.
+ * A row with a = 0 has q = 0 and qscale 0, one with a p that is not finite q = 0
+ * and qscale NaN.  Squares whose sum passes fp32's range leave rstd 0, as the
+ * formula does.  A call writes y or q, one of the two (the other NULL), and
+ * qscale with q alone; both at once are refused.  sum, rstd [rows fp32] and
  * weight (NULL: 1) may be NULL.  sum and y may be x or residual, not the same
  * one, at the same address and stride; no other overlap.  Options as for the
  * layer norm; flags 0.
