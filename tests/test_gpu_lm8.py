@@ -10,7 +10,7 @@ import compressed_sgd_amd as sgc
 import lm8_ref
 import lm_ref
 from gpu_util import announce
-from lm_ref import close
+from lm_ref import close, dbl
 
 pytestmark = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
@@ -220,6 +220,30 @@ def test_the_stream_of_a_norm_in_place_captured():
         graph.replay()
         torch.cuda.synchronize()
         same_bits([r.y, r.sum, r.rstd], [want.y, now.cuda(), want.rstd], f"replay {it}")
+
+
+@DTYPES
+@pytest.mark.parametrize("cols", [96, 650, 1031, 4096, 20000])
+def test_rms_q8_with_the_sum_in_place(cols, dtype):
+    """The sum in x's and in the residual's place beside 8 bits; the other one stays as it was."""
+    rows = 41
+    g = gen(cols + 2)
+    x, res = [torch.randn(rows, cols, generator=g).to(dtype) for _ in range(2)]
+    w = torch.randn(cols, generator=g).cuda()
+    announce(f"8 bits, the sum in place, {rows}x{cols} {dtype}")
+    q = sgc.rms_norm_q8(x.cuda(), w, residual=res.cuda())
+    for at in ("x", "res"):
+        for pad, offset in ((0, 0), (3, 1)):
+            t, buf = {}, {}
+            for k, a in (("x", x), ("res", res)):
+                t[k], buf[k] = rows_like(a, cols + pad, offset)
+            got = sgc.rms_norm_q8(t["x"], w, residual=t["res"], sum_out=t[at])
+            assert got.sum is t[at]
+            same_bits([got.q8.q, got.q8.scale, got.sum, got.rstd], [q.q8.q, q.q8.scale, q.sum, q.rstd], f"sum in {at}")
+            other = "res" if at == "x" else "x"
+            equal_bits(t[other], x if other == "x" else res, f"{other} beside the sum in {at}")
+            for k in t:
+                untouched(t[k], buf[k])
 
 
 def test_rms_edges():
@@ -451,6 +475,57 @@ def test_norm_backward_from_8_bits_wants(kind, cols):
     none = sgc.Quantized(c.q[:0], c.scale[:0], 128)
     r = backward_q8(kind, dy[:0], none, w, b, None if mean is None else mean[:0], rstd[:0], want_y=True)
     assert r.dx.shape == (0, cols) and r.y.shape == (0, cols) and not r.dweight.any()
+
+
+@pytest.mark.parametrize("cols", [100, 650, 4099, 9000, 20000])
+def test_layer_norm_from_8_bits_with_a_weight_or_a_bias_alone(cols):
+    """The one that is not given counts as 1 or 0, in the gradients and in y."""
+    rows, group = 19, 128
+    g = gen(cols + 3)
+    announce(f"layer norm from 8 bits, weight or bias alone, {cols} columns")
+    for dtype in (F32, BF16):
+        q, scale = lm8_ref.quantize(stream_rows(rows, cols, dtype, g), group)
+        v = lm8_ref.values(q, scale, group)
+        mean, rstd = stats_of(v, "layer")
+        dy = torch.randn(rows, cols, generator=g).to(dtype)
+        p = torch.randn(cols, generator=g)
+        for pt in (F32, dtype):
+            for w, b in ((p.to(pt), None), (None, p.to(pt))):
+                cuda = lambda t: None if t is None else t.cuda()
+                r = sgc.layer_norm_backward_q8(dy.cuda(), sgc.Quantized(q.cuda(), scale.cuda(), group), cuda(w),
+                                               cuda(b), mean.cuda(), rstd.cuda(), want_y=True)
+                (dx, dw, db), (tdx, tdw, tdb) = lm8_ref.backward(dy, v, w, mean, rstd, None)
+                close(r.dx, dx, tdx, "dx", dtype)
+                close(r.dweight, dw, tdw, "dweight")
+                close(r.dbias, db, tdb, "dbias")
+                y, ty = lm8_ref.normed(v, w, b, mean, rstd)
+                close(r.y, y, ty, "y", dtype)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("cols", [100, 650, 4096, 20000])
+def test_a_broken_group_stays_in_its_row_and_columns(cols, kind):
+    """A group whose scale is NaN: its row's dx, its columns' dweight and its own y are NaN, all else as without it."""
+    rows, group, at = 25, 32, 7
+    g = gen(cols + 4)
+    announce(f"{kind} backward from 8 bits, a broken group, {cols} columns")
+    x = stream_rows(rows, cols, BF16, g)
+    q, scale = lm8_ref.quantize(x, group)
+    mean, rstd = [None if t is None else t.cuda() for t in stats_of(lm8_ref.values(q, scale, group), kind)]
+    dy, w = torch.randn(rows, cols, generator=g).to(BF16).cuda(), torch.randn(cols, generator=g).cuda()
+    call = lambda s: backward_q8(kind, dy, sgc.Quantized(q.cuda(), s.cuda(), group), w,
+                                 w.flip(0).contiguous() if kind == "layer" else None, mean, rstd, want_y=True)
+    one = call(scale)
+    broken = scale.clone()
+    broken[at, 1] = NAN
+    r = call(broken)
+    rest = [k for k in range(rows) if k != at]
+    outside = torch.ones(cols, dtype=torch.bool)
+    outside[group:2 * group] = False
+    same_bits([r.dx[rest], r.y[rest], r.y[at][outside], r.dweight[outside], r.dbias],
+              [one.dx[rest], one.y[rest], one.y[at][outside], one.dweight[outside], one.dbias], "beside the group")
+    for t in (r.dx[at], r.y[at][~outside], r.dweight[~outside]):
+        assert torch.isnan(t).all()
 
 
 def test_checkpoint_gradient_against_differences():
@@ -907,3 +982,45 @@ def test_more_rows_than_a_grid_line():
     c = sgc.quantize_q8(x[pick.cuda()], group=0)
     ref, tol = lm8_ref.product(c.q, c.scale, w.q, w.scale, None)
     close(y[pick], ref, tol, "product")
+
+
+@DTYPES
+def test_the_longest_rows(dtype):
+    """2^20 columns: the norm, 8 bits in groups and a scale a row, and the backward passes from them."""
+    rows, cols = 2, 1 << 20
+    announce(f"the longest rows {dtype}")
+    g = gen(6)
+    x, dy = [torch.randn(rows, cols, generator=g).to(dtype) for _ in range(2)]
+    w, b = torch.randn(cols, generator=g), torch.randn(cols, generator=g)
+    xd, dyd, wd = x.cuda(), dy.cuda(), w.cuda()
+    r = sgc.rms_norm(xd, wd)
+    (y, rstd), (ty, tr) = lm8_ref.rms(x, w, 1e-6)
+    close(r.y, y, ty, "y", dtype)
+    close(r.rstd, rstd, tr, "rstd")
+    equal_bits(sgc.rms_norm_q8(xd, wd).q8.q, lm8_ref.rms_q8(x, w, 1e-6)[0], "q")
+    d = sgc.rms_norm_backward(dyd, xd, wd, r.rstd)
+    (dx, dw, _), (tdx, tdw, _) = lm8_ref.backward(dy, x, w, None, r.rstd, None)
+    close(d.dx, dx, tdx, "dx", dtype)
+    close(d.dweight, dw, tdw, "dweight")
+    for group in (0, 32, 256):
+        c = sgc.quantize_q8(xd, group=group)
+        q, scale = lm8_ref.quantize(x, group)
+        equal_bits(c.q, q, "q")
+        equal_bits(c.scale, scale, "scale")
+        v = lm8_ref.values(q, scale, group)
+        equal_bits(sgc.dequantize_q8(c, dtype), v.to(dtype), "values")
+        mean, rstd = stats_of(v, "layer")
+        k = sgc.layer_norm_backward_q8(dyd, c, wd, b.cuda(), mean.cuda(), rstd.cuda(), want_y=True)
+        (dx, dw, db), (tdx, tdw, tdb) = lm8_ref.backward(dy, v, w, mean, rstd, None)
+        # the two means over a row are sums of depth(cols) additions
+        h = (dbl(v) - dbl(mean)[:, None]) * dbl(rstd)[:, None]
+        p = (dbl(dy) * dbl(w)).abs()
+        tdx = tdx + lm8_ref.depth(cols) * lm_ref.U * dbl(rstd)[:, None] * (
+            p.mean(1, keepdim=True) + h.abs() * (p * h.abs()).mean(1, keepdim=True))
+        close(k.dx, dx, tdx, "dx from 8 bits", dtype)
+        close(k.dweight, dw, tdw, "dweight from 8 bits")
+        close(k.dbias, db, tdb, "dbias from 8 bits")
+        y, ty = lm8_ref.normed(v, w, b, mean, rstd)
+        close(k.y, y, ty, "y from 8 bits", dtype)
+    with pytest.raises(sgc.SGCError):
+        sgc.rms_norm(torch.empty(1, cols + 1, dtype=dtype, device="cuda"))
