@@ -95,6 +95,9 @@ __device__ inline void channel4(const Product& k, int64_t o, float* scale, float
 // all of which are on their way while the products before them run.  256 x 256 by
 // eight waves of 64 x 128: four waves of 128 x 128 would read a third less, but
 // spill.  A round's beginning and end, 6 us of 60 here, are not overlapped.
+// With rows through registers 256 x 256 spill (88 bytes a lane, 104 with fp32
+// results): 4096 x 4096 x 50000 with rows 4099 bytes apart 1967 us, 1500 x 650 x
+// 10000 fp32 45 (26 straight), 512 x 4096 x 4096 27 (15).
 constexpr int kStep = 128;
 constexpr int kBand = 8, kChips = 8;
 // Workgroups go to the chips in turn; each chip takes consecutive tiles.
@@ -406,8 +409,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(Product k, int tiles_m
 // ------------------------------------------------------------- few tokens
 // A workgroup takes 16 channels x 16 B tokens, each wave a share of the sum,
 // straight from memory into the matrix instruction; the waves join their sums in
-// shared memory.  Bound by memory: 1 x 1024 x 50000 11.2 us (4.6 TB/s), 2 x 4096 x
-// 50000 34 us a pass (6.1 TB/s).  Fetching a trip ahead takes twice the registers
+// shared memory.  Bound by memory: 1 x 1024 x 50000 10.6 us a pass (4.9 TB/s; rows
+// 1027 bytes apart 21), 2 x 4096 x 50000 34 us (6.1 TB/s).  Fetching a trip ahead takes twice the registers
 // and gains nothing.
 constexpr int kFewWaves = 8, kFewDeep = 8;
 template <typename T, int B>
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Product k, int split)
 }
 
 // The sum is split until eight waves a compute unit have work or each has one
-// trip's loads (32 x 4096 x 4096: 10 us).
+// trip's loads (32 x 4096 x 4096: 9.1 us a pass, 10.0 traced).
 template <typename T, int B>
 static int few(const Product& k, hipStream_t s)
 {
@@ -511,9 +514,14 @@ static int tiles_of(const Product& k, hipStream_t s)
     return direct ? tiles<T, TM, TN, WM, WN, STAGES, true>(k, s) : tiles<T, TM, TN, WM, WN, 2, false>(k, s);
 }
 
-// Few tokens: straight from memory up to 8192 channels (32 x 4096 x 4096 9.0 us, in
-// tiles 11.8; 24 x 4096 x 16384 21.9, in tiles 15.8: every wave reads the
-// tokens' rows, where a tile reads them once), for one or two tokens always.
+// Few tokens: straight from memory up to 8192 channels (past that most of what is
+// read are the tokens' rows: every workgroup reads them, a tile once), for one or two
+// tokens always.  bf16, straight and in tiles, us a pass: 32 x 4096 x 4096 9.1 and
+// 10.0, 32 x 14336 x 4096 22.5 and 25.7, 3 x 14336 x 4096 13 and 25; 24 x 4096 x 16384
+// 22 and 14.3, 32 x 14336 x 16384 92 and 47.  The bound looks neither at the number of
+// tokens nor at the width: 32 x 4096 x 8192 14.2 and 10.5, 32 x 14336 x 8192 49 and 40,
+// 3 x 14336 x 16384 43.2 and 45.4 lie on its other side; at a width of 1024 both take
+// 8.3.
 // Else tiles of the size whose rounds over the chip take least, by what a round
 // takes there in microseconds, a part and a part a step, the latter less where
 // a compute unit has one tile (and about 2 more a call): 2048 x 1024 x 10000 in

@@ -237,8 +237,15 @@ struct RowShape {
     int lanes, ept, waves, rows;
     int threads() const { return lanes < 64 ? 512 : 64 * waves * rows; }
 };
-// Workgroups that share out the rows: as many as run at once with `waves` on a
-// compute unit, the same number on each.
+// Workgroups that share out the rows: `waves` waves a compute unit to the nearest
+// whole workgroup, the same number on each.  That may be one more than a kernel's
+// registers leave room for, which then runs after the others; which number is best
+// differs.  As here, and rounded down (forward from 28 waves where rows are ragged,
+// what their registers allow in 16 bits): forward 10922 x 6144 bf16 92.5 and 91.6
+// us, 16384 x 4099 140 and 144, 46153 x 1300 105 and 106, into 8 bits 16384 x 4099
+// 131 and 111, 46153 x 1300 93 and 96; backward 10922 x 6144 91 and 91, 16384 x 4099
+// 137 and 132, 46153 x 1300 114 and 90, 13000 x 5120 fp32 182 and 175, layer norm
+// from 8 bits 16384 x 4099 bf16 175 and 171.
 inline int64_t row_groups(const RowShape& sh, int64_t rows, int waves)
 {
     const int each = (waves * 64 + sh.threads() / 2) / sh.threads();

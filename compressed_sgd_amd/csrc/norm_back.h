@@ -101,8 +101,9 @@ __device__ inline float weight_at(const void* w, bool w32, int c, float none)
 // registers each.  Where a row has more than 8 waves a layer norm's bias, and at 16
 // elements a thread the weights, lie in shared memory, each thread's own, and are
 // read again in every row (volatile: else they move back into registers); even so
-// rows of 16 elements a thread spill (4000 x 16384 from 8 bits: RMS norm bf16 102
-// us, layer norm bf16 156, fp32 396).
+// a layer norm's rows of 16 elements a thread spill, and an RMS norm's in fp32 or
+// where they are ragged (4000 x 16384 from 8 bits: RMS norm bf16 102 us, layer norm
+// bf16 156, fp32 396).
 typedef float Four __attribute__((ext_vector_type(4)));
 template <typename T, typename X, bool LAYER, int LANES, int EPT, bool RAG, int MOST>
 __global__ __launch_bounds__(MOST, 4) void k_back(X x, Back k, int waves, int side,

@@ -30,8 +30,9 @@ struct Rms {
 // way; the weights stay in registers across a workgroup's rows.  E8: 8 bits out;
 // the largest magnitude comes with the sum of squares, through the same barrier.
 // Bound by memory: 16384 x 4096 bf16 with the residual 94 us, 5.7 TB/s; 10007 x
-// 1024 fp16 into 8 bits 15 us; 8 x 1024 3.2 us.  Ragged rows (16384 x 4099 bf16:
-// 136 us) start at any 2 bytes and have a wave for their last vectors.
+// 1024 fp16 into 8 bits 15 us; 8 x 1024 3.2 us.  Ragged rows start at any 2 bytes
+// (16384 x 4094 bf16: 109 us); one whose last vector takes a wave of its own has
+// nine where eight would do (16384 x 4099: 140).
 template <typename T, int LANES, int EPT, bool RAG, bool E8>
 __global__ __launch_bounds__(LANES < 64 ? 512 : 1024) void k_rms(Rms k, int waves, int side, bool once)
 {
